@@ -325,6 +325,110 @@ fa_status fa_paged_gather(const void* k_cache, const void* v_cache, const int* b
                           int num_splits, void* stream);
 
 /*
+ * The e4m3 paged cache — half the bytes of the bf16 one.
+ *
+ *   k_cache, v_cache  e4m3 codes [num_pages][Hkv][page_size][d]
+ *   k_scale, v_scale  one byte per row, [num_pages][Hkv][page_size]: the row
+ *                     (a token of a kv head) stands for code * 2^(byte - 127)
+ * The exponent byte - 127 of a written row is the smallest integer >= -127
+ * with max|x| <= 448 * 2^(byte - 127) over the row's finite values (448 is
+ * e4m3's largest value; a row of zeros gets byte 0), each code is x *
+ * 2^-(byte - 127) rounded to nearest, ties to even; inf and NaN become e4m3's
+ * NaN.  Caches written by other means may use any byte from 0 to 254.
+ * Caches and scales are 16-byte aligned.
+ * Supported: d in {64, 128}, page_size == 16; num_pages*Hkv*16 and rows*Hkv
+ * below 2^31, max_blocks_per_seq below 2^27.
+ * The block table, seq_lens and (where taken) cu_seqlens are as for
+ * fa_paged_prefill: sequence s owns rows [cu_seqlens[s], cu_seqlens[s+1]) of
+ * the packed tensors, and those n_s rows are the last n_s of its seq_lens[s]
+ * tokens.  So one cu_seqlens writes a step's new tokens, then attends from them.
+ */
+
+/*
+ * fa_paged_kv_write_e4m3 — quantise new K and V rows into the paged cache.
+ * The pages have no counterpart for this call: "S12 FlashAttention", 生产实践,
+ * names FP8 only as a later feature.
+ *   k, v         bf16 rows [total][Hkv][d]; k_stride and v_stride are the
+ *                elements from one token to the next (multiples of 8, at least
+ *                Hkv*d; the heads of a token are dense), so K and V may be
+ *                parts of one projection's output
+ * Row cu_seqlens[s] + i is written to the slot of token seq_lens[s] - n_s + i.
+ * Other slots, and the slots of rows no sequence owns, keep their contents.
+ * Two rows of one call that name the same slot leave an unspecified mix there.
+ * A sequence whose offsets leave the rows, with n_s > seq_lens[s] or with
+ * seq_lens[s] outside [0, max_blocks_per_seq*page_size] is skipped and sets
+ * FA_ERR_INVALID_ARG; a token whose page id is out of range is skipped and
+ * sets FA_ERR_BAD_BLOCK_TABLE.
+ */
+fa_status fa_paged_kv_write_e4m3(const void* k, const void* v, void* k_cache, void* v_cache,
+                                 void* k_scale, void* v_scale, const int* block_table,
+                                 const int* seq_lens, const int* cu_seqlens, int num_seqs,
+                                 int total, int Hkv, int d, long long k_stride, long long v_stride,
+                                 int page_size, int num_pages, int max_blocks_per_seq,
+                                 void* stream);
+
+/*
+ * fa_paged_kv_read_e4m3 — read cached rows back as bf16, the inverse of
+ * fa_paged_kv_write_e4m3 (same arguments, same rows, same device status).
+ *   k, v         bf16 [total][Hkv][d] written: code * 2^(byte - 127), rounded
+ *                to bf16 (exact for every value in bf16's normal range).  Rows
+ *                of skipped tokens are not written.
+ */
+fa_status fa_paged_kv_read_e4m3(const void* k_cache, const void* v_cache, const void* k_scale,
+                                const void* v_scale, const int* block_table, const int* seq_lens,
+                                const int* cu_seqlens, void* k, void* v, int num_seqs, int total,
+                                int Hkv, int d, int page_size, int num_pages,
+                                int max_blocks_per_seq, void* stream);
+
+/*
+ * fa_paged_decode_e4m3 — one query token per sequence against the e4m3 paged
+ * cache, grouped heads, split over the warps of thread-block clusters and
+ * merged there: one launch, no workspace.
+ * Passage: as fa_paged_decode ("S12 FlashAttention", 实现, 组合, 它还解锁了什么
+ * and 练习 1).
+ *   q       bf16 [num_seqs][H][d]
+ *   o       bf16 [num_seqs][H][d] written
+ *   lse     fp32 [num_seqs][H]    written (may be NULL)
+ *   window  0: every key; w > 0: the query (the last of its L keys) sees the
+ *           last w keys, itself among them, and the first `sinks` keys
+ *   sinks   keys from the start that stay visible under a window (ignored
+ *           without one)
+ * Only pages that hold a visible key are looked up in the block table: ids of
+ * the others may be anything.  Cache contents of keys no query sees are never
+ * used, NaN included.  Device status as fa_paged_decode (bad page ids are
+ * skipped; a bad seq_lens[s] is treated as an empty sequence).
+ * K, V and the softmax weights enter the tensor cores in f16 (codes exactly,
+ * weights rounded to 11 bits), accumulation is fp32.
+ * Supported: H / Hkv <= 32; num_seqs*H below 2^28.
+ */
+fa_status fa_paged_decode_e4m3(const void* q, const void* k_cache, const void* v_cache,
+                               const void* k_scale, const void* v_scale, const int* block_table,
+                               const int* seq_lens, void* o, float* lse, int num_seqs, int H,
+                               int Hkv, int d, int page_size, int num_pages,
+                               int max_blocks_per_seq, float scale, int window, int sinks,
+                               void* stream);
+
+/*
+ * fa_paged_prefill_e4m3 — several new query tokens per sequence against the
+ * e4m3 paged cache (chunked prefill, draft tokens).
+ * Passage: as fa_paged_prefill.
+ *   q, cu_seqlens_q, max_seqlen_q, o, lse, causal   as fa_paged_prefill
+ *   window, sinks  as fa_paged_decode_e4m3, for each query from its own
+ *                  position p: keys j <= p with j > p - window or j < sinks;
+ *                  a window needs causal = 1
+ * A sequence with bad offsets, more than max_seqlen_q queries or a bad
+ * seq_lens[s] is skipped (its rows are not written) and sets
+ * FA_ERR_INVALID_ARG.
+ * Supported: H / Hkv <= 32; num_seqs*max_seqlen_q*H below 2^28.
+ */
+fa_status fa_paged_prefill_e4m3(const void* q, const void* k_cache, const void* v_cache,
+                                const void* k_scale, const void* v_scale, const int* block_table,
+                                const int* seq_lens, const int* cu_seqlens_q, void* o, float* lse,
+                                int num_seqs, int total_q, int max_seqlen_q, int H, int Hkv, int d,
+                                int page_size, int num_pages, int max_blocks_per_seq, float scale,
+                                int causal, int window, int sinks, void* stream);
+
+/*
  * fa_split_combine — merge per-split partial triples with the recurrence's
  * rescale rule ("S12 FlashAttention", 练习 1): for each (s, h)
  *     M = max_x m_x,  w_x = exp(m_x - M)  (w_x = 0 when m_x = -inf),

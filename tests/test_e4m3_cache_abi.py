@@ -1,0 +1,89 @@
+"""Refusals of the e4m3 paged cache's entries, on the CPU: nothing is launched."""
+import pytest
+
+from tiled_online_softmax_sm_gb300 import binding as fb
+from tiled_online_softmax_sm_gb300 import build as fbuild
+
+
+@pytest.fixture(scope="module")
+def lib():
+    fbuild.build()
+    return fb.load()
+
+
+CACHE = dict(kc=16, vc=16, ks=16, vs=16, bt=16, sl=16, S=4, Hkv=8, d=128, page=16, P=100, maxb=8)
+
+
+def _write(lib, **kw):
+    a = dict(CACHE, k=16, v=16, cu=16, T=10, kst=1024, vst=1024)
+    a.update(kw)
+    return lib.fa_paged_kv_write_e4m3(a["k"], a["v"], a["kc"], a["vc"], a["ks"], a["vs"], a["bt"],
+                                      a["sl"], a["cu"], a["S"], a["T"], a["Hkv"], a["d"], a["kst"],
+                                      a["vst"], a["page"], a["P"], a["maxb"], None)
+
+
+def _read(lib, **kw):
+    a = dict(CACHE, k=16, v=16, cu=16, T=10)
+    a.update(kw)
+    return lib.fa_paged_kv_read_e4m3(a["kc"], a["vc"], a["ks"], a["vs"], a["bt"], a["sl"], a["cu"],
+                                     a["k"], a["v"], a["S"], a["T"], a["Hkv"], a["d"], a["page"],
+                                     a["P"], a["maxb"], None)
+
+
+def _decode(lib, **kw):
+    a = dict(CACHE, q=16, o=16, lse=16, H=32, scale=0.1, win=0, sinks=0)
+    a.update(kw)
+    return lib.fa_paged_decode_e4m3(a["q"], a["kc"], a["vc"], a["ks"], a["vs"], a["bt"], a["sl"],
+                                    a["o"], a["lse"], a["S"], a["H"], a["Hkv"], a["d"], a["page"],
+                                    a["P"], a["maxb"], a["scale"], a["win"], a["sinks"], None)
+
+
+def _prefill(lib, **kw):
+    a = dict(CACHE, q=16, o=16, lse=16, cu=16, T=10, mq=4, H=32, scale=0.1, causal=1, win=0, sinks=0)
+    a.update(kw)
+    return lib.fa_paged_prefill_e4m3(a["q"], a["kc"], a["vc"], a["ks"], a["vs"], a["bt"], a["sl"],
+                                     a["cu"], a["o"], a["lse"], a["S"], a["T"], a["mq"], a["H"],
+                                     a["Hkv"], a["d"], a["page"], a["P"], a["maxb"], a["scale"],
+                                     a["causal"], a["win"], a["sinks"], None)
+
+
+@pytest.mark.parametrize("call", [_write, _read, _decode, _prefill])
+def test_cache_refusals(lib, call):
+    for kw in (dict(S=-1), dict(P=-1), dict(maxb=-1), dict(Hkv=0), dict(Hkv=-8), dict(kc=None),
+               dict(vc=None), dict(ks=None), dict(vs=None), dict(bt=None), dict(sl=None), dict(P=0),
+               dict(maxb=0), dict(kc=24), dict(vc=8), dict(ks=4), dict(vs=17), dict(bt=18),
+               dict(sl=17)):
+        assert call(lib, **kw) == fb.FA_ERR_INVALID_ARG, kw
+    for kw in (dict(d=96), dict(d=256), dict(page=32), dict(P=1 << 24), dict(maxb=1 << 27)):
+        assert call(lib, **kw) == fb.FA_ERR_UNSUPPORTED, kw
+    assert call(lib, S=0) == fb.FA_OK
+
+
+@pytest.mark.parametrize("call", [_write, _read])
+def test_row_refusals(lib, call):
+    for kw in (dict(k=None), dict(v=None), dict(k=24), dict(v=8), dict(cu=None), dict(cu=18),
+               dict(T=-1)):
+        assert call(lib, **kw) == fb.FA_ERR_INVALID_ARG, kw
+    assert call(lib, T=1 << 28) == fb.FA_ERR_UNSUPPORTED
+    assert call(lib, T=0) == fb.FA_OK
+    if call is _write:
+        for kw in (dict(kst=1016), dict(vst=0), dict(kst=-1024), dict(vst=1028)):
+            assert call(lib, **kw) == fb.FA_ERR_INVALID_ARG, kw
+
+
+@pytest.mark.parametrize("call", [_decode, _prefill])
+def test_attention_refusals(lib, call):
+    for kw in (dict(q=None), dict(o=None), dict(q=8), dict(o=24), dict(lse=2), dict(H=30),
+               dict(H=0), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
+               dict(scale=float("inf")), dict(win=-1), dict(sinks=-1)):
+        assert call(lib, **kw) == fb.FA_ERR_INVALID_ARG, kw
+    assert call(lib, H=8 * 33) == fb.FA_ERR_UNSUPPORTED       # group of 33
+    assert call(lib, S=1 << 24, T=1 << 24) == fb.FA_ERR_UNSUPPORTED
+
+
+def test_prefill_refusals(lib):
+    for kw in (dict(cu=None), dict(cu=18), dict(T=-1), dict(mq=-1), dict(causal=2),
+               dict(causal=0, win=5)):
+        assert _prefill(lib, **kw) == fb.FA_ERR_INVALID_ARG, kw
+    assert _prefill(lib, T=0) == fb.FA_OK
+    assert _prefill(lib, mq=0) == fb.FA_OK

@@ -8,8 +8,9 @@ raises FaError with the library's message.  There is no fallback: if the
 library is missing or cannot be loaded, the first call raises.
 
 The helpers at the end (``forward``, ``forward_f32``, ``forward_varlen``,
-``paged_decode``, ``paged_decode_fused``, ``split_combine``) allocate outputs
-with torch and then call the same entry points.
+``paged_decode``, ``paged_decode_fused``, the e4m3 cache's ``paged_..._e4m3``,
+``split_combine``) allocate outputs with torch and then call the same entry
+points.
 """
 from __future__ import annotations
 
@@ -34,6 +35,8 @@ FA_ERR_DEBUG_CHECK = 7
 EXPORTED = ("fa_forward", "fa_forward_fp8", "fa_forward_f32", "fa_forward_varlen", "fa_paged_prefill",
             "fa_paged_decode_workspace_size",
             "fa_paged_decode", "fa_paged_decode_fused", "fa_paged_decode_noalloc", "fa_paged_gather", "fa_split_combine",
+            "fa_paged_kv_write_e4m3", "fa_paged_kv_read_e4m3", "fa_paged_decode_e4m3",
+            "fa_paged_prefill_e4m3",
             "fa_last_error",
             "fa_get_device_status")
 FA_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -72,6 +75,11 @@ def load(path: str = LIB_PATH):
         lib.fa_paged_decode_noalloc.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, P]
         lib.fa_paged_gather.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, P]
         lib.fa_split_combine.argtypes = [P, P, P, P, P, I, I, I, I, P]
+        LL = ctypes.c_longlong
+        lib.fa_paged_kv_write_e4m3.argtypes = [P] * 9 + [I, I, I, I, LL, LL, I, I, I, P]
+        lib.fa_paged_kv_read_e4m3.argtypes = [P] * 9 + [I, I, I, I, I, I, I, P]
+        lib.fa_paged_decode_e4m3.argtypes = [P] * 9 + [I, I, I, I, I, I, I, F, I, I, P]
+        lib.fa_paged_prefill_e4m3.argtypes = [P] * 10 + [I, I, I, I, I, I, I, I, I, F, I, I, I, P]
         lib.fa_last_error.argtypes = []
         lib.fa_last_error.restype = ctypes.c_char_p
         lib.fa_get_device_status.argtypes = [P, ctypes.POINTER(I)]
@@ -79,7 +87,8 @@ def load(path: str = LIB_PATH):
                      "fa_paged_prefill",
                      "fa_paged_decode", "fa_paged_decode_fused",
                      "fa_paged_decode_noalloc", "fa_paged_gather", "fa_split_combine",
-                     "fa_get_device_status"):
+                     "fa_paged_kv_write_e4m3", "fa_paged_kv_read_e4m3", "fa_paged_decode_e4m3",
+                     "fa_paged_prefill_e4m3", "fa_get_device_status"):
             getattr(lib, name).restype = I
         _lib = lib
         return lib
@@ -185,6 +194,45 @@ def fa_paged_gather(k_cache, v_cache, block_table, seq_lens, k_out, v_out, num_s
     _check(load().fa_paged_gather(_p(k_cache), _p(v_cache), _p(block_table), _p(seq_lens),
                                   _p(k_out), _p(v_out), num_seqs, Hkv, d, page_size, num_pages,
                                   max_blocks_per_seq, num_splits, _stream(stream)))
+
+
+def fa_paged_kv_write_e4m3(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                           cu_seqlens, num_seqs, total, Hkv, d, k_stride, v_stride, page_size,
+                           num_pages, max_blocks_per_seq, stream=None):
+    _check(load().fa_paged_kv_write_e4m3(_p(k), _p(v), _p(k_cache), _p(v_cache), _p(k_scale),
+                                         _p(v_scale), _p(block_table), _p(seq_lens),
+                                         _p(cu_seqlens), num_seqs, total, Hkv, d, k_stride,
+                                         v_stride, page_size, num_pages, max_blocks_per_seq,
+                                         _stream(stream)))
+
+
+def fa_paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens,
+                          k, v, num_seqs, total, Hkv, d, page_size, num_pages,
+                          max_blocks_per_seq, stream=None):
+    _check(load().fa_paged_kv_read_e4m3(_p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale),
+                                        _p(block_table), _p(seq_lens), _p(cu_seqlens), _p(k),
+                                        _p(v), num_seqs, total, Hkv, d, page_size, num_pages,
+                                        max_blocks_per_seq, _stream(stream)))
+
+
+def fa_paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse,
+                         num_seqs, H, Hkv, d, page_size, num_pages, max_blocks_per_seq, scale,
+                         window=0, sinks=0, stream=None):
+    _check(load().fa_paged_decode_e4m3(_p(q), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale),
+                                       _p(block_table), _p(seq_lens), _p(o), _p(lse), num_seqs, H,
+                                       Hkv, d, page_size, num_pages, max_blocks_per_seq,
+                                       float(scale), int(window), int(sinks), _stream(stream)))
+
+
+def fa_paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                          cu_seqlens_q, o, lse, num_seqs, total_q, max_seqlen_q, H, Hkv, d,
+                          page_size, num_pages, max_blocks_per_seq, scale, causal=True, window=0,
+                          sinks=0, stream=None):
+    _check(load().fa_paged_prefill_e4m3(_p(q), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale),
+                                        _p(block_table), _p(seq_lens), _p(cu_seqlens_q), _p(o),
+                                        _p(lse), num_seqs, total_q, max_seqlen_q, H, Hkv, d,
+                                        page_size, num_pages, max_blocks_per_seq, float(scale),
+                                        int(causal), int(window), int(sinks), _stream(stream)))
 
 
 def fa_split_combine(part_m, part_l, part_o, o, lse, num_seqs, H, num_splits, dv, stream=None):
@@ -297,6 +345,108 @@ def paged_decode_fused(q, k_cache, v_cache, block_table, seq_lens, num_splits, s
     fa_paged_decode_fused(q, k_cache, v_cache, block_table, seq_lens, o, lse, S, H, Hkv, d, dv,
                           page, P, block_table.shape[1], num_splits, scale, workspace,
                           workspace.numel(), stream)
+    return o, lse
+
+
+def _tensors(fn, like, **named):
+    """Refuse tensors the C entry could not tell apart from good ones: another
+    device than `like`, another type, or (contiguous ones) a gap in memory.
+    Each argument is (tensor, bytes per element or dtype, shape or None)."""
+    import torch
+    if not like.is_cuda or like.device.index != torch.cuda.current_device():
+        raise FaError(FA_ERR_INVALID_ARG, f"{fn}: the tensors are on {like.device}, the current "
+                                          f"device is cuda:{torch.cuda.current_device()}")
+    for name, (t, kind, shape) in named.items():
+        if t.device != like.device:
+            raise FaError(FA_ERR_INVALID_ARG, f"{fn}: {name} is on {t.device}, not {like.device}")
+        if (t.element_size() != 1 or t.dtype is torch.bool) if kind == 1 else t.dtype is not kind:
+            raise FaError(FA_ERR_INVALID_ARG, f"{fn}: {name} has type {t.dtype}")
+        if shape is not None and (tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+            raise FaError(FA_ERR_INVALID_ARG, f"{fn}: {name} has shape {tuple(t.shape)} and strides "
+                                              f"{t.stride()}, wanted contiguous {tuple(shape)}")
+
+
+def _e4m3_cache(fn, like, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens):
+    """Checks of the paged e4m3 cache's tensors -> (pages, Hkv, page, d, sequences, max_blocks)."""
+    import torch
+    P, Hkv, page, d = k_cache.shape
+    S, max_blocks = block_table.shape
+    _tensors(fn, like, k_cache=(k_cache, 1, (P, Hkv, page, d)), v_cache=(v_cache, 1, (P, Hkv, page, d)),
+             k_scale=(k_scale, 1, (P, Hkv, page)), v_scale=(v_scale, 1, (P, Hkv, page)),
+             block_table=(block_table, torch.int32, (S, max_blocks)),
+             seq_lens=(seq_lens, torch.int32, (S,)))
+    return P, Hkv, page, d, S, max_blocks
+
+
+def paged_kv_write_e4m3(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                        cu_seqlens, stream=None):
+    """Quantise new rows k, v [T,Hkv,d] bf16 (token strides may be larger than Hkv*d) into the
+    cache [P,Hkv,16,d] (float8_e4m3fn or any 1-byte type) and its scale bytes [P,Hkv,16]."""
+    import torch
+    fn = "paged_kv_write_e4m3"
+    P, Hkv, page, d, S, max_blocks = _e4m3_cache(fn, k, k_cache, v_cache, k_scale, v_scale,
+                                                 block_table, seq_lens)
+    _tensors(fn, k, k=(k, torch.bfloat16, None), v=(v, torch.bfloat16, None),
+             cu_seqlens=(cu_seqlens, torch.int32, (S + 1,)))
+    T = k.shape[0]
+    strides = []
+    for name, t in (("k", k), ("v", v)):
+        if tuple(t.shape) != (T, Hkv, d) or t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != d):
+            raise FaError(FA_ERR_INVALID_ARG, f"{fn}: {name} has shape {tuple(t.shape)} and "
+                                              f"strides {t.stride()}, wanted {(T, Hkv, d)} with "
+                                              f"dense heads")
+        strides.append(t.stride(0) if T > 1 else max(t.stride(0), Hkv * d) // 8 * 8)
+    fa_paged_kv_write_e4m3(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                           cu_seqlens, S, T, Hkv, d, strides[0], strides[1], page, P, max_blocks,
+                           stream)
+
+
+def paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens,
+                       total, stream=None):
+    """The last n_s cached rows of every sequence -> (k, v) [total,Hkv,d] bf16."""
+    import torch
+    fn = "paged_kv_read_e4m3"
+    P, Hkv, page, d, S, max_blocks = _e4m3_cache(fn, k_cache, k_cache, v_cache, k_scale, v_scale,
+                                                 block_table, seq_lens)
+    _tensors(fn, k_cache, cu_seqlens=(cu_seqlens, torch.int32, (S + 1,)))
+    k = torch.empty((total, Hkv, d), dtype=torch.bfloat16, device=k_cache.device)
+    v = torch.empty((total, Hkv, d), dtype=torch.bfloat16, device=k_cache.device)
+    fa_paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, k,
+                          v, S, total, Hkv, d, page, P, max_blocks, stream)
+    return k, v
+
+
+def paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale,
+                      window=0, sinks=0, stream=None):
+    """q [S,H,d]; e4m3 cache [P,Hkv,16,d] with scale bytes [P,Hkv,16] -> (o [S,H,d], lse [S,H])."""
+    import torch
+    fn = "paged_decode_e4m3"
+    P, Hkv, page, d, S, max_blocks = _e4m3_cache(fn, q, k_cache, v_cache, k_scale, v_scale,
+                                                 block_table, seq_lens)
+    H = q.shape[1]
+    _tensors(fn, q, q=(q, torch.bfloat16, (S, H, d)))
+    o = torch.empty((S, H, d), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((S, H), dtype=torch.float32, device=q.device)
+    fa_paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse, S,
+                         H, Hkv, d, page, P, max_blocks, scale, window, sinks, stream)
+    return o, lse
+
+
+def paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens_q,
+                       max_seqlen_q, scale, causal=True, window=0, sinks=0, stream=None):
+    """q [Tq,H,d] packed by cu_seqlens_q over the e4m3 cache -> (o [Tq,H,d], lse [H,Tq])."""
+    import torch
+    fn = "paged_prefill_e4m3"
+    P, Hkv, page, d, S, max_blocks = _e4m3_cache(fn, q, k_cache, v_cache, k_scale, v_scale,
+                                                 block_table, seq_lens)
+    Tq, H = q.shape[:2]
+    _tensors(fn, q, q=(q, torch.bfloat16, (Tq, H, d)),
+             cu_seqlens_q=(cu_seqlens_q, torch.int32, (S + 1,)))
+    o = torch.empty((Tq, H, d), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
+    fa_paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                          cu_seqlens_q, o, lse, S, Tq, max_seqlen_q, H, Hkv, d, page, P,
+                          max_blocks, scale, causal, window, sinks, stream)
     return o, lse
 
 

@@ -427,6 +427,180 @@ fa_status fa_paged_gather(const void* k_cache, const void* v_cache, const int* b
   return FA_OK;
 }
 
+}  // extern "C"
+
+namespace {
+
+// Checks shared by the entries of the e4m3 paged cache.  `cu` may be null
+// where the entry takes one token per sequence (need_cu false).
+fa_status check_cache(const char* fn, const void* k_cache, const void* v_cache, const void* k_scale,
+                      const void* v_scale, const int* block_table, const int* seq_lens,
+                      const int* cu, bool need_cu, int num_seqs, int total, int Hkv, int d,
+                      int page_size, int num_pages, int max_blocks_per_seq, bool* nothing) {
+  *nothing = false;
+  if (num_seqs < 0 || total < 0 || num_pages < 0 || max_blocks_per_seq < 0)
+    return fail(FA_ERR_INVALID_ARG, "%s: negative size", fn);
+  if (Hkv <= 0) return fail(FA_ERR_INVALID_ARG, "%s: Hkv=%d", fn, Hkv);
+  if (d != 64 && d != 128)
+    return fail(FA_ERR_UNSUPPORTED, "%s: d=%d (supported: 64, 128)", fn, d);
+  if (page_size != 16) return fail(FA_ERR_UNSUPPORTED, "%s: page_size=%d (supported: 16)", fn, page_size);
+  if (num_seqs == 0 || total == 0) {
+    *nothing = true;
+    return FA_OK;
+  }
+  if (k_cache == nullptr || v_cache == nullptr || k_scale == nullptr || v_scale == nullptr ||
+      block_table == nullptr || seq_lens == nullptr || (need_cu && cu == nullptr))
+    return fail(FA_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (num_pages == 0 || max_blocks_per_seq == 0)
+    return fail(FA_ERR_INVALID_ARG, "%s: empty page pool or block table", fn);
+  // cache rows (page * Hkv + head) * 16 and token positions are 32-bit
+  if ((long long)num_pages * Hkv * 16 > 0x7fffffffLL || (long long)total * Hkv > 0x7fffffffLL ||
+      max_blocks_per_seq > 0x7ffffff)
+    return fail(FA_ERR_UNSUPPORTED, "%s: page pool, block table or rows too large", fn);
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale) ||
+      (reinterpret_cast<uintptr_t>(block_table) & 3u) ||
+      (reinterpret_cast<uintptr_t>(seq_lens) & 3u) || (reinterpret_cast<uintptr_t>(cu) & 3u))
+    return fail(FA_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+  return FA_OK;
+}
+
+fa_status check_window(const char* fn, int causal, int window, int sinks) {
+  if (window < 0 || sinks < 0)
+    return fail(FA_ERR_INVALID_ARG, "%s: window=%d sinks=%d (not negative)", fn, window, sinks);
+  if (window > 0 && !causal)
+    return fail(FA_ERR_INVALID_ARG, "%s: a window needs causal=1", fn);
+  return FA_OK;
+}
+
+fa_status check_heads(const char* fn, const void* q, const void* o, const float* lse, int H,
+                      int Hkv, float scale) {
+  if (H <= 0 || Hkv <= 0 || H % Hkv != 0)
+    return fail(FA_ERR_INVALID_ARG, "%s: H=%d Hkv=%d (need H %% Hkv == 0)", fn, H, Hkv);
+  if (H / Hkv > fa::kRowsE4m3Max)
+    return fail(FA_ERR_UNSUPPORTED, "%s: H/Hkv=%d > %d", fn, H / Hkv, fa::kRowsE4m3Max);
+  if (!(scale > 0.f) || scale == INFINITY)
+    return fail(FA_ERR_INVALID_ARG, "%s: scale must be positive and finite", fn);
+  if (!aligned16(q) || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return fail(FA_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+  return FA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_paged_kv_write_e4m3(const void* k, const void* v, void* k_cache, void* v_cache,
+                                 void* k_scale, void* v_scale, const int* block_table,
+                                 const int* seq_lens, const int* cu_seqlens, int num_seqs,
+                                 int total, int Hkv, int d, long long k_stride, long long v_stride,
+                                 int page_size, int num_pages, int max_blocks_per_seq,
+                                 void* stream) {
+  const char* fn = "fa_paged_kv_write_e4m3";
+  bool nothing = false;
+  fa_status st = check_cache(fn, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                             cu_seqlens, true, num_seqs, total, Hkv, d, page_size, num_pages,
+                             max_blocks_per_seq, &nothing);
+  if (st != FA_OK || nothing) return st;
+  if (k == nullptr || v == nullptr) return fail(FA_ERR_INVALID_ARG, "%s: null k/v", fn);
+  const long long row = (long long)Hkv * d;
+  if (k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return fail(FA_ERR_INVALID_ARG,
+                "%s: k_stride=%lld v_stride=%lld (multiples of 8, at least Hkv*d)", fn, k_stride,
+                v_stride);
+  if (!aligned16(k) || !aligned16(v)) return fail(FA_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+  int* sp = nullptr;
+  if ((st = status_ptr(&sp)) != FA_OK) return st;
+  fa::KvRowsParams p{k, v, k_stride, v_stride, k_cache, v_cache, k_scale, v_scale, block_table,
+                     seq_lens, cu_seqlens, num_seqs, total, Hkv, d, num_pages, max_blocks_per_seq,
+                     sp};
+  cudaError_t e = fa::launch_kv_write_e4m3(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fa_paged_kv_write_e4m3 launch");
+  return FA_OK;
+}
+
+fa_status fa_paged_kv_read_e4m3(const void* k_cache, const void* v_cache, const void* k_scale,
+                                const void* v_scale, const int* block_table, const int* seq_lens,
+                                const int* cu_seqlens, void* k, void* v, int num_seqs, int total,
+                                int Hkv, int d, int page_size, int num_pages,
+                                int max_blocks_per_seq, void* stream) {
+  const char* fn = "fa_paged_kv_read_e4m3";
+  bool nothing = false;
+  fa_status st = check_cache(fn, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                             cu_seqlens, true, num_seqs, total, Hkv, d, page_size, num_pages,
+                             max_blocks_per_seq, &nothing);
+  if (st != FA_OK || nothing) return st;
+  if (k == nullptr || v == nullptr) return fail(FA_ERR_INVALID_ARG, "%s: null k/v", fn);
+  if (!aligned16(k) || !aligned16(v)) return fail(FA_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+  int* sp = nullptr;
+  if ((st = status_ptr(&sp)) != FA_OK) return st;
+  fa::KvRowsParams p{k, v, 0, 0, const_cast<void*>(k_cache), const_cast<void*>(v_cache),
+                     const_cast<void*>(k_scale), const_cast<void*>(v_scale), block_table, seq_lens,
+                     cu_seqlens, num_seqs, total, Hkv, d, num_pages, max_blocks_per_seq, sp};
+  cudaError_t e = fa::launch_kv_read_e4m3(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fa_paged_kv_read_e4m3 launch");
+  return FA_OK;
+}
+
+fa_status fa_paged_decode_e4m3(const void* q, const void* k_cache, const void* v_cache,
+                               const void* k_scale, const void* v_scale, const int* block_table,
+                               const int* seq_lens, void* o, float* lse, int num_seqs, int H,
+                               int Hkv, int d, int page_size, int num_pages,
+                               int max_blocks_per_seq, float scale, int window, int sinks,
+                               void* stream) {
+  const char* fn = "fa_paged_decode_e4m3";
+  fa_status st = check_heads(fn, q, o, lse, H, Hkv, scale);
+  if (st == FA_OK) st = check_window(fn, 1, window, sinks);
+  if (st != FA_OK) return st;
+  bool nothing = false;
+  st = check_cache(fn, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, nullptr, false,
+                   num_seqs, num_seqs, Hkv, d, page_size, num_pages, max_blocks_per_seq, &nothing);
+  if (st != FA_OK || nothing) return st;
+  if (q == nullptr || o == nullptr) return fail(FA_ERR_INVALID_ARG, "%s: null q/o", fn);
+  if ((long long)num_seqs * H > 0xfffffffLL)
+    return fail(FA_ERR_UNSUPPORTED, "%s: num_seqs*H must stay below 2^28", fn);
+  int* sp = nullptr;
+  if ((st = status_ptr(&sp)) != FA_OK) return st;
+  fa::PagedE4m3Params p{q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, nullptr, o,
+                        lse, num_seqs, num_seqs, 1, H, Hkv, d, num_pages, max_blocks_per_seq,
+                        scale, 1, window, sinks, sp};
+  const char* why = nullptr;
+  cudaError_t e = fa::launch_rows_e4m3(p, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) return cuda_fail(e, why ? why : "fa_paged_decode_e4m3 launch");
+  return FA_OK;
+}
+
+fa_status fa_paged_prefill_e4m3(const void* q, const void* k_cache, const void* v_cache,
+                                const void* k_scale, const void* v_scale, const int* block_table,
+                                const int* seq_lens, const int* cu_seqlens_q, void* o, float* lse,
+                                int num_seqs, int total_q, int max_seqlen_q, int H, int Hkv, int d,
+                                int page_size, int num_pages, int max_blocks_per_seq, float scale,
+                                int causal, int window, int sinks, void* stream) {
+  const char* fn = "fa_paged_prefill_e4m3";
+  fa_status st = check_heads(fn, q, o, lse, H, Hkv, scale);
+  if (st != FA_OK) return st;
+  if (causal != 0 && causal != 1) return fail(FA_ERR_INVALID_ARG, "%s: causal=%d", fn, causal);
+  if ((st = check_window(fn, causal, window, sinks)) != FA_OK) return st;
+  if (max_seqlen_q < 0) return fail(FA_ERR_INVALID_ARG, "%s: negative size", fn);
+  bool nothing = false;
+  st = check_cache(fn, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens_q,
+                   true, num_seqs, total_q, Hkv, d, page_size, num_pages, max_blocks_per_seq,
+                   &nothing);
+  if (st != FA_OK || nothing || max_seqlen_q == 0) return st;
+  if (q == nullptr || o == nullptr) return fail(FA_ERR_INVALID_ARG, "%s: null q/o", fn);
+  if (max_seqlen_q > total_q) max_seqlen_q = total_q;   // no sequence has more
+  if ((long long)num_seqs * max_seqlen_q * H > 0xfffffffLL)
+    return fail(FA_ERR_UNSUPPORTED, "%s: num_seqs*max_seqlen_q*H must stay below 2^28", fn);
+  int* sp = nullptr;
+  if ((st = status_ptr(&sp)) != FA_OK) return st;
+  fa::PagedE4m3Params p{q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens_q,
+                        o, lse, num_seqs, total_q, max_seqlen_q, H, Hkv, d, num_pages,
+                        max_blocks_per_seq, scale, causal, window, sinks, sp};
+  const char* why = nullptr;
+  cudaError_t e = fa::launch_rows_e4m3(p, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) return cuda_fail(e, why ? why : "fa_paged_prefill_e4m3 launch");
+  return FA_OK;
+}
+
 fa_status fa_split_combine(const float* part_m, const float* part_l, const float* part_o, void* o,
                            float* lse, int num_seqs, int H, int num_splits, int dv, void* stream) {
   const char* fn = "fa_split_combine";

@@ -129,6 +129,45 @@ struct GatherParams {
   int* status;
 };
 
+// Rows written to, or read back from, the e4m3 paged cache.
+struct KvRowsParams {
+  const void* k;             // bf16 rows [total][Hkv][d] (written by the read-back)
+  const void* v;
+  long long k_stride, v_stride;  // write: elements from one token to the next
+  void* k_cache;             // e4m3 [pages][Hkv][16][d]
+  void* v_cache;
+  void* k_scale;             // scale bytes [pages][Hkv][16]
+  void* v_scale;
+  const int* block_table;
+  const int* seq_lens;
+  const int* cu;
+  int num_seqs, total, Hkv, d, num_pages, max_blocks;
+  int* status;
+};
+
+// Attention of a few query rows per sequence over the e4m3 paged cache.
+struct PagedE4m3Params {
+  const void* q;             // bf16 [total_q][H][d]
+  const void* k_cache;
+  const void* v_cache;
+  const void* k_scale;
+  const void* v_scale;
+  const int* block_table;
+  const int* seq_lens;
+  const int* cu_q;           // null: one query token per sequence
+  void* o;                   // bf16 [total_q][H][d]
+  float* lse;                // decode [S][H], chunk [H][total_q]; may be null
+  int num_seqs, total_q, max_q, H, Hkv, d, num_pages, max_blocks;
+  float scale;
+  int causal, window, sinks; // window 0: none
+  int* status;
+};
+
+cudaError_t launch_kv_write_e4m3(const KvRowsParams& p, cudaStream_t stream);
+cudaError_t launch_kv_read_e4m3(const KvRowsParams& p, cudaStream_t stream);
+// Query rows (tokens x grouped heads) of one kv head that the split kernel takes.
+constexpr int kRowsE4m3Max = 32;
+cudaError_t launch_rows_e4m3(const PagedE4m3Params& p, cudaStream_t stream, const char** why);
 cudaError_t launch_fwd_f32(const FwdParams& p, cudaStream_t stream);
 cudaError_t launch_fwd_bf16(const FwdParams& p, cudaStream_t stream, const char** why);
 // fused: partials and merge in one launch (p.tickets, p.o, p.lse set)
