@@ -154,6 +154,35 @@ fa_status fa_forward_varlen(const void* q, const void* k, const void* v, void* o
                             int H, int Hkv, int d, int dv, float scale, int causal, void* stream);
 
 /*
+ * fa_forward_window, fa_forward_varlen_window — bf16 attention forward under
+ * a sliding window with a few first tokens that stay visible (sinks).
+ * Passage: the pages name no window; the recurrence ("手搓 Attention" §7
+ * version 4) runs over the tiles that hold a visible key only, as it does for
+ * the causal mask (§6).
+ *
+ * Arguments, layouts and device status as fa_forward and fa_forward_varlen,
+ * always causal (bottom-right): the query at position p = i + (m - n) sees key
+ * j iff j <= p and (window == 0, or j > p - window, or j < sinks).
+ *   window  0: no window; w > 0: the last w keys, the query's own among them
+ *   sinks   keys from the start that stay visible under a window (ignored
+ *           without one)
+ * K/V tiles between the sinks and the window are never loaded, so the work is
+ * linear in n for a fixed window.
+ * Supported: d == dv in {64, 128}; pointers 16-byte aligned; dense: B*n, B*m
+ * and H*n below 2^31; packed: H*total_q below 2^31, num_seqs*max_seqlen_q*H
+ * below 2^36.
+ */
+fa_status fa_forward_window(const void* q, const void* k, const void* v, void* o, float* lse,
+                            int B, int H, int Hkv, int n, int m, int d, int dv, float scale,
+                            int window, int sinks, void* stream);
+
+fa_status fa_forward_varlen_window(const void* q, const void* k, const void* v, void* o,
+                                   float* lse, const int* cu_seqlens_q, const int* cu_seqlens_k,
+                                   int num_seqs, int total_q, int total_k, int max_seqlen_q,
+                                   int max_seqlen_k, int H, int Hkv, int d, int dv, float scale,
+                                   int window, int sinks, void* stream);
+
+/*
  * fa_paged_prefill — bf16 attention for several new query tokens per
  * sequence against that sequence's paged keys (chunked prefill).
  * Passage: "S12 FlashAttention", 它还解锁了什么 (the tiles the recurrence walks
@@ -418,7 +447,13 @@ fa_status fa_paged_decode_e4m3(const void* q, const void* k_cache, const void* v
  *                  a window needs causal = 1
  * A sequence with bad offsets, more than max_seqlen_q queries or a bad
  * seq_lens[s] is skipped (its rows are not written) and sets
- * FA_ERR_INVALID_ARG.
+ * FA_ERR_INVALID_ARG.  Bad page ids set FA_ERR_BAD_BLOCK_TABLE; the sequence's
+ * output is then unspecified.
+ * Cache contents of keys that none of a sequence's queries sees are never
+ * used; a NaN in a key that one query sees may reach others of its sequence.
+ * Chunks of at most 32 rows (max_seqlen_q * H / Hkv) run as
+ * fa_paged_decode_e4m3 does; larger ones on the tcgen05 path of fa_forward,
+ * their K/V tiles widened to bf16 (exactly) on the way to the tensor cores.
  * Supported: H / Hkv <= 32; num_seqs*max_seqlen_q*H below 2^28.
  */
 fa_status fa_paged_prefill_e4m3(const void* q, const void* k_cache, const void* v_cache,

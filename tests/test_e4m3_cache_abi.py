@@ -1,4 +1,5 @@
-"""Refusals of the e4m3 paged cache's entries, on the CPU: nothing is launched."""
+"""Refusals of the e4m3 paged cache's and the windowed forward's entries, on the CPU: nothing is
+launched."""
 import pytest
 
 from tiled_online_softmax_sm_gb300 import binding as fb
@@ -87,3 +88,45 @@ def test_prefill_refusals(lib):
         assert _prefill(lib, **kw) == fb.FA_ERR_INVALID_ARG, kw
     assert _prefill(lib, T=0) == fb.FA_OK
     assert _prefill(lib, mq=0) == fb.FA_OK
+
+
+def _win(lib, **kw):
+    a = dict(q=16, k=16, v=16, o=16, lse=16, B=1, H=2, Hkv=1, n=8, m=8, d=128, dv=128, scale=0.1,
+             win=4, sinks=1)
+    a.update(kw)
+    return lib.fa_forward_window(a["q"], a["k"], a["v"], a["o"], a["lse"], a["B"], a["H"], a["Hkv"],
+                                 a["n"], a["m"], a["d"], a["dv"], a["scale"], a["win"], a["sinks"], None)
+
+
+def _varwin(lib, **kw):
+    a = dict(q=16, k=16, v=16, o=16, lse=16, cq=16, ck=16, S=2, Tq=20, Tk=20, mq=10, mk=10, H=2,
+             Hkv=1, d=128, dv=128, scale=0.1, win=4, sinks=1)
+    a.update(kw)
+    return lib.fa_forward_varlen_window(a["q"], a["k"], a["v"], a["o"], a["lse"], a["cq"], a["ck"],
+                                        a["S"], a["Tq"], a["Tk"], a["mq"], a["mk"], a["H"], a["Hkv"],
+                                        a["d"], a["dv"], a["scale"], a["win"], a["sinks"], None)
+
+
+@pytest.mark.parametrize("call", [_win, _varwin])
+def test_window_refusals(lib, call):
+    for kw in (dict(win=-1), dict(sinks=-2), dict(H=3, Hkv=2), dict(H=0), dict(q=None), dict(o=None),
+               dict(k=None), dict(v=None), dict(q=8), dict(o=24), dict(lse=2), dict(scale=0.0),
+               dict(scale=float("nan")), dict(scale=float("inf"))):
+        assert call(lib, **kw) == fb.FA_ERR_INVALID_ARG, kw
+    for kw in (dict(d=96, dv=96), dict(dv=64)):
+        assert call(lib, **kw) == fb.FA_ERR_UNSUPPORTED, kw
+
+
+def test_window_sizes(lib):
+    assert _win(lib, B=-1) == fb.FA_ERR_INVALID_ARG
+    assert _win(lib, n=-1) == fb.FA_ERR_INVALID_ARG
+    assert _win(lib, B=0) == fb.FA_OK
+    assert _win(lib, n=0) == fb.FA_OK
+    assert _win(lib, n=1 << 30) == fb.FA_ERR_UNSUPPORTED
+    for kw in (dict(S=-1), dict(Tq=-1), dict(Tk=-1), dict(mq=-1), dict(mk=-1), dict(cq=None),
+               dict(ck=None), dict(cq=18), dict(ck=17)):
+        assert _varwin(lib, **kw) == fb.FA_ERR_INVALID_ARG, kw
+    assert _varwin(lib, S=0) == fb.FA_OK
+    assert _varwin(lib, Tq=0) == fb.FA_OK
+    assert _varwin(lib, mq=0) == fb.FA_OK
+    assert _varwin(lib, Tq=1 << 30, mq=1 << 30) == fb.FA_ERR_UNSUPPORTED

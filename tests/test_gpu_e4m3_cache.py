@@ -1,8 +1,7 @@
 """The e4m3 paged cache on the GPU: writing, reading back, decode and chunks.
 
 Codes, scale bytes and read-back rows are compared bit for bit with a plain
-float64 implementation; attention within the bounds that _e4m3.bounds derives
-(weights rounded to f16: 2^-11).  Slots no query sees hold NaN codes.
+float64 implementation; attention within the bounds that _e4m3.bounds derives.  Slots no query sees hold NaN codes.
 """
 import numpy as np
 import pytest
@@ -13,7 +12,8 @@ from tiled_online_softmax_sm_gb300 import binding as fb
 import _e4m3 as E
 
 pytestmark = pytest.mark.gpu
-W_ROUND = 2.0 ** -11
+W_ROUND = 2.0 ** -11           # up to 32 rows (tokens x group) per kv head: weights rounded to f16
+P_ROUND = 2.0 ** -7 * 1.01     # more: P rounded to bf16 (2^-8) in the value product and in O's divisor
 
 
 def _i32(a):
@@ -346,7 +346,7 @@ def test_short_chunks(d, group, causal):
     lens, new = [1, 16, 17, 130, 0, 300, 5], [1, 4, 3, 8, 2, 0, 8]   # the last: more queries than keys
     c = _cache(rng, lens, 2, d)
     q = E.bf16(rng.standard_normal((sum(new), 2 * group, d)))[0]
-    _chunk_check(c, q, new, causal)
+    _chunk_check(c, q, new, causal, rounding=W_ROUND if 8 * group <= 32 else P_ROUND)
     assert fb.fa_get_device_status() == 0
 
 
@@ -358,6 +358,128 @@ def test_short_chunks_window(window, sinks):
     q = E.bf16(rng.standard_normal((sum(new), 6, 128)))[0]
     _chunk_check(c, q, new, True, window, sinks)
     assert fb.fa_get_device_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [1, 3, 4, 16, 32])
+@pytest.mark.parametrize("causal", [True, False])
+def test_chunks(d, group, causal):
+    rng = np.random.default_rng(3 * group + d)
+    # partial pages and tiles, more queries than keys, no keys, no queries, single tokens
+    lens, new = [1, 128, 129, 700, 0, 300, 60, 259], [1, 64, 129, 40, 2, 0, 90, 1]
+    c = _cache(rng, lens, 2, d)
+    q = E.bf16(rng.standard_normal((sum(new), 2 * group, d)))[0]
+    _chunk_check(c, q, new, causal, rounding=P_ROUND)
+    assert fb.fa_get_device_status() == 0
+
+
+@pytest.mark.parametrize("group", [1, 4, 6])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 3), (64, 4), (128, 0), (129, 128), (200, 129),
+                                          (300, 400), (511, 1), (4000, 9)])
+def test_chunks_window(window, sinks, group):
+    rng = np.random.default_rng(window + group)
+    lens, new = [900, 257, 40, 130, 1200], [300, 257, 70, 1, 129]
+    c = _cache(rng, lens, 2, 128)
+    q = E.bf16(rng.standard_normal((sum(new), 2 * group, 128)))[0]
+    _chunk_check(c, q, new, True, window, sinks, P_ROUND)
+    assert fb.fa_get_device_status() == 0
+
+
+def test_chunk_equals_the_bf16_prefill_of_the_read_back_cache():
+    """Widening a tile is exact, so with one query head per kv head (no packing) the bits are
+    those of fa_paged_prefill on the rows read back into a bf16 cache."""
+    rng = np.random.default_rng(30)
+    lens, new = [300, 77, 513, 20], [200, 77, 60, 33]
+    for d in (64, 128):
+        c = _cache(rng, lens, 4, d, spread=2.0)
+        q = E.bf16(rng.standard_normal((sum(new), 4, d)))[0].cuda()
+        t, cu = c.gpu(), _i32(np.concatenate([[0], np.cumsum(new)]))
+        kc, vc = (torch.from_numpy(E.values(c.codes[x], np.where(c.scales[x] == 255, 0, c.scales[x]))
+                                   .astype(np.float32)).bfloat16().cuda() for x in "kv")
+        o1, l1 = fb.paged_prefill_e4m3(q, *t, cu, max(new), 0.1)
+        o2, l2 = fb.paged_prefill(q, kc, vc, t[4], t[5], cu, max(new), 0.1)
+        assert torch.equal(o1.view(torch.int16), o2.view(torch.int16))
+        assert torch.equal(l1.view(torch.int32), l2.view(torch.int32))
+    assert fb.fa_get_device_status() == 0
+
+
+def test_chunk_hidden_keys_are_never_used():
+    rng = np.random.default_rng(31)
+    lens, new, window, sinks = [700, 400, 300], [100, 60, 300], 150, 5
+    c = _cache(rng, lens, 2, 128)
+    for s, (L, n) in enumerate(zip(lens, new)):
+        pos = np.arange(sinks, max(sinks, L - n - window + 1))    # before the first query's window
+        for x in "kv":
+            c.codes[x][c.table[s, pos // 16], :, pos % 16] = 0x7f
+            c.scales[x][c.table[s, pos // 16], :, pos % 16] = 255
+    c.table[0, 1:(700 - 100 - 150) // 16] = -1
+    c.table[1, 1:3] = 1 << 30
+    q = E.bf16(rng.standard_normal((sum(new), 8, 128)))[0]
+    _chunk_check(c, q, new, True, window, sinks, P_ROUND)
+    assert fb.fa_get_device_status() == 0
+
+
+def test_chunks_of_many_sequences():
+    """More (sequence, query pair) combinations than the sorted list holds: one CTA per unit."""
+    rng = np.random.default_rng(32)
+    new = rng.integers(0, 50, 300)
+    lens = new + rng.integers(0, 60, 300)
+    c = _cache(rng, lens, 1, 64)
+    q = E.bf16(rng.standard_normal((int(new.sum()), 4, 64)))[0]
+    _chunk_check(c, q, list(new), True, 70, 3, P_ROUND)
+    assert fb.fa_get_device_status() == 0
+
+
+def test_chunk_scales_far_apart():
+    """Power-of-two scales from 2^-60 to 2^40: inside and outside the widening's f16 range."""
+    rng = np.random.default_rng(33)
+    L, n, d = 400, 120, 128
+    k = rng.standard_normal((L, 1, d)) * np.exp2(rng.integers(-12, 2, (L, 1, 1)))
+    v = rng.standard_normal((L, 1, d)) * np.exp2(rng.integers(-40, 41, (L, 1, 1)))
+    v[20:40], k[30] = 0.0, 0.0
+    c = E.Cache(rng, [k, k * 2.0 ** -40], [v, v * 2.0 ** -20])
+    q = rng.standard_normal((2 * n, 2, d))
+    q[n:] *= 2.0 ** 40
+    _chunk_check(c, E.bf16(q)[0], [n, n], True, 0, 0, P_ROUND)
+
+
+def test_chunk_status():
+    """Bad page ids, lengths, offsets and counts set the status; the other sequences' rows are
+    right and a skipped sequence's rows are left alone."""
+    rng = np.random.default_rng(34)
+    lens, new = [100, 200, 150], [40, 50, 60]
+    c = _cache(rng, lens, 2, 128, max_blocks=13)
+    q = E.bf16(rng.standard_normal((150, 8, 128)))[0]
+    cu, scale = [0, 40, 90, 150], E.softmax_scale(128)
+
+    def run(t, cu, mq=60):
+        o = torch.full((150, 8, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((8, 150), 9.0, device="cuda")
+        fb.fa_paged_prefill_e4m3(q.cuda(), *t, _i32(cu), o, lse, 3, 150, mq, 8, 2, 128, 16,
+                                 c.num_pages, 13, scale)
+        st = fb.fa_get_device_status()
+        good = []
+        for s in range(3):
+            r = slice(cu[s], cu[s + 1])
+            ref = E.attend(q[r].double().numpy(), c.rows["k"][s], c.rows["v"][s], scale)
+            try:
+                E.check(_f64(o[r]), _f64(lse[:, r]).T, ref, 128, P_ROUND)
+                good.append(s)
+            except AssertionError:
+                pass
+        return st, good, [s for s in range(3) if (o[cu[s]:cu[s + 1]] == 9.0).all()]
+
+    t = c.gpu()
+    assert run(t, cu) == (0, [0, 1, 2], [])
+    t[4][1, 3] = c.num_pages
+    st, good, left = run(t, cu)     # (that sequence's rows are unspecified)
+    assert st == fb.FA_ERR_BAD_BLOCK_TABLE and {0, 2} <= set(good)
+    for bad_len in (-1, 13 * 16 + 1):
+        t = c.gpu()
+        t[5][2] = bad_len
+        assert run(t, cu) == (fb.FA_ERR_INVALID_ARG, [0, 1], [2])
+    assert run(c.gpu(), cu, mq=55) == (fb.FA_ERR_INVALID_ARG, [0, 1], [2])
+    assert run(c.gpu(), [0, 40, 90, 151])[0] == fb.FA_ERR_INVALID_ARG
 
 
 def test_chunk_of_one_token_is_the_decode():
@@ -379,7 +501,7 @@ def test_serving_loop(window, sinks):
     attends from them; every step's output is held to the rows quantised so far."""
     rng = np.random.default_rng(20)
     S, H, Hkv, d = 3, 8, 2, 128
-    steps = [[37, 5, 64], [20, 0, 33]] + [[1, 1, 1]] * 4
+    steps = [[37, 5, 64], [20, 0, 33], [2, 1, 2]] + [[1, 1, 1]] * 4
     full = np.array(steps).sum(0)
     blocks = int((full.max() + 15) // 16)
     table = rng.permutation(S * blocks).reshape(S, blocks).astype(np.int32)
@@ -412,7 +534,7 @@ def test_serving_loop(window, sinks):
                 if name == "v":
                     vexp[s] = np.concatenate([vexp[s], b.astype(float) - 127])
             ref = E.attend(qd[r], rows["k"][s], rows["v"][s], scale, True, window, sinks, vexp[s])
-            E.check(o[r], lse[r], ref, d, 2.0 ** -7, f"step {new} sequence {s}")
+            E.check(o[r], lse[r], ref, d, P_ROUND, f"step {new} sequence {s}")
         back, _ = fb.paged_kv_read_e4m3(*cache, _i32(np.concatenate([[0], np.cumsum(lens)])),
                                         int(lens.sum()))
         assert np.array_equal(_f64(back), np.concatenate(rows["k"]))

@@ -35,6 +35,7 @@ FA_ERR_DEBUG_CHECK = 7
 EXPORTED = ("fa_forward", "fa_forward_fp8", "fa_forward_f32", "fa_forward_varlen", "fa_paged_prefill",
             "fa_paged_decode_workspace_size",
             "fa_paged_decode", "fa_paged_decode_fused", "fa_paged_decode_noalloc", "fa_paged_gather", "fa_split_combine",
+            "fa_forward_window", "fa_forward_varlen_window",
             "fa_paged_kv_write_e4m3", "fa_paged_kv_read_e4m3", "fa_paged_decode_e4m3",
             "fa_paged_prefill_e4m3",
             "fa_last_error",
@@ -67,6 +68,8 @@ def load(path: str = LIB_PATH):
         lib.fa_forward_f32.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, F, I, P]
         lib.fa_forward_fp8.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, F, F, F, F, I, P]
         lib.fa_forward_varlen.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, I, P]
+        lib.fa_forward_window.argtypes = [P] * 5 + [I, I, I, I, I, I, I, F, I, I, P]
+        lib.fa_forward_varlen_window.argtypes = [P] * 7 + [I] * 9 + [F, I, I, P]
         lib.fa_paged_prefill.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, I, P]
         lib.fa_paged_decode_workspace_size.argtypes = [I, I, I, I]
         lib.fa_paged_decode_workspace_size.restype = Z
@@ -87,6 +90,7 @@ def load(path: str = LIB_PATH):
                      "fa_paged_prefill",
                      "fa_paged_decode", "fa_paged_decode_fused",
                      "fa_paged_decode_noalloc", "fa_paged_gather", "fa_split_combine",
+                     "fa_forward_window", "fa_forward_varlen_window",
                      "fa_paged_kv_write_e4m3", "fa_paged_kv_read_e4m3", "fa_paged_decode_e4m3",
                      "fa_paged_prefill_e4m3", "fa_get_device_status"):
             getattr(lib, name).restype = I
@@ -142,6 +146,21 @@ def fa_forward_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, num_seqs, tot
                                     _p(cu_seqlens_k), num_seqs, total_q, total_k, max_seqlen_q,
                                     max_seqlen_k, H, Hkv, d, dv, float(scale), int(causal),
                                     _stream(stream)))
+
+
+def fa_forward_window(q, k, v, o, lse, B, H, Hkv, n, m, d, dv, scale, window, sinks=0,
+                      stream=None):
+    _check(load().fa_forward_window(_p(q), _p(k), _p(v), _p(o), _p(lse), B, H, Hkv, n, m, d, dv,
+                                    float(scale), int(window), int(sinks), _stream(stream)))
+
+
+def fa_forward_varlen_window(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, num_seqs, total_q,
+                             total_k, max_seqlen_q, max_seqlen_k, H, Hkv, d, dv, scale, window,
+                             sinks=0, stream=None):
+    _check(load().fa_forward_varlen_window(_p(q), _p(k), _p(v), _p(o), _p(lse), _p(cu_seqlens_q),
+                                           _p(cu_seqlens_k), num_seqs, total_q, total_k,
+                                           max_seqlen_q, max_seqlen_k, H, Hkv, d, dv, float(scale),
+                                           int(window), int(sinks), _stream(stream)))
 
 
 def fa_paged_prefill(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, o, lse, num_seqs,
@@ -296,6 +315,39 @@ def forward_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen
     lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
     fa_forward_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, S, Tq, Tk, max_seqlen_q,
                       max_seqlen_k, H, Hkv, d, dv, scale, causal, stream)
+    return o, lse
+
+
+def forward_window(q, k, v, scale, window, sinks=0, stream=None):
+    """q [B,n,H,d], k/v [B,m,Hkv,d] bf16, causal under a sliding window with sinks
+    -> (o [B,n,H,d] bf16, lse [B,H,n] fp32)."""
+    import torch
+    B, n, H, d = q.shape
+    m, Hkv = k.shape[1:3]
+    _tensors("forward_window", q, q=(q, torch.bfloat16, (B, n, H, d)),
+             k=(k, torch.bfloat16, (B, m, Hkv, d)), v=(v, torch.bfloat16, (B, m, Hkv, d)))
+    o = torch.empty((B, n, H, d), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((B, H, n), dtype=torch.float32, device=q.device)
+    fa_forward_window(q, k, v, o, lse, B, H, Hkv, n, m, d, d, scale, window, sinks, stream)
+    return o, lse
+
+
+def forward_varlen_window(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale,
+                          window, sinks=0, stream=None):
+    """Packed q [Tq,H,d], k/v [Tk,Hkv,d] bf16, causal under a sliding window with sinks
+    -> (o [Tq,H,d] bf16, lse [H,Tq] fp32)."""
+    import torch
+    Tq, H, d = q.shape
+    Tk, Hkv = k.shape[:2]
+    S = cu_seqlens_q.shape[0] - 1
+    _tensors("forward_varlen_window", q, q=(q, torch.bfloat16, (Tq, H, d)),
+             k=(k, torch.bfloat16, (Tk, Hkv, d)), v=(v, torch.bfloat16, (Tk, Hkv, d)),
+             cu_seqlens_q=(cu_seqlens_q, torch.int32, (S + 1,)),
+             cu_seqlens_k=(cu_seqlens_k, torch.int32, (S + 1,)))
+    o = torch.empty((Tq, H, d), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
+    fa_forward_varlen_window(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, S, Tq, Tk, max_seqlen_q,
+                             max_seqlen_k, H, Hkv, d, d, scale, window, sinks, stream)
     return o, lse
 
 

@@ -232,6 +232,70 @@ fa_status fa_forward_varlen(const void* q, const void* k, const void* v, void* o
   return FA_OK;
 }
 
+fa_status fa_forward_window(const void* q, const void* k, const void* v, void* o, float* lse,
+                            int B, int H, int Hkv, int n, int m, int d, int dv, float scale,
+                            int window, int sinks, void* stream) {
+  const char* fn = "fa_forward_window";
+  fa_status st = check_dense(q, k, v, o, lse, B, H, Hkv, n, m, d, dv, 1, fn);
+  if (st != FA_OK) return st;
+  if (!(scale > 0.f) || scale == INFINITY)
+    return fail(FA_ERR_INVALID_ARG, "%s: scale must be positive and finite", fn);
+  if (window < 0 || sinks < 0)
+    return fail(FA_ERR_INVALID_ARG, "%s: window=%d sinks=%d (not negative)", fn, window, sinks);
+  if (!(d == dv && (d == 64 || d == 128)))
+    return fail(FA_ERR_UNSUPPORTED, "%s: d=%d dv=%d (supported: d == dv in {64, 128})", fn, d, dv);
+  if ((st = check_rows(B, H, n, m, fn)) != FA_OK) return st;
+  if (B == 0 || n == 0) return FA_OK;
+  int* sp = nullptr;
+  if ((st = status_ptr(&sp)) != FA_OK) return st;
+  fa::FwdParams p{q, k, v, o, lse, nullptr, nullptr, B, H, Hkv, n, m, d, dv, 0, 0, scale, 1, sp};
+  p.window = window;
+  p.sinks = window > 0 ? sinks : 0;
+  const char* why = nullptr;
+  cudaError_t e = fa::launch_fwd_window(p, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) return cuda_fail(e, why ? why : "fa_forward_window launch");
+  return FA_OK;
+}
+
+fa_status fa_forward_varlen_window(const void* q, const void* k, const void* v, void* o,
+                                   float* lse, const int* cu_seqlens_q, const int* cu_seqlens_k,
+                                   int num_seqs, int total_q, int total_k, int max_seqlen_q,
+                                   int max_seqlen_k, int H, int Hkv, int d, int dv, float scale,
+                                   int window, int sinks, void* stream) {
+  const char* fn = "fa_forward_varlen_window";
+  if (num_seqs < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || total_q < 0 || total_k < 0)
+    return fail(FA_ERR_INVALID_ARG, "%s: negative size", fn);
+  if (!(scale > 0.f) || scale == INFINITY)
+    return fail(FA_ERR_INVALID_ARG, "%s: scale must be positive and finite", fn);
+  if (window < 0 || sinks < 0)
+    return fail(FA_ERR_INVALID_ARG, "%s: window=%d sinks=%d (not negative)", fn, window, sinks);
+  if (num_seqs > 0 && (cu_seqlens_q == nullptr || cu_seqlens_k == nullptr))
+    return fail(FA_ERR_INVALID_ARG, "%s: null cu_seqlens", fn);
+  if ((reinterpret_cast<uintptr_t>(cu_seqlens_q) & 3u) ||
+      (reinterpret_cast<uintptr_t>(cu_seqlens_k) & 3u))
+    return fail(FA_ERR_INVALID_ARG, "%s: misaligned cu_seqlens", fn);
+  fa_status st = check_dense(q, k, v, o, lse, num_seqs, H, Hkv, max_seqlen_q, max_seqlen_k, d, dv,
+                             1, fn);
+  if (st != FA_OK) return st;
+  if (!(d == dv && (d == 64 || d == 128)))
+    return fail(FA_ERR_UNSUPPORTED, "%s: d=%d dv=%d (supported: d == dv in {64, 128})", fn, d, dv);
+  if (num_seqs == 0 || max_seqlen_q == 0 || total_q == 0) return FA_OK;
+  if (max_seqlen_q > total_q) max_seqlen_q = total_q;   // no sequence has more
+  if ((long long)H * total_q > 0x7fffffffLL || (long long)num_seqs * max_seqlen_q * H > 0xfffffffffLL)
+    return fail(FA_ERR_UNSUPPORTED, "%s: H*total_q must stay below 2^31, num_seqs*max_seqlen_q*H "
+                "below 2^36", fn);
+  int* sp = nullptr;
+  if ((st = status_ptr(&sp)) != FA_OK) return st;
+  fa::FwdParams p{q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, num_seqs, H, Hkv,
+                  max_seqlen_q, max_seqlen_k, d, dv, total_q, total_k, scale, 1, sp};
+  p.window = window;
+  p.sinks = window > 0 ? sinks : 0;
+  const char* why = nullptr;
+  cudaError_t e = fa::launch_fwd_window(p, static_cast<cudaStream_t>(stream), &why);
+  if (e != cudaSuccess) return cuda_fail(e, why ? why : "fa_forward_varlen_window launch");
+  return FA_OK;
+}
+
 fa_status fa_paged_prefill(const void* q, const void* k_cache, const void* v_cache,
                            const int* block_table, const int* seq_lens, const int* cu_seqlens_q,
                            void* o, float* lse, int num_seqs, int total_q, int max_seqlen_q,
@@ -592,11 +656,26 @@ fa_status fa_paged_prefill_e4m3(const void* q, const void* k_cache, const void* 
     return fail(FA_ERR_UNSUPPORTED, "%s: num_seqs*max_seqlen_q*H must stay below 2^28", fn);
   int* sp = nullptr;
   if ((st = status_ptr(&sp)) != FA_OK) return st;
-  fa::PagedE4m3Params p{q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens_q,
-                        o, lse, num_seqs, total_q, max_seqlen_q, H, Hkv, d, num_pages,
-                        max_blocks_per_seq, scale, causal, window, sinks, sp};
   const char* why = nullptr;
-  cudaError_t e = fa::launch_rows_e4m3(p, static_cast<cudaStream_t>(stream), &why);
+  cudaError_t e;
+  if ((long long)max_seqlen_q * (H / Hkv) <= fa::kRowsE4m3Max) {
+    fa::PagedE4m3Params p{q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                          cu_seqlens_q, o, lse, num_seqs, total_q, max_seqlen_q, H, Hkv, d,
+                          num_pages, max_blocks_per_seq, scale, causal, window, sinks, sp};
+    e = fa::launch_rows_e4m3(p, static_cast<cudaStream_t>(stream), &why);
+  } else {
+    fa::FwdParams p{q, k_cache, v_cache, o, lse, cu_seqlens_q, nullptr, num_seqs, H, Hkv,
+                    max_seqlen_q, 0, d, d, total_q, 0, scale, causal, sp};
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_pages = num_pages;
+    p.window = window;
+    p.sinks = window > 0 ? sinks : 0;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    e = fa::launch_fwd_e4m3_cache(p, static_cast<cudaStream_t>(stream), &why);
+  }
   if (e != cudaSuccess) return cuda_fail(e, why ? why : "fa_paged_prefill_e4m3 launch");
   return FA_OK;
 }

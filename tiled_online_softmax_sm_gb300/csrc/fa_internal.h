@@ -88,6 +88,10 @@ struct FwdParams {
   // e4m3 operands (q, k, v hold x / descale), bf16 output
   int fp8 = 0;
   float q_descale = 1.f, k_descale = 1.f, v_descale = 1.f;
+  // sliding window (0: none; causal only) and sinks; e4m3 page caches' scale bytes
+  int window = 0, sinks = 0;
+  const void* k_scale = nullptr;
+  const void* v_scale = nullptr;
 };
 
 struct DecodeParams {
@@ -170,6 +174,8 @@ constexpr int kRowsE4m3Max = 32;
 cudaError_t launch_rows_e4m3(const PagedE4m3Params& p, cudaStream_t stream, const char** why);
 cudaError_t launch_fwd_f32(const FwdParams& p, cudaStream_t stream);
 cudaError_t launch_fwd_bf16(const FwdParams& p, cudaStream_t stream, const char** why);
+cudaError_t launch_fwd_window(const FwdParams& p, cudaStream_t stream, const char** why);
+cudaError_t launch_fwd_e4m3_cache(const FwdParams& p, cudaStream_t stream, const char** why);
 // fused: partials and merge in one launch (p.tickets, p.o, p.lse set)
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream, bool fused);
 cudaError_t launch_decode_partials(const DecodeParams& p, cudaStream_t stream);
