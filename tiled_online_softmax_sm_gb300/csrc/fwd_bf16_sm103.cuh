@@ -135,7 +135,7 @@ constexpr int kMaxSortedCombos = KV8 ? 256 : 512;
 
 template <bool KV8>
 struct Shared {
-  uint16_t work[kMaxSortedCombos<KV8>];    // K/V tiles of combination b * num_pairs + t
+  alignas(16) uint16_t work[kMaxSortedCombos<KV8>];    // K/V tiles of combination b * num_pairs + t
   uint16_t order[kMaxSortedCombos<KV8>];   // combinations, heaviest first
   int n_order;                        // combinations with any work
   uint64_t q_full[2];
@@ -171,24 +171,54 @@ struct Unit {
   bool rows;       // the unit holds at least one valid query row
   bool bad;        // varlen offsets outside the buffers
   bool split;      // the two tiles are one query tile over two key ranges
-  // WIN: the unit's K/V tiles are a list, the sinks' tiles 0 .. ns - 1 and then
-  // tiles w0, w0 + 1, ...; n_kv[i] ends tile i's part of it, and tile 1 skips
-  // entry ns when that K/V tile lies before its window (skip1)
-  int ns, w0;
-  bool skip1;
+  // WIN: the unit's K/V tiles are a list of n_list entries, the nw tiles from
+  // w0 on, rotated by rot, and then the sinks' tiles 0, 1, ...  Tile i skips
+  // entry skip[i] (-1: none): tile 0 the last one, when all of it lies behind
+  // its rows, tile 1 the first one, when all of it lies before their windows.
+  int n_list, w0, nw, rot;
+  int skip[2];
   int key_sink, key_lo, key_hi;  // keys some row of the unit sees: [0, key_sink), [key_lo, key_hi)
 };
 
-// K/V tile of list entry j.
+// Entries of the unit's K/V tile list, and the K/V tile of entry j.
 template <bool WIN>
-__device__ __forceinline__ int list_tile(const Unit& U, int j) {
-  return WIN && j >= U.ns ? U.w0 + (j - U.ns) : j;
+__device__ __forceinline__ int list_size(const Unit& U) {
+  return WIN ? U.n_list : max(U.n_kv[0], U.n_kv[1]);
 }
 
-// Whether query tile i uses list entry j.
+template <bool WIN>
+__device__ __forceinline__ int list_tile(const Unit& U, int j) {
+  if (!WIN) return j;
+  if (j >= U.nw) return j - U.nw;
+  const int t = j + U.rot;
+  return U.w0 + (t < U.nw ? t : t - U.nw);
+}
+
+// Whether query tile i uses entry j, and the first and last entries it uses.
+// (selects, not U.x[i]: a runtime index would put the unit in local memory)
 template <bool WIN>
 __device__ __forceinline__ bool uses(const Unit& U, int i, int j) {
-  return j < (i == 0 ? U.n_kv[0] : U.n_kv[1]) && !(WIN && i == 1 && U.skip1 && j == U.ns);
+  const int n = i == 0 ? U.n_kv[0] : U.n_kv[1];
+  if (!WIN) return j < n;
+  return n > 0 && j < U.n_list && j != (i == 0 ? U.skip[0] : U.skip[1]);
+}
+
+template <bool WIN>
+__device__ __forceinline__ int first_use(const Unit& U, int i) {
+  return WIN && (i == 0 ? U.skip[0] : U.skip[1]) == 0 ? 1 : 0;
+}
+
+template <bool WIN>
+__device__ __forceinline__ int last_use(const Unit& U, int i) {
+  if (!WIN) return (i == 0 ? U.n_kv[0] : U.n_kv[1]) - 1;
+  return U.n_list - 1 - ((i == 0 ? U.skip[0] : U.skip[1]) == U.n_list - 1 ? 1 : 0);
+}
+
+// Whether entry j + 1 is tile i's last.
+template <bool WIN>
+__device__ __forceinline__ bool last_next(const Unit& U, int i, int j) {
+  if (!WIN) return j + 2 == (i == 0 ? U.n_kv[0] : U.n_kv[1]);
+  return j + 1 == last_use<WIN>(U, i);
 }
 
 // Row max of a 128-key S row: 8 independent chains of three-input max (one
@@ -340,7 +370,7 @@ __device__ __forceinline__ Unit make_unit(int b, int h, int t, int H, int Hkv, i
   U.split = false;
   if constexpr (WIN) {
     const int diff = U.kv_len - U.q_len;   // position of query 0
-    int lo[2], hi[2];
+    int lo[2], hi[2], lo_last = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int qs = U.q_start0 + i * tile_q;
@@ -351,6 +381,7 @@ __device__ __forceinline__ Unit make_unit(int b, int h, int t, int H, int Hkv, i
       hi[i] = (!U.rows || qs >= U.q_len || keys <= 0) ? 0 : (keys + kBlockN - 1) / kBlockN;
       const int lo_key = causal && window > 0 ? max(0, qs + diff + 1 - window) : 0;
       lo[i] = lo_key / kBlockN;
+      if (hi[i] > 0) lo_last = lo_key;
       if (i == 0) {
         U.key_lo = lo_key;
         U.key_sink = min(sinks, lo_key);
@@ -359,11 +390,21 @@ __device__ __forceinline__ Unit make_unit(int b, int h, int t, int H, int Hkv, i
         U.key_hi = max(0, keys);
       }
     }
+    const int end = max(hi[0], hi[1]);
     U.w0 = lo[0];
-    U.ns = min((U.key_sink + kBlockN - 1) / kBlockN, lo[0]);
+    U.nw = end > lo[0] ? end - lo[0] : 0;
+    // The first tile a row uses sets its reference: start two tiles in, where
+    // (most) rows see whole tiles, and visit the window's masked first tiles and
+    // the few sinks last.  A reference from a handful of keys would be raised,
+    // or its sums missed, tile after tile.
+    // (A unit whose windows reach back to key 0 keeps the plain order.)
+    U.rot = lo_last > 0 ? max(0, min(2, U.nw - 2)) : 0;
+    U.n_list = U.nw > 0 ? U.nw + min((U.key_sink + kBlockN - 1) / kBlockN, lo[0]) : 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) U.n_kv[i] = hi[i] > 0 ? U.ns + hi[i] - lo[0] : 0;
-    U.skip1 = hi[1] > 0 && lo[1] > lo[0] && lo[0] * kBlockN >= sinks;
+    for (int i = 0; i < 2; ++i) U.n_kv[i] = hi[i] > 0 ? U.n_list : 0;
+    U.skip[0] = hi[0] > 0 && hi[0] < end ? U.nw - 1 - U.rot : -1;
+    U.skip[1] = hi[1] > 0 && lo[1] > lo[0] && lo[0] * kBlockN >= sinks
+                    ? (U.rot > 0 ? U.nw - U.rot : 0) : -1;
   } else {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -439,7 +480,33 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   // (b, h).  Sorted (varlen and paged, few combinations): every CTA builds the
   // same list of (sequence, pair) combinations ordered by K/V tiles
   // descending (ties by index), and unit u is head u % H of entry u / H.
-  if (VAR && sched_sorted) {
+  // Counted (windowed varlen and paged, few sequences: units of much the same
+  // size): every CTA sums up the sequences' pairs, and unit u is head u % Hg of
+  // pair u / Hg of all.
+  int* const pair_end = reinterpret_cast<int*>(&sh.work[0]);   // pairs of sequences 0 .. b
+  if (VAR && WIN && sched_sorted == 2) {
+    int run = 0;
+    if (warp == 0) {
+      for (int b0 = 0; b0 < B; b0 += 32) {
+        int c = 0;
+        if (b0 + lane < B) {
+          const Unit U = unit_bt(b0 + lane, 0, 0);
+          if (U.bad) atomicExch(status, kDevInvalidArg);  // skipped, touches nothing
+          c = U.bad ? 0 : (U.q_len + (2 * kBlockM >> gl) - 1) / (2 * kBlockM >> gl);
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, c, o);
+          if (lane >= o) c += v;
+        }
+        if (b0 + lane < B) pair_end[b0 + lane] = run + c;
+        run += __shfl_sync(0xffffffffu, c, 31);
+      }
+      if (lane == 0) sh.n_order = run;
+    }
+    __syncthreads();
+  }
+  if (VAR && sched_sorted == 1) {
     const int C = B * num_pairs;
     if (threadIdx.x == 0) sh.n_order = 0;
     __syncthreads();
@@ -470,6 +537,16 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   // about half a unit's time.
   const int num_units = VAR && sched_sorted ? Hg * sh.n_order : BH * num_pairs + (VAR ? 0 : num_split);
   auto unit_at = [&](int u) {
+    if (VAR && WIN && sched_sorted == 2) {
+      const int c = u / Hg;
+      int lo = 0, hi = B - 1;   // the first sequence whose pairs end past c
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (pair_end[mid] > c) hi = mid;
+        else lo = mid + 1;
+      }
+      return unit_bt(lo, u % Hg, c - (lo > 0 ? pair_end[lo - 1] : 0));
+    }
     if (VAR && sched_sorted) {
       const int c = sh.order[u / Hg];
       return unit_bt(c / num_pairs, u % Hg, c % num_pairs);
@@ -701,7 +778,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             return true;
           }
         };
-        const int n_kv_max = max(U.n_kv[0], U.n_kv[1]);
+        const int n_kv_max = list_size<WIN>(U);
         if (WIN || !U.split) {
           for (int j = 0; j < n_kv_max && ok; ++j)
             for (int which = 0; which < 2 && ok; ++which) ok = issue_kv(which, list_tile<WIN>(U, j));  // K then V
@@ -786,7 +863,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         if (u >= num_units) continue;
         const Unit U = FA_UNIT(u);
         if (!U.rows) continue;
-        const int n_kv_max = max(U.n_kv[0], U.n_kv[1]);
+        const int n_kv_max = list_size<WIN>(U);
         if (n_kv_max == 0) continue;
         #pragma unroll
         for (int i = 0; i < 2 && ok; ++i) {
@@ -850,10 +927,10 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           ptx::tc_fence_after();
           #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            if (!uses<WIN>(U, i, 0)) continue;
+            if (WIN ? !uses<WIN>(U, i, 0) : U.n_kv[i] == 0) continue;
             issue_s(i, slot);
             ptx::tc_commit(bar_s + 8 * i);
-            if (U.n_kv[i] == 1) ptx::tc_commit(bar_qe + 8 * i);
+            if (WIN ? last_use<WIN>(U, i) == 0 : U.n_kv[i] == 1) ptx::tc_commit(bar_qe + 8 * i);
           }
           ptx::tc_commit(bar_kve + 8 * slot);  // K(0)
         }
@@ -871,31 +948,32 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           ptx::tc_fence_after();
           // before the first P V of a unit, the previous unit's epilogue must
           // have read O_i out of tensor memory
-          if (j < U.n_kv[0]) {
-            if (j == 0 && !(ok = ptx::mbar_wait(bar_oe, (no[0] & 1) ^ 1, status, abort_flag))) break;
-            if (!(ok = issue_pv(0, sv, j == 0))) break;
-            if (j == U.n_kv[0] - 1) ptx::tc_commit(bar_o);
+          if (uses<WIN>(U, 0, j)) {
+            const bool first = j == first_use<WIN>(U, 0);
+            if (first && !(ok = ptx::mbar_wait(bar_oe, (no[0] & 1) ^ 1, status, abort_flag))) break;
+            if (!(ok = issue_pv(0, sv, first))) break;
+            if (j == last_use<WIN>(U, 0)) ptx::tc_commit(bar_o);
           }
           // release K(j) (last read by S_i(j), issued in the previous
           // iteration) here, behind a burst of queued MMAs rather than in the
           // gap after S_1(j); K(0) was released in the prologue
           if (j > 0) ptx::tc_commit(bar_kve + 8 * ((lc + 2 * j) % C::kStages));
-          if (j + 1 < U.n_kv[0]) {
+          if (uses<WIN>(U, 0, j + 1)) {
             issue_s(0, sk);
             ptx::tc_commit(bar_s);
-            if (j + 2 == U.n_kv[0]) ptx::tc_commit(bar_qe);
+            if (last_next<WIN>(U, 0, j)) ptx::tc_commit(bar_qe);
           }
           if (uses<WIN>(U, 1, j)) {
-            const bool first = j == (WIN && U.skip1 && U.ns == 0 ? 1 : 0);
+            const bool first = j == first_use<WIN>(U, 1);
             if (first && !(ok = ptx::mbar_wait(bar_oe + 8, (no[1] & 1) ^ 1, status, abort_flag))) break;
             if (!(ok = issue_pv(1, sv, first))) break;
-            if (j == U.n_kv[1] - 1) ptx::tc_commit(bar_o + 8);
+            if (j == last_use<WIN>(U, 1)) ptx::tc_commit(bar_o + 8);
           }
           ptx::tc_commit(bar_kve + 8 * sv);  // V(j)
           if (uses<WIN>(U, 1, j + 1)) {
             issue_s(1, sk);
             ptx::tc_commit(bar_s + 8);
-            if (j + 2 == U.n_kv[1]) ptx::tc_commit(bar_qe + 8);
+            if (last_next<WIN>(U, 1, j)) ptx::tc_commit(bar_qe + 8);
           }
         }
         lc += 2 * n_kv_max;
@@ -925,7 +1003,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         if (u >= num_units) continue;
         const Unit U = FA_UNIT(u);
         if (!U.rows) continue;
-        const int n_list = max(U.n_kv[0], U.n_kv[1]);
+        const int n_list = list_size<WIN>(U);
         for (int j2 = 0; j2 < 2 * n_list && ok; ++j2) {
           const int j = list_tile<WIN>(U, j2 >> 1);
           const int slot = lc % C::kStages, rslot = lc % C::kRawStages;
@@ -940,29 +1018,44 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           // weights never meet a NaN
           const int k0 = j * kBlockN;
           const bool whole = k0 + kBlockN <= U.key_hi && (k0 >= U.key_lo || k0 + kBlockN <= U.key_sink);
-#pragma unroll 4
-          for (int it = 0; it < kUnits; ++it) {
-            const int idx = it * 128 + tid;
+          auto put = [&](int idx, const uint4& x, uint32_t b) __attribute__((always_inline)) {
             const int row = idx / kUnits, un = idx % kUnits;
-            uint4 x = *reinterpret_cast<const uint4*>(raw + idx * 16);
-            uint32_t b = raw[128 * D + row];
-            if (!whole) {
-              const int key = k0 + row;
+            uint4 lo, hi;
+            ptx::widen16(x, b, lo, hi);
+            uint8_t* rowp = tile + (un >> 2) * 16384 + row * 128;
+            const bool odd = un >> 2;
+            const int p0 = ((2 * (un & 3)) ^ (row & 7) ^ (odd ? 1 : 0)) << 4;
+            *reinterpret_cast<uint4*>(rowp + p0) = odd ? hi : lo;
+            *reinterpret_cast<uint4*>(rowp + (p0 ^ 16)) = odd ? lo : hi;
+          };
+          if (whole) {
+            // two units at a time, their loads first: 974 us with one and a
+            // branch in the loop, 668 so (16 x 512-token chunks)
+#pragma unroll 1
+            for (int it = 0; it < kUnits; it += 2) {
+              uint4 x[2];
+              uint32_t b[2];
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int idx = (it + y) * 128 + tid;
+                x[y] = *reinterpret_cast<const uint4*>(raw + idx * 16);
+                b[y] = raw[128 * D + idx / kUnits];
+              }
+#pragma unroll
+              for (int y = 0; y < 2; ++y) put((it + y) * 128 + tid, x[y], b[y]);
+            }
+          } else {
+#pragma unroll 1
+            for (int it = 0; it < kUnits; ++it) {
+              const int idx = it * 128 + tid;
+              uint4 x = *reinterpret_cast<const uint4*>(raw + idx * 16);
+              uint32_t b = raw[128 * D + idx / kUnits];
+              const int key = k0 + idx / kUnits;
               if (!(key < U.key_sink || (key >= U.key_lo && key < U.key_hi))) {
                 x = make_uint4(0u, 0u, 0u, 0u);
                 b = 127u;
               }
-            }
-            uint4 lo, hi;
-            ptx::widen16(x, b, lo, hi);
-            uint8_t* rowp = tile + (un >> 2) * 16384 + row * 128;
-            const int p0 = ((2 * (un & 3)) ^ (row & 7)) << 4, p1 = p0 ^ 16;
-            if (un >> 2) {
-              *reinterpret_cast<uint4*>(rowp + p1) = hi;
-              *reinterpret_cast<uint4*>(rowp + p0) = lo;
-            } else {
-              *reinterpret_cast<uint4*>(rowp + p0) = lo;
-              *reinterpret_cast<uint4*>(rowp + p1) = hi;
+              put(idx, x, b);
             }
           }
           ptx::fence_proxy_async_smem();   // the MMA (and the next copy) come behind these accesses
@@ -1018,7 +1111,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       float l_p = 0.f;           // bf16: sum of the rounded p the P V MMA used (O's divisor)
       bool begun = false;        // this tile has used a K/V tile
       for (int jl = 0; jl < nkv; ++jl) {
-        if (WIN && !uses<WIN>(U, i, jl)) continue;
+        if (WIN && jl == (i == 0 ? U.skip[0] : U.skip[1])) continue;
         const int j = WIN ? (begun ? 1 : 0) : jl;   // 0: this tile's first K/V tile
         begun = true;
         // warp-uniform outcome: the tcgen05.ld/st below are warp-collective
@@ -1033,16 +1126,21 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         bool masked = k0 + kBlockN > U.kv_len || (causal && k0 + kBlockN - 1 > diag);
         int vis = U.kv_len - k0;
         if (causal) vis = min(vis, qi + (U.kv_len - U.q_len) - k0 + 1);
-        // WIN: keys [hide0, hide0 + hide_n) of the tile lie between the sinks
-        // and the row's window; the tile needs no mask when its last row sees
-        // its first key, or when all of it are sinks
-        int hide0 = 0, hide_n = 0;
+        // WIN: keys [hide0, hide1) of the tile lie between the sinks and the
+        // row's window; the tile needs that mask when its last row does not see
+        // its first key.  A tile before the window shows its sinks only.
+        int hide0 = 0, hide1 = 0;
+        bool low = false;
         if constexpr (WIN) {
           if (window > 0) {
-            const int tile_q = kBlockM >> gl;
-            hide0 = max(0, sinks - k0);
-            hide_n = max(0, (qi + (U.kv_len - U.q_len) - window + 1 - k0) - hide0);
-            masked = masked || (k0 < diag + tile_q - window && hide0 < kBlockN);
+            if (jl >= U.nw) {
+              vis = min(vis, sinks - k0);
+              masked = masked || k0 + kBlockN > sinks;
+            } else {
+              low = k0 < diag + (kBlockM >> gl) - window && k0 + kBlockN > sinks;
+              hide0 = max(0, sinks - k0);
+              hide1 = qi + (U.kv_len - U.q_len) - window + 1 - k0;
+            }
           }
         }
         uint32_t sr[4][32];
@@ -1055,7 +1153,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         float mred = -INFINITY;
         bool have_mred = false;
         auto load_s = [&](bool want_max) {
-          if (!masked && want_max) {
+          if (!masked && !low && want_max) {
             float mc[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) ptx::tmem_ld32_max(s_col + c * 32, sr[c], mc[c]);
@@ -1072,8 +1170,22 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             for (int c = 0; c < 4; ++c)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (c * 32 + e >= vis || (WIN && (uint32_t)(c * 32 + e - hide0) < (uint32_t)hide_n))
-                  sr[c][e] = __float_as_uint(-INFINITY);
+                if (c * 32 + e >= vis) sr[c][e] = __float_as_uint(-INFINITY);
+          }
+          if (WIN && low) {
+            if (hide0 == 0) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (c * 32 + e < hide1) sr[c][e] = __float_as_uint(-INFINITY);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (c * 32 + e >= hide0 && c * 32 + e < hide1) sr[c][e] = __float_as_uint(-INFINITY);
+            }
           }
         };
         load_s(j == 0 || max_first);
@@ -1370,7 +1482,10 @@ cudaError_t launch(const FwdParams& p, cudaStream_t stream, const char** why) {
   // pair) combinations (the kernel sorts them by size).  Otherwise one CTA
   // per unit, so the hardware block scheduler balances units whose sizes
   // depend on lengths the host does not know (idle units exit at once).
-  const bool sorted = varlen && (long long)p.B * num_pairs <= kMaxSortedCombos<KV8>;
+  // (A windowed launch's units are of much the same size: they are counted
+  // instead of sorted, for as many sequences as the list has room for.)
+  const bool counted = WIN && varlen && p.causal && p.window > 0 && p.B <= kMaxSortedCombos<KV8>;
+  const bool sorted = counted || (varlen && (long long)p.B * num_pairs <= kMaxSortedCombos<KV8>);
   const int grid = varlen && !sorted ? (int)units : (int)(units < sms ? units : sms);
   // Dense and non-causal (units of equal size): when the last wave of pair
   // units would leave at least half the CTAs idle, those units run as twice
@@ -1398,7 +1513,7 @@ cudaError_t launch(const FwdParams& p, cudaStream_t stream, const char** why) {
         tq, tk, tv, static_cast<__nv_bfloat16*>(p.o), p.lse, p.cu_q, p.cu_k, p.B, p.H, p.Hkv, p.n,
         p.m, varlen ? p.total_q : p.B * p.n, varlen ? p.total_k : p.B * p.m, num_pairs, scale_log2,
         p.causal, lse_stride_h, lse_stride_b, p.block_table, p.seq_lens, p.max_blocks, p.num_pages,
-        out_scale, sorted ? 1 : 0, num_split, p.status, p.window, p.sinks, gl,
+        out_scale, counted ? 2 : sorted ? 1 : 0, num_split, p.status, p.window, p.sinks, gl,
         static_cast<const uint8_t*>(p.k), static_cast<const uint8_t*>(p.v),
         static_cast<const uint8_t*>(p.k_scale), static_cast<const uint8_t*>(p.v_scale));
     err = cudaGetLastError();
