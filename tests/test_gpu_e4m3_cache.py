@@ -594,3 +594,36 @@ def test_offsets_past_32_bits():
                    E.quantise(v.double().numpy())[1].astype(float) - 127)
     E.check(_f64(o), _f64(lse), ref, d, W_ROUND)
     assert fb.fa_get_device_status() == 0
+
+
+def test_binding_refuses_tensors_the_c_entry_cannot_tell_apart():
+    rng = np.random.default_rng(40)
+    c = _cache(rng, [20, 30], 2, 64)
+    q = torch.zeros((2, 4, 64), dtype=torch.bfloat16, device="cuda")
+    good = c.gpu()
+
+    def refused(i=None, t=None, q=q):
+        a = list(good)
+        if i is not None:
+            a[i] = t
+        with pytest.raises(fb.FaError) as e:
+            fb.paged_decode_e4m3(q, *a, 0.1)
+        return e.value.status == fb.FA_ERR_INVALID_ARG
+
+    fb.paged_decode_e4m3(q, *good, 0.1)
+    assert refused(0, good[0].cpu())
+    assert refused(0, good[0].view(torch.uint8).to(torch.int16))
+    assert refused(1, good[1][:-1])
+    assert refused(2, good[2].view(torch.uint8).bool())
+    assert refused(3, good[3].transpose(1, 2))
+    assert refused(4, good[4].long())
+    assert refused(4, good[4][:, ::2]) if good[4].shape[1] > 1 else True
+    assert refused(5, good[5][:1])
+    assert refused(q=q.float())
+    assert refused(q=q.transpose(1, 2))
+    assert refused(q=q.cpu())
+    k = torch.zeros((2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    for bad in (k.float(), k[:1], k.cpu(), k.transpose(0, 1).contiguous().transpose(0, 1),
+                torch.zeros((2, 2, 128), dtype=torch.bfloat16, device="cuda")[:, :, ::2]):
+        with pytest.raises(fb.FaError):
+            fb.paged_kv_write_e4m3(k, bad, *good, _i32([0, 1, 2]))

@@ -18,6 +18,8 @@ import ctypes
 import os
 import threading
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 # FA_LIBRARY selects another build of the same ABI (the debug build,
 # libfa_gb300_debug.so, for instance); by default the in-tree library.
@@ -56,6 +58,8 @@ _lib = None
 def load(path: str = LIB_PATH):
     """Load the library (once) and declare the C signatures."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -109,7 +113,10 @@ def _p(x):
 
 def _stream(stream):
     if stream is None:
-        import torch
+        # the handle alone: building a Stream object takes 3 us
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -273,7 +280,6 @@ def fa_last_error() -> str:
 # ------------------------------------------------ torch-allocating helpers
 def forward(q, k, v, scale, causal=False, stream=None):
     """q [B,n,H,d], k [B,m,Hkv,d], v [B,m,Hkv,dv] bf16 CUDA tensors -> (o bf16, lse fp32 [B,H,n])."""
-    import torch
     B, n, H, d = q.shape
     _, m, Hkv, dv = v.shape
     o = torch.empty((B, n, H, dv), dtype=torch.bfloat16, device=q.device)
@@ -284,7 +290,6 @@ def forward(q, k, v, scale, causal=False, stream=None):
 
 def forward_fp8(q, k, v, scale, q_descale, k_descale, v_descale, causal=False, stream=None):
     """e4m3 q [B,n,H,d], k/v [B,m,Hkv,d] (uint8 or float8 tensors) -> (o bf16, lse fp32)."""
-    import torch
     B, n, H, d = q.shape
     _, m, Hkv, dv = v.shape
     o = torch.empty((B, n, H, dv), dtype=torch.bfloat16, device=q.device)
@@ -295,7 +300,6 @@ def forward_fp8(q, k, v, scale, q_descale, k_descale, v_descale, causal=False, s
 
 
 def forward_f32(q, k, v, scale, causal=False, stream=None):
-    import torch
     B, n, H, d = q.shape
     _, m, Hkv, dv = v.shape
     o = torch.empty((B, n, H, dv), dtype=torch.float32, device=q.device)
@@ -307,7 +311,6 @@ def forward_f32(q, k, v, scale, causal=False, stream=None):
 def forward_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale,
                    causal=True, stream=None):
     """Packed q [Tq,H,d], k/v [Tk,Hkv,d] -> (o [Tq,H,dv] bf16, lse [H,Tq] fp32)."""
-    import torch
     Tq, H, d = q.shape
     Tk, Hkv, dv = v.shape
     S = cu_seqlens_q.shape[0] - 1
@@ -321,12 +324,11 @@ def forward_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen
 def forward_window(q, k, v, scale, window, sinks=0, stream=None):
     """q [B,n,H,d], k/v [B,m,Hkv,d] bf16, causal under a sliding window with sinks
     -> (o [B,n,H,d] bf16, lse [B,H,n] fp32)."""
-    import torch
     B, n, H, d = q.shape
     m, Hkv = k.shape[1:3]
-    _tensors("forward_window", q, q=(q, torch.bfloat16, (B, n, H, d)),
-             k=(k, torch.bfloat16, (B, m, Hkv, d)), v=(v, torch.bfloat16, (B, m, Hkv, d)))
-    o = torch.empty((B, n, H, d), dtype=torch.bfloat16, device=q.device)
+    _tensors("forward_window", q.get_device(), ("q", q, torch.bfloat16, (B, n, H, d)),
+             ("k", k, torch.bfloat16, (B, m, Hkv, d)), ("v", v, torch.bfloat16, (B, m, Hkv, d)))
+    o = torch.empty_like(q)
     lse = torch.empty((B, H, n), dtype=torch.float32, device=q.device)
     fa_forward_window(q, k, v, o, lse, B, H, Hkv, n, m, d, d, scale, window, sinks, stream)
     return o, lse
@@ -336,15 +338,14 @@ def forward_varlen_window(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max
                           window, sinks=0, stream=None):
     """Packed q [Tq,H,d], k/v [Tk,Hkv,d] bf16, causal under a sliding window with sinks
     -> (o [Tq,H,d] bf16, lse [H,Tq] fp32)."""
-    import torch
     Tq, H, d = q.shape
     Tk, Hkv = k.shape[:2]
     S = cu_seqlens_q.shape[0] - 1
-    _tensors("forward_varlen_window", q, q=(q, torch.bfloat16, (Tq, H, d)),
-             k=(k, torch.bfloat16, (Tk, Hkv, d)), v=(v, torch.bfloat16, (Tk, Hkv, d)),
-             cu_seqlens_q=(cu_seqlens_q, torch.int32, (S + 1,)),
-             cu_seqlens_k=(cu_seqlens_k, torch.int32, (S + 1,)))
-    o = torch.empty((Tq, H, d), dtype=torch.bfloat16, device=q.device)
+    _tensors("forward_varlen_window", q.get_device(), ("q", q, torch.bfloat16, (Tq, H, d)),
+             ("k", k, torch.bfloat16, (Tk, Hkv, d)), ("v", v, torch.bfloat16, (Tk, Hkv, d)),
+             ("cu_seqlens_q", cu_seqlens_q, torch.int32, (S + 1,)),
+             ("cu_seqlens_k", cu_seqlens_k, torch.int32, (S + 1,)))
+    o = torch.empty_like(q)
     lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
     fa_forward_varlen_window(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, S, Tq, Tk, max_seqlen_q,
                              max_seqlen_k, H, Hkv, d, d, scale, window, sinks, stream)
@@ -354,7 +355,6 @@ def forward_varlen_window(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max
 def paged_prefill(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, max_seqlen_q, scale,
                   causal=True, stream=None):
     """q [Tq,H,d] packed by cu_seqlens_q; caches [P,Hkv,page,d] -> (o [Tq,H,dv], lse [H,Tq])."""
-    import torch
     Tq, H, d = q.shape
     P, Hkv, page, dv = v_cache.shape
     S = cu_seqlens_q.shape[0] - 1
@@ -369,7 +369,6 @@ def paged_prefill(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, max_
 def paged_decode(q, k_cache, v_cache, block_table, seq_lens, num_splits, scale, workspace=None,
                  stream=None):
     """q [S,H,d]; caches [P,Hkv,page,d]; block_table [S,max_blocks] int32; seq_lens [S] int32."""
-    import torch
     S, H, d = q.shape
     P, Hkv, page, dv = v_cache.shape
     need = fa_paged_decode_workspace_size(S, H, dv, num_splits)
@@ -386,7 +385,6 @@ def paged_decode_fused(q, k_cache, v_cache, block_table, seq_lens, num_splits, s
                        workspace=None, stream=None):
     """As paged_decode, in one launch; a workspace passed in must have had its
     ticket words zeroed once (a new one is zeroed here)."""
-    import torch
     S, H, d = q.shape
     P, Hkv, page, dv = v_cache.shape
     need = fa_paged_decode_workspace_size(S, H, dv, num_splits)
@@ -400,54 +398,70 @@ def paged_decode_fused(q, k_cache, v_cache, block_table, seq_lens, num_splits, s
     return o, lse
 
 
-def _tensors(fn, like, **named):
-    """Refuse tensors the C entry could not tell apart from good ones: another
-    device than `like`, another type, or (contiguous ones) a gap in memory.
-    Each argument is (tensor, bytes per element or dtype, shape or None)."""
-    import torch
-    if not like.is_cuda or like.device.index != torch.cuda.current_device():
-        raise FaError(FA_ERR_INVALID_ARG, f"{fn}: the tensors are on {like.device}, the current "
-                                          f"device is cuda:{torch.cuda.current_device()}")
-    for name, (t, kind, shape) in named.items():
-        if t.device != like.device:
-            raise FaError(FA_ERR_INVALID_ARG, f"{fn}: {name} is on {t.device}, not {like.device}")
-        if (t.element_size() != 1 or t.dtype is torch.bool) if kind == 1 else t.dtype is not kind:
+def _refuse(fn, device, *named):
+    """Raise for the first of (name, tensor, type, shape) that is not a contiguous CUDA tensor of
+    that type (1: any one-byte type) and shape on the current device: the C entry sees only its
+    address."""
+    current = torch.cuda.current_device()
+    if device != current:
+        raise FaError(FA_ERR_INVALID_ARG, f"{fn}: the tensors are on device {device}, the current "
+                                          f"one is {current}")
+    for name, t, kind, shape in named:
+        if t.get_device() != device:
+            raise FaError(FA_ERR_INVALID_ARG, f"{fn}: {name} is on {t.device}, not cuda:{device}")
+        if t.dtype is not kind and not (kind == 1 and t.element_size() == 1 and t.dtype is not torch.bool):
             raise FaError(FA_ERR_INVALID_ARG, f"{fn}: {name} has type {t.dtype}")
-        if shape is not None and (tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        if t.shape != shape or not t.is_contiguous():
             raise FaError(FA_ERR_INVALID_ARG, f"{fn}: {name} has shape {tuple(t.shape)} and strides "
                                               f"{t.stride()}, wanted contiguous {tuple(shape)}")
 
 
-def _e4m3_cache(fn, like, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens):
+def _tensors(fn, device, *named):
+    """_refuse, for calls on the serving path: good tensors pass in 0.3 us each."""
+    ok = device == torch.cuda.current_device()
+    for _, t, kind, shape in named:
+        ok = ok and (t.dtype is kind or kind == 1) and t.shape == shape and \
+            t.get_device() == device and t.is_contiguous()
+        if kind == 1:
+            ok = ok and t.element_size() == 1 and t.dtype is not torch.bool
+    if not ok:
+        _refuse(fn, device, *named)
+
+
+def _e4m3_cache(fn, device, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens):
     """Checks of the paged e4m3 cache's tensors -> (pages, Hkv, page, d, sequences, max_blocks)."""
-    import torch
-    P, Hkv, page, d = k_cache.shape
-    S, max_blocks = block_table.shape
-    _tensors(fn, like, k_cache=(k_cache, 1, (P, Hkv, page, d)), v_cache=(v_cache, 1, (P, Hkv, page, d)),
-             k_scale=(k_scale, 1, (P, Hkv, page)), v_scale=(v_scale, 1, (P, Hkv, page)),
-             block_table=(block_table, torch.int32, (S, max_blocks)),
-             seq_lens=(seq_lens, torch.int32, (S,)))
-    return P, Hkv, page, d, S, max_blocks
+    shape = k_cache.shape
+    table = block_table.shape
+    if len(shape) != 4 or len(table) != 2:
+        raise FaError(FA_ERR_INVALID_ARG, f"{fn}: k_cache has shape {tuple(shape)}, block_table "
+                                          f"{tuple(table)}, wanted 4 and 2 dimensions")
+    rows = shape[:3]
+    _tensors(fn, device, ("k_cache", k_cache, 1, shape), ("v_cache", v_cache, 1, shape),
+             ("k_scale", k_scale, 1, rows), ("v_scale", v_scale, 1, rows),
+             ("block_table", block_table, torch.int32, table),
+             ("seq_lens", seq_lens, torch.int32, table[:1]))
+    return (*shape, *table)
 
 
 def paged_kv_write_e4m3(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                         cu_seqlens, stream=None):
     """Quantise new rows k, v [T,Hkv,d] bf16 (token strides may be larger than Hkv*d) into the
     cache [P,Hkv,16,d] (float8_e4m3fn or any 1-byte type) and its scale bytes [P,Hkv,16]."""
-    import torch
     fn = "paged_kv_write_e4m3"
-    P, Hkv, page, d, S, max_blocks = _e4m3_cache(fn, k, k_cache, v_cache, k_scale, v_scale,
+    device = k.get_device()
+    P, Hkv, page, d, S, max_blocks = _e4m3_cache(fn, device, k_cache, v_cache, k_scale, v_scale,
                                                  block_table, seq_lens)
-    _tensors(fn, k, k=(k, torch.bfloat16, None), v=(v, torch.bfloat16, None),
-             cu_seqlens=(cu_seqlens, torch.int32, (S + 1,)))
+    _tensors(fn, device, ("cu_seqlens", cu_seqlens, torch.int32, (S + 1,)))
     T = k.shape[0]
     strides = []
     for name, t in (("k", k), ("v", v)):
-        if tuple(t.shape) != (T, Hkv, d) or t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != d):
-            raise FaError(FA_ERR_INVALID_ARG, f"{fn}: {name} has shape {tuple(t.shape)} and "
-                                              f"strides {t.stride()}, wanted {(T, Hkv, d)} with "
-                                              f"dense heads")
-        strides.append(t.stride(0) if T > 1 else max(t.stride(0), Hkv * d) // 8 * 8)
+        st = t.stride()
+        if t.shape != (T, Hkv, d) or st[2] != 1 or (Hkv > 1 and st[1] != d) or \
+                t.dtype is not torch.bfloat16 or t.get_device() != device:
+            raise FaError(FA_ERR_INVALID_ARG, f"{fn}: {name} is {t.dtype} on {t.device} of shape "
+                                              f"{tuple(t.shape)} and strides {st}, wanted bf16 "
+                                              f"{(T, Hkv, d)} with dense heads")
+        strides.append(st[0] if T > 1 else Hkv * d)
     fa_paged_kv_write_e4m3(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                            cu_seqlens, S, T, Hkv, d, strides[0], strides[1], page, P, max_blocks,
                            stream)
@@ -456,13 +470,13 @@ def paged_kv_write_e4m3(k, v, k_cache, v_cache, k_scale, v_scale, block_table, s
 def paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens,
                        total, stream=None):
     """The last n_s cached rows of every sequence -> (k, v) [total,Hkv,d] bf16."""
-    import torch
     fn = "paged_kv_read_e4m3"
-    P, Hkv, page, d, S, max_blocks = _e4m3_cache(fn, k_cache, k_cache, v_cache, k_scale, v_scale,
+    device = k_cache.get_device()
+    P, Hkv, page, d, S, max_blocks = _e4m3_cache(fn, device, k_cache, v_cache, k_scale, v_scale,
                                                  block_table, seq_lens)
-    _tensors(fn, k_cache, cu_seqlens=(cu_seqlens, torch.int32, (S + 1,)))
+    _tensors(fn, device, ("cu_seqlens", cu_seqlens, torch.int32, (S + 1,)))
     k = torch.empty((total, Hkv, d), dtype=torch.bfloat16, device=k_cache.device)
-    v = torch.empty((total, Hkv, d), dtype=torch.bfloat16, device=k_cache.device)
+    v = torch.empty_like(k)
     fa_paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, k,
                           v, S, total, Hkv, d, page, P, max_blocks, stream)
     return k, v
@@ -471,13 +485,13 @@ def paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
 def paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale,
                       window=0, sinks=0, stream=None):
     """q [S,H,d]; e4m3 cache [P,Hkv,16,d] with scale bytes [P,Hkv,16] -> (o [S,H,d], lse [S,H])."""
-    import torch
     fn = "paged_decode_e4m3"
-    P, Hkv, page, d, S, max_blocks = _e4m3_cache(fn, q, k_cache, v_cache, k_scale, v_scale,
+    device = q.get_device()
+    P, Hkv, page, d, S, max_blocks = _e4m3_cache(fn, device, k_cache, v_cache, k_scale, v_scale,
                                                  block_table, seq_lens)
     H = q.shape[1]
-    _tensors(fn, q, q=(q, torch.bfloat16, (S, H, d)))
-    o = torch.empty((S, H, d), dtype=torch.bfloat16, device=q.device)
+    _tensors(fn, device, ("q", q, torch.bfloat16, (S, H, d)))
+    o = torch.empty_like(q)
     lse = torch.empty((S, H), dtype=torch.float32, device=q.device)
     fa_paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse, S,
                          H, Hkv, d, page, P, max_blocks, scale, window, sinks, stream)
@@ -487,14 +501,14 @@ def paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_le
 def paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens_q,
                        max_seqlen_q, scale, causal=True, window=0, sinks=0, stream=None):
     """q [Tq,H,d] packed by cu_seqlens_q over the e4m3 cache -> (o [Tq,H,d], lse [H,Tq])."""
-    import torch
     fn = "paged_prefill_e4m3"
-    P, Hkv, page, d, S, max_blocks = _e4m3_cache(fn, q, k_cache, v_cache, k_scale, v_scale,
+    device = q.get_device()
+    P, Hkv, page, d, S, max_blocks = _e4m3_cache(fn, device, k_cache, v_cache, k_scale, v_scale,
                                                  block_table, seq_lens)
     Tq, H = q.shape[:2]
-    _tensors(fn, q, q=(q, torch.bfloat16, (Tq, H, d)),
-             cu_seqlens_q=(cu_seqlens_q, torch.int32, (S + 1,)))
-    o = torch.empty((Tq, H, d), dtype=torch.bfloat16, device=q.device)
+    _tensors(fn, device, ("q", q, torch.bfloat16, (Tq, H, d)),
+             ("cu_seqlens_q", cu_seqlens_q, torch.int32, (S + 1,)))
+    o = torch.empty_like(q)
     lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
     fa_paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                           cu_seqlens_q, o, lse, S, Tq, max_seqlen_q, H, Hkv, d, page, P,
@@ -503,7 +517,6 @@ def paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_l
 
 
 def split_combine(part_m, part_l, part_o, stream=None):
-    import torch
     S, H, X, dv = part_o.shape
     o = torch.empty((S, H, dv), dtype=torch.bfloat16, device=part_o.device)
     lse = torch.empty((S, H), dtype=torch.float32, device=part_o.device)
@@ -513,7 +526,6 @@ def split_combine(part_m, part_l, part_o, stream=None):
 
 def decode_workspace_views(workspace, num_seqs, H, dv, num_splits):
     """Views (part_m, part_l, part_o) of a decode workspace, for inspection."""
-    import torch
 
     def r256(x):
         return (x + 255) // 256 * 256
