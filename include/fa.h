@@ -410,9 +410,16 @@ fa_status fa_paged_kv_read_e4m3(const void* k_cache, const void* v_cache, const 
                                 int max_blocks_per_seq, void* stream);
 
 /*
+ * fa_paged_e4m3_workspace_size — bytes of the optional workspace of
+ * fa_paged_decode_e4m3 (max_seqlen_q 1) and fa_paged_prefill_e4m3: split
+ * partials of a few long sequences.  0 where the calls use none (more than 32 rows
+ * max_seqlen_q * H / Hkv, more than 1024 sequences) or for invalid sizes.
+ */
+size_t fa_paged_e4m3_workspace_size(int num_seqs, int max_seqlen_q, int H, int Hkv, int d);
+
+/*
  * fa_paged_decode_e4m3 — one query token per sequence against the e4m3 paged
- * cache, grouped heads, split over the warps of thread-block clusters and
- * merged there: one launch, no workspace.
+ * cache, grouped heads, split-KV.
  * Passage: as fa_paged_decode ("S12 FlashAttention", 实现, 组合, 它还解锁了什么
  * and 练习 1).
  *   q       bf16 [num_seqs][H][d]
@@ -422,6 +429,13 @@ fa_status fa_paged_kv_read_e4m3(const void* k_cache, const void* v_cache, const 
  *           last w keys, itself among them, and the first `sinks` keys
  *   sinks   keys from the start that stay visible under a window (ignored
  *           without one)
+ *   workspace  device scratch of at least fa_paged_e4m3_workspace_size() bytes,
+ *           256-byte aligned, or NULL.  A call normally runs in one launch, a
+ *           thread-block cluster per (sequence, kv head) that splits the keys
+ *           and merges; with a workspace, a few long sequences are instead cut
+ *           into equal shares for every warp of the GPU, with a merge launch
+ *           behind.  The workspace needs no initialisation; calls on one
+ *           workspace must not overlap on the GPU.
  * Only pages that hold a visible key are looked up in the block table: ids of
  * the others may be anything.  Cache contents of keys no query sees are never
  * used, NaN included.  Device status as fa_paged_decode (bad page ids are
@@ -435,7 +449,7 @@ fa_status fa_paged_decode_e4m3(const void* q, const void* k_cache, const void* v
                                const int* seq_lens, void* o, float* lse, int num_seqs, int H,
                                int Hkv, int d, int page_size, int num_pages,
                                int max_blocks_per_seq, float scale, int window, int sinks,
-                               void* stream);
+                               void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * fa_paged_prefill_e4m3 — several new query tokens per sequence against the
@@ -445,6 +459,7 @@ fa_status fa_paged_decode_e4m3(const void* q, const void* k_cache, const void* v
  *   window, sinks  as fa_paged_decode_e4m3, for each query from its own
  *                  position p: keys j <= p with j > p - window or j < sinks;
  *                  a window needs causal = 1
+ *   workspace      as fa_paged_decode_e4m3
  * A sequence with bad offsets, more than max_seqlen_q queries or a bad
  * seq_lens[s] is skipped (its rows are not written) and sets
  * FA_ERR_INVALID_ARG.  Bad page ids set FA_ERR_BAD_BLOCK_TABLE; the sequence's
@@ -461,7 +476,8 @@ fa_status fa_paged_prefill_e4m3(const void* q, const void* k_cache, const void* 
                                 const int* seq_lens, const int* cu_seqlens_q, void* o, float* lse,
                                 int num_seqs, int total_q, int max_seqlen_q, int H, int Hkv, int d,
                                 int page_size, int num_pages, int max_blocks_per_seq, float scale,
-                                int causal, int window, int sinks, void* stream);
+                                int causal, int window, int sinks, void* workspace,
+                                size_t workspace_bytes, void* stream);
 
 /*
  * fa_split_combine — merge per-split partial triples with the recurrence's

@@ -32,20 +32,22 @@ def _read(lib, **kw):
 
 
 def _decode(lib, **kw):
-    a = dict(CACHE, q=16, o=16, lse=16, H=32, scale=0.1, win=0, sinks=0)
+    a = dict(CACHE, q=16, o=16, lse=16, H=32, scale=0.1, win=0, sinks=0, ws=None, wsb=0)
     a.update(kw)
     return lib.fa_paged_decode_e4m3(a["q"], a["kc"], a["vc"], a["ks"], a["vs"], a["bt"], a["sl"],
                                     a["o"], a["lse"], a["S"], a["H"], a["Hkv"], a["d"], a["page"],
-                                    a["P"], a["maxb"], a["scale"], a["win"], a["sinks"], None)
+                                    a["P"], a["maxb"], a["scale"], a["win"], a["sinks"], a["ws"],
+                                    a["wsb"], None)
 
 
 def _prefill(lib, **kw):
-    a = dict(CACHE, q=16, o=16, lse=16, cu=16, T=10, mq=4, H=32, scale=0.1, causal=1, win=0, sinks=0)
+    a = dict(CACHE, q=16, o=16, lse=16, cu=16, T=10, mq=4, H=32, scale=0.1, causal=1, win=0, sinks=0,
+             ws=None, wsb=0)
     a.update(kw)
     return lib.fa_paged_prefill_e4m3(a["q"], a["kc"], a["vc"], a["ks"], a["vs"], a["bt"], a["sl"],
                                      a["cu"], a["o"], a["lse"], a["S"], a["T"], a["mq"], a["H"],
                                      a["Hkv"], a["d"], a["page"], a["P"], a["maxb"], a["scale"],
-                                     a["causal"], a["win"], a["sinks"], None)
+                                     a["causal"], a["win"], a["sinks"], a["ws"], a["wsb"], None)
 
 
 @pytest.mark.parametrize("call", [_write, _read, _decode, _prefill])
@@ -79,6 +81,10 @@ def test_attention_refusals(lib, call):
                dict(scale=float("inf")), dict(win=-1), dict(sinks=-1)):
         assert call(lib, **kw) == fb.FA_ERR_INVALID_ARG, kw
     assert call(lib, H=8 * 33) == fb.FA_ERR_UNSUPPORTED       # group of 33
+    need = fb.fa_paged_e4m3_workspace_size(4, 4 if call is _prefill else 1, 32, 8, 128)
+    assert need > 0
+    assert call(lib, ws=256, wsb=need - 1) == fb.FA_ERR_WORKSPACE
+    assert call(lib, ws=272, wsb=need) == fb.FA_ERR_WORKSPACE   # not 256-byte aligned
     assert call(lib, S=1 << 24, T=1 << 24) == fb.FA_ERR_UNSUPPORTED
 
 
@@ -130,3 +136,14 @@ def test_window_sizes(lib):
     assert _varwin(lib, Tq=0) == fb.FA_OK
     assert _varwin(lib, mq=0) == fb.FA_OK
     assert _varwin(lib, Tq=1 << 30, mq=1 << 30) == fb.FA_ERR_UNSUPPORTED
+
+
+def test_workspace_size(lib):
+    size = fb.fa_paged_e4m3_workspace_size
+    # (warps of one wave + units) x rows x (d values of O; m, r, l and a gap), and page counts
+    assert size(64, 1, 32, 8, 128) == (152 * 3 * 4 + 64 * 8) * 8 * 132 * 4 + 1025 * 4
+    assert size(64, 4, 32, 8, 128) == (152 * 2 * 4 + 64 * 8) * 16 * 132 * 4 + 1025 * 4
+    assert size(3, 1, 9, 1, 64) == (152 * 2 * 4 + 3) * 16 * 68 * 4 + 1025 * 4
+    for bad in ((0, 1, 32, 8, 128), (4, 0, 32, 8, 128), (4, 1, 30, 8, 128), (4, 1, 32, 8, 96),
+                (4, 9, 32, 8, 128), (1025, 1, 32, 8, 128), (-1, 1, 8, 8, 64)):
+        assert size(*bad) == 0

@@ -238,6 +238,92 @@ def test_decode_batch_sizes(num_seqs):
     assert fb.fa_get_device_status() == 0
 
 
+@pytest.mark.parametrize("d,group", [(128, 4), (64, 2), (128, 12), (64, 20)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (900, 5)])
+def test_decode_shares_of_a_few_long_sequences(d, group, window, sinks):
+    """A few long sequences cut into equal shares (with a workspace): a warp's piece starts and ends
+    anywhere and may span several units, where the lengths are short; and the same without one."""
+    rng = np.random.default_rng(d + group)
+    lens, Hkv = [20, 3000, 0, 1, 17, 4096], 3
+    c = _cache(rng, lens, Hkv, d, max_blocks=400)
+    q = E.bf16(rng.standard_normal((len(lens), Hkv * group, d)))[0]
+    scale, t = E.softmax_scale(d), c.gpu()
+    _decode_check(c, q, window, sinks)
+    S, H = q.shape[:2]
+    o = torch.full((S, H, d), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((S, H), device="cuda")
+    fb.fa_paged_decode_e4m3(q.cuda(), *t, o, lse, S, H, Hkv, d, 16, c.num_pages, 400, scale, window,
+                            sinks)                       # no workspace: clusters
+    qd = q.double().numpy()
+    for s in range(S):
+        ref = E.attend(qd[s:s + 1], c.rows["k"][s], c.rows["v"][s], scale, True, window, sinks, c.vexp[s])
+        E.check(_f64(o[s:s + 1]), _f64(lse[s:s + 1]), ref, d, W_ROUND)
+    assert fb.fa_get_device_status() == 0
+
+
+@pytest.mark.parametrize("num_seqs,lo,hi,window", [(20, 300, 3000, 0), (80, 40, 600, 0), (80, 700, 800, 300)])
+def test_decode_batches_of_many_units(num_seqs, lo, hi, window):
+    """Units by the hundred: clusters of several sizes, longest first."""
+    rng = np.random.default_rng(num_seqs + lo)
+    lens = rng.integers(lo, hi, num_seqs)
+    c = _cache(rng, lens, 8, 128, max_blocks=200)
+    q = E.bf16(rng.standard_normal((num_seqs, 16, 128)))[0]
+    _decode_check(c, q, window, 4)
+    assert fb.fa_get_device_status() == 0
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 3)])
+def test_one_long_sequence_is_shared_by_every_warp(window, sinks):
+    rng = np.random.default_rng(50)
+    c = _cache(rng, [20001], 1, 128, max_blocks=10000)
+    q = E.bf16(rng.standard_normal((1, 4, 128)))[0]
+    _decode_check(c, q, window, sinks)
+    q = E.bf16(rng.standard_normal((5, 4, 128)))[0]
+    _chunk_check(c, q, [5], True, window, sinks)
+    assert fb.fa_get_device_status() == 0
+
+
+def test_shares_of_short_chunks_skip_bad_sequences():
+    """As the cluster form: bad sequences set the status and leave their rows alone."""
+    rng = np.random.default_rng(51)
+    new = np.array([3, 0, 4, 1, 2, 4])
+    lens = rng.integers(900, 2500, 6)
+    c = _cache(rng, lens, 2, 128, max_blocks=160)
+    q = E.bf16(rng.standard_normal((int(new.sum()), 8, 128)))[0]
+    _chunk_check(c, q, list(new), True, 400, 4)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    t = c.gpu()
+    t[5][2], t[5][4] = 160 * 16 + 1, -5
+    t[4][0, 3] = c.num_pages
+    ws = torch.empty(fb.fa_paged_e4m3_workspace_size(6, 4, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    o = torch.full((int(cu[-1]), 8, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((8, int(cu[-1])), 9.0, device="cuda")
+    for i in range(2):
+        fb.fa_paged_prefill_e4m3(q.cuda(), *t, _i32(cu), o, lse, 6, int(cu[-1]), 4, 8, 2, 128, 16,
+                                 c.num_pages, 160, 0.1, workspace=ws, workspace_bytes=ws.numel())
+        assert fb.fa_get_device_status() in (fb.FA_ERR_INVALID_ARG, fb.FA_ERR_BAD_BLOCK_TABLE)
+        for s in range(6):
+            r = slice(cu[s], cu[s + 1])
+            if s in (2, 4):
+                assert (o[r] == 9.0).all() and (lse[:, r] == 9.0).all()
+            elif s != 0:
+                ref = E.attend(q[r].double().numpy(), c.rows["k"][s], c.rows["v"][s],
+                               float(np.float32(0.1)), True, 0, 0, c.vexp[s])
+                E.check(_f64(o[r]), _f64(lse[:, r]).T, ref, 128, W_ROUND, f"sequence {s}")
+
+
+def test_timeout_in_a_share_is_recorded(monkeypatch):
+    rng = np.random.default_rng(52)
+    c = _cache(rng, [900] * 4, 8, 64, max_blocks=200)
+    q = E.bf16(rng.standard_normal((4, 8, 64)))[0]
+    monkeypatch.setenv("FA_TEST_FORCE_WAIT_TIMEOUT", "1")
+    fb.paged_decode_e4m3(q.cuda(), *c.gpu(), 0.1)
+    assert fb.fa_get_device_status() == fb.FA_ERR_TIMEOUT
+    monkeypatch.delenv("FA_TEST_FORCE_WAIT_TIMEOUT")
+    _decode_check(c, q)
+    assert fb.fa_get_device_status() == 0
+
+
 def test_hidden_keys_are_never_used():
     """NaN codes and infinite scales outside the window and the sinks, and freed pages (table
     entries -1 or past the pool) there, change nothing and set no status."""

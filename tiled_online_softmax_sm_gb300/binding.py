@@ -38,8 +38,8 @@ EXPORTED = ("fa_forward", "fa_forward_fp8", "fa_forward_f32", "fa_forward_varlen
             "fa_paged_decode_workspace_size",
             "fa_paged_decode", "fa_paged_decode_fused", "fa_paged_decode_noalloc", "fa_paged_gather", "fa_split_combine",
             "fa_forward_window", "fa_forward_varlen_window",
-            "fa_paged_kv_write_e4m3", "fa_paged_kv_read_e4m3", "fa_paged_decode_e4m3",
-            "fa_paged_prefill_e4m3",
+            "fa_paged_kv_write_e4m3", "fa_paged_kv_read_e4m3", "fa_paged_e4m3_workspace_size",
+            "fa_paged_decode_e4m3", "fa_paged_prefill_e4m3",
             "fa_last_error",
             "fa_get_device_status")
 FA_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -85,8 +85,10 @@ def load(path: str = LIB_PATH):
         LL = ctypes.c_longlong
         lib.fa_paged_kv_write_e4m3.argtypes = [P] * 9 + [I, I, I, I, LL, LL, I, I, I, P]
         lib.fa_paged_kv_read_e4m3.argtypes = [P] * 9 + [I, I, I, I, I, I, I, P]
-        lib.fa_paged_decode_e4m3.argtypes = [P] * 9 + [I, I, I, I, I, I, I, F, I, I, P]
-        lib.fa_paged_prefill_e4m3.argtypes = [P] * 10 + [I, I, I, I, I, I, I, I, I, F, I, I, I, P]
+        lib.fa_paged_decode_e4m3.argtypes = [P] * 9 + [I, I, I, I, I, I, I, F, I, I, P, Z, P]
+        lib.fa_paged_prefill_e4m3.argtypes = [P] * 10 + [I, I, I, I, I, I, I, I, I, F, I, I, I, P, Z, P]
+        lib.fa_paged_e4m3_workspace_size.argtypes = [I] * 5
+        lib.fa_paged_e4m3_workspace_size.restype = Z
         lib.fa_last_error.argtypes = []
         lib.fa_last_error.restype = ctypes.c_char_p
         lib.fa_get_device_status.argtypes = [P, ctypes.POINTER(I)]
@@ -241,24 +243,30 @@ def fa_paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_l
                                         max_blocks_per_seq, _stream(stream)))
 
 
+def fa_paged_e4m3_workspace_size(num_seqs, max_seqlen_q, H, Hkv, d) -> int:
+    return int(load().fa_paged_e4m3_workspace_size(num_seqs, max_seqlen_q, H, Hkv, d))
+
+
 def fa_paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse,
                          num_seqs, H, Hkv, d, page_size, num_pages, max_blocks_per_seq, scale,
-                         window=0, sinks=0, stream=None):
+                         window=0, sinks=0, workspace=None, workspace_bytes=0, stream=None):
     _check(load().fa_paged_decode_e4m3(_p(q), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale),
                                        _p(block_table), _p(seq_lens), _p(o), _p(lse), num_seqs, H,
                                        Hkv, d, page_size, num_pages, max_blocks_per_seq,
-                                       float(scale), int(window), int(sinks), _stream(stream)))
+                                       float(scale), int(window), int(sinks), _p(workspace),
+                                       int(workspace_bytes), _stream(stream)))
 
 
 def fa_paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                           cu_seqlens_q, o, lse, num_seqs, total_q, max_seqlen_q, H, Hkv, d,
                           page_size, num_pages, max_blocks_per_seq, scale, causal=True, window=0,
-                          sinks=0, stream=None):
+                          sinks=0, workspace=None, workspace_bytes=0, stream=None):
     _check(load().fa_paged_prefill_e4m3(_p(q), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale),
                                         _p(block_table), _p(seq_lens), _p(cu_seqlens_q), _p(o),
                                         _p(lse), num_seqs, total_q, max_seqlen_q, H, Hkv, d,
                                         page_size, num_pages, max_blocks_per_seq, float(scale),
-                                        int(causal), int(window), int(sinks), _stream(stream)))
+                                        int(causal), int(window), int(sinks), _p(workspace),
+                                        int(workspace_bytes), _stream(stream)))
 
 
 def fa_split_combine(part_m, part_l, part_o, o, lse, num_seqs, H, num_splits, dv, stream=None):
@@ -482,8 +490,17 @@ def paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
     return k, v
 
 
+def _e4m3_workspace(workspace, device, S, max_q, H, Hkv, d, max_blocks):
+    """The caller's workspace, a new one for a few long sequences, or none."""
+    if workspace is None and S * Hkv <= 38 and max_blocks >= 128:
+        need = fa_paged_e4m3_workspace_size(S, max_q, H, Hkv, d)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel()
+
+
 def paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale,
-                      window=0, sinks=0, stream=None):
+                      window=0, sinks=0, workspace=None, stream=None):
     """q [S,H,d]; e4m3 cache [P,Hkv,16,d] with scale bytes [P,Hkv,16] -> (o [S,H,d], lse [S,H])."""
     fn = "paged_decode_e4m3"
     device = q.get_device()
@@ -493,13 +510,16 @@ def paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_le
     _tensors(fn, device, ("q", q, torch.bfloat16, (S, H, d)))
     o = torch.empty_like(q)
     lse = torch.empty((S, H), dtype=torch.float32, device=q.device)
+    workspace, size = _e4m3_workspace(workspace, q.device, S, 1, H, Hkv, d, max_blocks)
     fa_paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse, S,
-                         H, Hkv, d, page, P, max_blocks, scale, window, sinks, stream)
+                         H, Hkv, d, page, P, max_blocks, scale, window, sinks, workspace, size,
+                         stream)
     return o, lse
 
 
 def paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens_q,
-                       max_seqlen_q, scale, causal=True, window=0, sinks=0, stream=None):
+                       max_seqlen_q, scale, causal=True, window=0, sinks=0, workspace=None,
+                       stream=None):
     """q [Tq,H,d] packed by cu_seqlens_q over the e4m3 cache -> (o [Tq,H,d], lse [H,Tq])."""
     fn = "paged_prefill_e4m3"
     device = q.get_device()
@@ -510,9 +530,10 @@ def paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_l
              ("cu_seqlens_q", cu_seqlens_q, torch.int32, (S + 1,)))
     o = torch.empty_like(q)
     lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
+    workspace, size = _e4m3_workspace(workspace, q.device, S, max_seqlen_q, H, Hkv, d, max_blocks)
     fa_paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                           cu_seqlens_q, o, lse, S, Tq, max_seqlen_q, H, Hkv, d, page, P,
-                          max_blocks, scale, causal, window, sinks, stream)
+                          max_blocks, scale, causal, window, sinks, workspace, size, stream)
     return o, lse
 
 

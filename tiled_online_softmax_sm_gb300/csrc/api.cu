@@ -549,9 +549,27 @@ fa_status check_heads(const char* fn, const void* q, const void* o, const float*
   return FA_OK;
 }
 
+// The workspace of the e4m3 attention entries is optional.
+fa_status check_e4m3_workspace(const char* fn, const void* workspace, size_t bytes, int num_seqs,
+                               int max_q, int H, int Hkv, int d) {
+  if (workspace == nullptr) return FA_OK;
+  const size_t need = fa::rows_e4m3_workspace(num_seqs, max_q, H, Hkv, d);
+  if (bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return fail(FA_ERR_WORKSPACE, "%s: workspace %p of %zu bytes (need %zu, 256-byte aligned)", fn,
+                workspace, bytes, need);
+  return FA_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t fa_paged_e4m3_workspace_size(int num_seqs, int max_seqlen_q, int H, int Hkv, int d) {
+  if (num_seqs <= 0 || max_seqlen_q <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 ||
+      (d != 64 && d != 128))
+    return 0;
+  return fa::rows_e4m3_workspace(num_seqs, max_seqlen_q, H, Hkv, d);
+}
 
 fa_status fa_paged_kv_write_e4m3(const void* k, const void* v, void* k_cache, void* v_cache,
                                  void* k_scale, void* v_scale, const int* block_table,
@@ -610,7 +628,7 @@ fa_status fa_paged_decode_e4m3(const void* q, const void* k_cache, const void* v
                                const int* seq_lens, void* o, float* lse, int num_seqs, int H,
                                int Hkv, int d, int page_size, int num_pages,
                                int max_blocks_per_seq, float scale, int window, int sinks,
-                               void* stream) {
+                               void* workspace, size_t workspace_bytes, void* stream) {
   const char* fn = "fa_paged_decode_e4m3";
   fa_status st = check_heads(fn, q, o, lse, H, Hkv, scale);
   if (st == FA_OK) st = check_window(fn, 1, window, sinks);
@@ -622,11 +640,14 @@ fa_status fa_paged_decode_e4m3(const void* q, const void* k_cache, const void* v
   if (q == nullptr || o == nullptr) return fail(FA_ERR_INVALID_ARG, "%s: null q/o", fn);
   if ((long long)num_seqs * H > 0xfffffffLL)
     return fail(FA_ERR_UNSUPPORTED, "%s: num_seqs*H must stay below 2^28", fn);
+  if ((st = check_e4m3_workspace(fn, workspace, workspace_bytes, num_seqs, 1, H, Hkv, d)) != FA_OK)
+    return st;
   int* sp = nullptr;
   if ((st = status_ptr(&sp)) != FA_OK) return st;
   fa::PagedE4m3Params p{q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, nullptr, o,
                         lse, num_seqs, num_seqs, 1, H, Hkv, d, num_pages, max_blocks_per_seq,
                         scale, 1, window, sinks, sp};
+  p.workspace = workspace;
   const char* why = nullptr;
   cudaError_t e = fa::launch_rows_e4m3(p, static_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess) return cuda_fail(e, why ? why : "fa_paged_decode_e4m3 launch");
@@ -638,7 +659,8 @@ fa_status fa_paged_prefill_e4m3(const void* q, const void* k_cache, const void* 
                                 const int* seq_lens, const int* cu_seqlens_q, void* o, float* lse,
                                 int num_seqs, int total_q, int max_seqlen_q, int H, int Hkv, int d,
                                 int page_size, int num_pages, int max_blocks_per_seq, float scale,
-                                int causal, int window, int sinks, void* stream) {
+                                int causal, int window, int sinks, void* workspace,
+                                size_t workspace_bytes, void* stream) {
   const char* fn = "fa_paged_prefill_e4m3";
   fa_status st = check_heads(fn, q, o, lse, H, Hkv, scale);
   if (st != FA_OK) return st;
@@ -654,6 +676,9 @@ fa_status fa_paged_prefill_e4m3(const void* q, const void* k_cache, const void* 
   if (max_seqlen_q > total_q) max_seqlen_q = total_q;   // no sequence has more
   if ((long long)num_seqs * max_seqlen_q * H > 0xfffffffLL)
     return fail(FA_ERR_UNSUPPORTED, "%s: num_seqs*max_seqlen_q*H must stay below 2^28", fn);
+  if ((st = check_e4m3_workspace(fn, workspace, workspace_bytes, num_seqs, max_seqlen_q, H, Hkv,
+                                 d)) != FA_OK)
+    return st;
   int* sp = nullptr;
   if ((st = status_ptr(&sp)) != FA_OK) return st;
   const char* why = nullptr;
@@ -662,6 +687,7 @@ fa_status fa_paged_prefill_e4m3(const void* q, const void* k_cache, const void* 
     fa::PagedE4m3Params p{q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                           cu_seqlens_q, o, lse, num_seqs, total_q, max_seqlen_q, H, Hkv, d,
                           num_pages, max_blocks_per_seq, scale, causal, window, sinks, sp};
+    p.workspace = workspace;
     e = fa::launch_rows_e4m3(p, static_cast<cudaStream_t>(stream), &why);
   } else {
     fa::FwdParams p{q, k_cache, v_cache, o, lse, cu_seqlens_q, nullptr, num_seqs, H, Hkv,

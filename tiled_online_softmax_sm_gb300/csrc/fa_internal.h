@@ -165,12 +165,14 @@ struct PagedE4m3Params {
   float scale;
   int causal, window, sinks; // window 0: none
   int* status;
+  void* workspace = nullptr; // stream form's partials (rows_e4m3_workspace bytes), or null
 };
 
 cudaError_t launch_kv_write_e4m3(const KvRowsParams& p, cudaStream_t stream);
 cudaError_t launch_kv_read_e4m3(const KvRowsParams& p, cudaStream_t stream);
 // Query rows (tokens x grouped heads) of one kv head that the split kernel takes.
 constexpr int kRowsE4m3Max = 32;
+size_t rows_e4m3_workspace(int num_seqs, int max_q, int H, int Hkv, int d);
 cudaError_t launch_rows_e4m3(const PagedE4m3Params& p, cudaStream_t stream, const char** why);
 cudaError_t launch_fwd_f32(const FwdParams& p, cudaStream_t stream);
 cudaError_t launch_fwd_bf16(const FwdParams& p, cudaStream_t stream, const char** why);

@@ -271,7 +271,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 
 // 2^(b - 127) for a scale byte b of 0 .. 254 (b = 0: the fp32 subnormal 2^-127).
 __device__ __forceinline__ float exp2_byte(uint32_t b) {
-  return __uint_as_float(b == 0u ? 0x00400000u : b << 23);
+  return __uint_as_float(max(b << 23, 0x00400000u));
+}
+
+// b - 127 as a float, for a byte b.
+__device__ __forceinline__ float log2_byte(uint32_t b) {
+  return __uint_as_float(0x4b000000u | b) - 8388735.f;   // 2^23 + b, less 2^23 + 127
 }
 
 // 16 e4m3 codes times 2^(b - 127) as 16 bf16, exact in bf16's normal range:
