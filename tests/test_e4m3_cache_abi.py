@@ -142,8 +142,13 @@ def test_workspace_size(lib):
     size = fb.fa_paged_e4m3_workspace_size
     # (warps of one wave + units) x rows x (d values of O; m, r, l and a gap), and page counts
     assert size(64, 1, 32, 8, 128) == (152 * 3 * 4 + 64 * 8) * 8 * 132 * 4 + 1025 * 4
-    assert size(64, 4, 32, 8, 128) == (152 * 2 * 4 + 64 * 8) * 16 * 132 * 4 + 1025 * 4
-    assert size(3, 1, 9, 1, 64) == (152 * 2 * 4 + 3) * 16 * 68 * 4 + 1025 * 4
+    assert size(64, 4, 32, 8, 128) == (152 * 3 * 4 + 64 * 8) * 16 * 132 * 4 + 1025 * 4
+    assert size(3, 1, 9, 1, 64) == (152 * 3 * 4 + 3) * 16 * 68 * 4 + 1025 * 4
+    # chunks above 32 rows: units of 256 rows, cut into parts that fill 152 SMs once (one
+    # sequence) or twice, of 256 rows x (d values of O; m, l, l_p and a gap)
+    assert size(1, 64, 32, 8, 128) == 8 * 19 * 256 * 132 * 4
+    assert size(4, 512, 32, 8, 64) == 0
+    assert size(2, 65, 16, 4, 64) == 16 * 19 * 256 * 68 * 4
     for bad in ((0, 1, 32, 8, 128), (4, 0, 32, 8, 128), (4, 1, 30, 8, 128), (4, 1, 32, 8, 96),
-                (4, 9, 32, 8, 128), (1025, 1, 32, 8, 128), (-1, 1, 8, 8, 64)):
+                (1025, 1, 32, 8, 128), (-1, 1, 8, 8, 64)):
         assert size(*bad) == 0

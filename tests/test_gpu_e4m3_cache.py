@@ -413,15 +413,26 @@ def test_decode_timeout_is_recorded_and_the_next_call_runs(monkeypatch):
 
 # --------------------------------------------------------------------- chunks
 def _chunk_check(c, q, new, causal=True, window=0, sinks=0, rounding=W_ROUND, what=""):
+    """With a workspace (the keys of few units are split) and without one."""
     scale = E.softmax_scale(c.d)
     cu = np.concatenate([[0], np.cumsum(new)])
-    o, lse = fb.paged_prefill_e4m3(q.cuda(), *c.gpu(), _i32(cu), int(max(new)), scale,
-                                   causal=causal, window=window, sinks=sinks)
-    o, lse, qd = _f64(o), _f64(lse).T, q.double().numpy()
-    for s in range(len(c.lens)):
-        r = slice(cu[s], cu[s + 1])
-        ref = E.attend(qd[r], c.rows["k"][s], c.rows["v"][s], scale, causal, window, sinks, c.vexp[s])
-        E.check(o[r], lse[r], ref, c.d, rounding, f"{what} sequence {s}")
+    S, (Tq, H, d), mq, t = len(c.lens), q.shape, int(max(new)), c.gpu()
+    refs = []
+    qd = q.double().numpy()
+    for s in range(S):
+        refs.append(E.attend(qd[cu[s]:cu[s + 1]], c.rows["k"][s], c.rows["v"][s], scale, causal, window,
+                             sinks, c.vexp[s]))
+    need = fb.fa_paged_e4m3_workspace_size(S, mq, H, c.Hkv, d)
+    for ws in [None] + ([torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")] if need else []):
+        o = torch.full((Tq, H, d), 9.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((H, Tq), 9.0, device="cuda")
+        fb.fa_paged_prefill_e4m3(q.cuda(), *t, _i32(cu), o, lse, S, Tq, mq, H, c.Hkv, d, 16, c.num_pages,
+                                 c.table.shape[1], scale, causal, window, sinks, ws,
+                                 0 if ws is None else need)
+        o, lse = _f64(o), _f64(lse).T
+        for s in range(S):
+            r = slice(cu[s], cu[s + 1])
+            E.check(o[r], lse[r], refs[s], c.d, rounding, f"{what} sequence {s} workspace {need if ws is not None else 0}")
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -482,10 +493,29 @@ def test_chunk_equals_the_bf16_prefill_of_the_read_back_cache():
         t, cu = c.gpu(), _i32(np.concatenate([[0], np.cumsum(new)]))
         kc, vc = (torch.from_numpy(E.values(c.codes[x], np.where(c.scales[x] == 255, 0, c.scales[x]))
                                    .astype(np.float32)).bfloat16().cuda() for x in "kv")
-        o1, l1 = fb.paged_prefill_e4m3(q, *t, cu, max(new), 0.1)
+        o1, l1 = torch.empty_like(q), torch.empty((4, sum(new)), device="cuda")
+        fb.fa_paged_prefill_e4m3(q, *t, cu, o1, l1, 4, sum(new), max(new), 4, 4, d, 16, c.num_pages,
+                                 c.table.shape[1], 0.1)
         o2, l2 = fb.paged_prefill(q, kc, vc, t[4], t[5], cu, max(new), 0.1)
         assert torch.equal(o1.view(torch.int16), o2.view(torch.int16))
         assert torch.equal(l1.view(torch.int32), l2.view(torch.int32))
+    assert fb.fa_get_device_status() == 0
+
+
+@pytest.mark.parametrize("d,group,new", [(128, 4, [40]), (64, 2, [64]), (128, 1, [90]), (128, 8, [5, 9]),
+                                         (64, 6, [33, 0, 20])])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 5)])
+def test_chunks_split_over_long_contexts(d, group, new, window, sinks):
+    """A chunk of few units whose K/V tiles are cut into parts, merged by a second launch: parts with
+    no tile, parts whose only tile one query tile skips, sequences shorter than the parts are many."""
+    rng = np.random.default_rng(d + group)
+    lens = [5000, 100, 2300][:len(new)]
+    c = _cache(rng, lens, 2, d, max_blocks=320)
+    q = E.bf16(rng.standard_normal((sum(new), 2 * group, d)))[0]
+    assert fb.fa_paged_e4m3_workspace_size(len(new), max(new), 2 * group, 2, d) > 0
+    _chunk_check(c, q, new, True, window, sinks, P_ROUND)
+    if not window:
+        _chunk_check(c, q, new, False, 0, 0, P_ROUND)
     assert fb.fa_get_device_status() == 0
 
 

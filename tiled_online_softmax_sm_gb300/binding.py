@@ -491,8 +491,9 @@ def paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
 
 
 def _e4m3_workspace(workspace, device, S, max_q, H, Hkv, d, max_blocks):
-    """The caller's workspace, a new one for a few long sequences, or none."""
-    if workspace is None and S * Hkv <= 38 and max_blocks >= 128:
+    """The caller's workspace, a new one where few units share long sequences, or none."""
+    if workspace is None and max_blocks >= 32 and \
+            (max_q * H > 32 * Hkv or (S * Hkv <= 38 and max_blocks >= 128)):
         need = fa_paged_e4m3_workspace_size(S, max_q, H, Hkv, d)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=device)

@@ -44,8 +44,8 @@ def _headers():
 
 # Kernels that re-split registers with setmaxnreg: the split is sized for
 # exactly this many registers per thread at launch (see the kernel source).
-# (the instances with a fourth warpgroup, last template argument true, launch at 128)
-REQUIRED_REGS = {r"fwd_bf16_kernelI.*Lb0EEEv": 168, r"fwd_bf16_kernelI.*Lb1EEEv": 128}
+# (the instances with a fourth warpgroup, next to last template argument true, launch at 128)
+REQUIRED_REGS = {r"fwd_bf16_kernelI.*Lb0ELb[01]EEEv": 168, r"fwd_bf16_kernelI.*Lb1ELb[01]EEEv": 128}
 
 
 def _check_regs(src: str, ptxas_log: str):

@@ -700,6 +700,7 @@ fa_status fa_paged_prefill_e4m3(const void* q, const void* k_cache, const void* 
     p.sinks = window > 0 ? sinks : 0;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
+    p.workspace = workspace;
     e = fa::launch_fwd_e4m3_cache(p, static_cast<cudaStream_t>(stream), &why);
   }
   if (e != cudaSuccess) return cuda_fail(e, why ? why : "fa_paged_prefill_e4m3 launch");

@@ -92,7 +92,35 @@ struct FwdParams {
   int window = 0, sinks = 0;
   const void* k_scale = nullptr;
   const void* v_scale = nullptr;
+  void* workspace = nullptr;   // e4m3 caches: parts of cut units (cache_parts_bytes), or null
 };
+
+// Heads that share a kv head and are rows of one query tile: the largest power
+// of two that divides the group, at most 128 (its log2).
+inline int packed_heads_log2(int H, int Hkv) {
+  int gl = 0;
+  while (gl < 7 && (H / Hkv) % (2 << gl) == 0) ++gl;
+  return gl;
+}
+
+// Parts that each unit (sequence, head group, pair of query tiles) of a chunk
+// launch over the e4m3 cache is cut into: as many as fill the SMs where units
+// are few, twice as many for several sequences (whose lengths may differ), and
+// 1 from 152 units on.
+inline int cache_parts(int num_seqs, int max_q, int H, int Hkv) {
+  const int gl = packed_heads_log2(H, Hkv);
+  const long long pair_q = 256 >> gl;
+  const long long units = (long long)num_seqs * (H >> gl) * ((max_q + pair_q - 1) / pair_q);
+  if (units <= 0 || units > 152) return 1;
+  return (int)((num_seqs == 1 ? 152 : 304) / units);
+}
+inline size_t cache_parts_bytes(int num_seqs, int max_q, int H, int Hkv, int d) {
+  const int parts = cache_parts(num_seqs, max_q, H, Hkv);
+  if (parts <= 1) return 0;
+  const int gl = packed_heads_log2(H, Hkv);
+  const long long pair_q = 256 >> gl;
+  return (size_t)num_seqs * (H >> gl) * ((max_q + pair_q - 1) / pair_q) * parts * 256 * (d + 4) * 4;
+}
 
 struct DecodeParams {
   const void* q;

@@ -59,6 +59,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "fa_internal.h"
 #include "ptx.cuh"
 #include "tma_host.h"
@@ -175,7 +177,10 @@ struct Unit {
   // w0 on, rotated by rot, and then the sinks' tiles 0, 1, ...  Tile i skips
   // entry skip[i] (-1: none): tile 0 the last one, when all of it lies behind
   // its rows, tile 1 the first one, when all of it lies before their windows.
+  // KV8 launches of few units cut the list into parts for several CTAs: a part
+  // starts at entry list0 of the whole list, and n_list and skip are the part's.
   int n_list, w0, nw, rot;
+  int list0;
   int skip[2];
   int key_sink, key_lo, key_hi;  // keys some row of the unit sees: [0, key_sink), [key_lo, key_hi)
 };
@@ -186,9 +191,10 @@ __device__ __forceinline__ int list_size(const Unit& U) {
   return WIN ? U.n_list : max(U.n_kv[0], U.n_kv[1]);
 }
 
-template <bool WIN>
+template <bool WIN, bool PARTS = false>
 __device__ __forceinline__ int list_tile(const Unit& U, int j) {
   if (!WIN) return j;
+  if (PARTS) j += U.list0;
   if (j >= U.nw) return j - U.nw;
   const int t = j + U.rot;
   return U.w0 + (t < U.nw ? t : t - U.nw);
@@ -399,6 +405,7 @@ __device__ __forceinline__ Unit make_unit(int b, int h, int t, int H, int Hkv, i
     // or its sums missed, tile after tile.
     // (A unit whose windows reach back to key 0 keeps the plain order.)
     U.rot = lo_last > 0 ? max(0, min(2, U.nw - 2)) : 0;
+    U.list0 = 0;
     U.n_list = U.nw > 0 ? U.nw + min((U.key_sink + kBlockN - 1) / kBlockN, lo[0]) : 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) U.n_kv[i] = hi[i] > 0 ? U.n_list : 0;
@@ -439,6 +446,19 @@ __device__ __forceinline__ Unit split_unit(Unit R, int tile) {
   return U;
 }
 
+// Part x of X of a unit's K/V tile list (WIN).
+__device__ __forceinline__ Unit cut_unit(Unit U, int x, int X) {
+  const int lo = (int)((long long)x * U.n_list / X), hi = (int)((long long)(x + 1) * U.n_list / X);
+  U.list0 = lo;
+  U.n_list = hi - lo;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    U.skip[i] = U.skip[i] >= lo && U.skip[i] < hi ? U.skip[i] - lo : -1;
+    U.n_kv[i] = U.n_kv[i] > 0 && U.n_list > (U.skip[i] >= 0 ? 1 : 0) ? U.n_list : 0;
+  }
+  return U;
+}
+
 // PAGED: K and V come from page caches [pages][Hkv][16][d] through the block
 // table (2-D tensor maps, one 16-row box per page), seq_lens gives each
 // sequence's key count; otherwise K/V are dense or packed rows (3-D maps).
@@ -449,7 +469,10 @@ __device__ __forceinline__ Unit split_unit(Unit R, int tile) {
 // scale byte per row; warp 0 stages them (untiled copies, one per page), warps
 // 12-15 widen them to bf16 (exact) in the ring slots, and the rest of the
 // kernel runs as for a bf16 cache.
-template <int D, bool PAGED, bool FP8, bool VAR, bool WIN = false, bool KV8 = false>
+// PARTS (KV8): units are cut into `parts` parts (see cut_unit), whose states go
+// to part_s and part_o for merge_parts_kernel.
+template <int D, bool PAGED, bool FP8, bool VAR, bool WIN = false, bool KV8 = false,
+          bool PARTS = false>
 __global__ void __launch_bounds__(KV8 ? kThreads8 : kThreads, 1)
 fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, __nv_bfloat16* __restrict__ o,
@@ -460,7 +483,8 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 const int* __restrict__ seq_lens, int max_blocks, int num_pages, float out_scale,
                 int sched_sorted, int num_split, int* status, int window, int sinks, int gl,
                 const uint8_t* __restrict__ raw_k, const uint8_t* __restrict__ raw_v,
-                const uint8_t* __restrict__ k_scale, const uint8_t* __restrict__ v_scale) {
+                const uint8_t* __restrict__ k_scale, const uint8_t* __restrict__ v_scale, int parts,
+                float* __restrict__ part_s, float* __restrict__ part_o) {
   using C = Cfg<D, FP8, KV8>;
   static_assert(!KV8 || (PAGED && VAR && WIN && !FP8), "KV8 instances are paged, with windows");
   extern __shared__ uint8_t smem_raw[];
@@ -535,8 +559,9 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   // Dense: the last num_split pair units (the partial last wave) are run as
   // 2 * num_split split units, one per query tile, so that wave finishes in
   // about half a unit's time.
-  const int num_units = VAR && sched_sorted ? Hg * sh.n_order : BH * num_pairs + (VAR ? 0 : num_split);
-  auto unit_at = [&](int u) {
+  const int num_units =
+      (VAR && sched_sorted ? Hg * sh.n_order : BH * num_pairs + (VAR ? 0 : num_split)) * (PARTS ? parts : 1);
+  auto whole_unit = [&](int u) {
     if (VAR && WIN && sched_sorted == 2) {
       const int c = u / Hg;
       int lo = 0, hi = B - 1;   // the first sequence whose pairs end past c
@@ -557,6 +582,13 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const Unit R = unit_bt(bh / Hg, bh % Hg, num_pairs - 1 - r / BH);
     if constexpr (WIN) return R;
     return u < base ? R : split_unit(R, (u - base) & 1);
+  };
+  auto unit_at = [&](int u) {
+    if constexpr (PARTS) {
+      return cut_unit(whole_unit(u / parts), u % parts, parts);
+    } else {
+      return whole_unit(u);
+    }
   };
 #define FA_UNIT(u) unit_at(u)
   // k-th unit of this CTA: waves of gridDim.x units in snake order (even waves
@@ -781,7 +813,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const int n_kv_max = list_size<WIN>(U);
         if (WIN || !U.split) {
           for (int j = 0; j < n_kv_max && ok; ++j)
-            for (int which = 0; which < 2 && ok; ++which) ok = issue_kv(which, list_tile<WIN>(U, j));  // K then V
+            for (int which = 0; which < 2 && ok; ++which) ok = issue_kv(which, list_tile<WIN, PARTS>(U, j));  // K then V
         } else {
           // the MMA warp's order for a split unit: K_0(0), K_1(0), then per
           // step V_0(j), K_0(j+1), V_1(j), K_1(j+1) (tile i's K/V tiles
@@ -1005,7 +1037,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         if (!U.rows) continue;
         const int n_list = list_size<WIN>(U);
         for (int j2 = 0; j2 < 2 * n_list && ok; ++j2) {
-          const int j = list_tile<WIN>(U, j2 >> 1);
+          const int j = list_tile<WIN, PARTS>(U, j2 >> 1);
           const int slot = lc % C::kStages, rslot = lc % C::kRawStages;
           ok = __all_sync(0xffffffffu,
                           ptx::mbar_wait(bar_rf + 8 * rslot, (lc / C::kRawStages) & 1, status, abort_flag) &&
@@ -1121,7 +1153,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         ptx::tc_fence_after();
         // mask keys past the end and, causal, keys j > qi + (m - n): only tiles
         // that reach past the end or past the tile's first row's diagonal
-        const int k0 = (WIN ? list_tile<WIN>(U, jl) : kv_first + jl) * kBlockN;
+        const int k0 = (WIN ? list_tile<WIN, PARTS>(U, jl) : kv_first + jl) * kBlockN;
         const int diag = q_start + (U.kv_len - U.q_len);   // last key row q_start sees
         bool masked = k0 + kBlockN > U.kv_len || (causal && k0 + kBlockN - 1 > diag);
         int vis = U.kv_len - k0;
@@ -1133,7 +1165,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         bool low = false;
         if constexpr (WIN) {
           if (window > 0) {
-            if (jl >= U.nw) {
+            if ((PARTS ? jl + U.list0 : jl) >= U.nw) {
               vis = min(vis, sinks - k0);
               masked = masked || k0 + kBlockN > sinks;
             } else {
@@ -1366,6 +1398,27 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 #pragma unroll
           for (int e = 0; e < 32; ++e) ov[c][e] = 0u;
       }
+      if constexpr (PARTS) {
+        // this part's state, for the merge behind this kernel: rows are numbered
+        // by (sequence, head group, pair), part and row of the pair
+        const size_t slot =
+            ((((size_t)U.b * Hg + U.h) * num_pairs + U.q_start0 / (2 * kBlockM >> gl)) * parts + u % parts) *
+                (2 * kBlockM) + i * kBlockM + r;
+        if (row_valid) {
+          *reinterpret_cast<float4*>(part_s + slot * 4) = make_float4(m_ref, l_run, l_p, 0.f);
+          if (nkv > 0) {
+            uint4* dst = reinterpret_cast<uint4*>(part_o + slot * D);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+              for (int w = 0; w < 4; ++w)
+                ptx::st_global_v8(dst + c * 8 + w * 2,
+                                  make_uint4(ov[c][8 * w], ov[c][8 * w + 1], ov[c][8 * w + 2], ov[c][8 * w + 3]),
+                                  make_uint4(ov[c][8 * w + 4], ov[c][8 * w + 5], ov[c][8 * w + 6], ov[c][8 * w + 7]));
+          }
+        }
+        continue;
+      }
       // O has total_q * H rows of D (dense: total_q = B * n); LSE as many entries
       if (row_valid && FA_IN_BOUNDS(orow, (size_t)total_q * H, status)) {
         // O's divisor (bf16: the rounded sum, positive exactly when l_run is:
@@ -1402,6 +1455,79 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   }
 }
 
+// KV8: merge of the parts of cut units, one warp per (token, head): with M =
+// max m_x, O = sum 2^(m_x - M) O_x / sum 2^(m_x - M) l_p_x and the LSE from the
+// exact sums, as the split units merge in the kernel.
+template <int D>
+__global__ void __launch_bounds__(256)
+merge_parts_kernel(const float* __restrict__ part_s, const float* __restrict__ part_o,
+                   __nv_bfloat16* __restrict__ o, float* __restrict__ lse,
+                   const int* __restrict__ cu_q, const int* __restrict__ seq_lens, int B, int H,
+                   int total_q, int n, int max_blocks, int num_pairs, int parts, int gl, int* status) {
+  constexpr int kVec = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long t = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (t >= (long long)total_q * H) return;
+  const int tok = (int)(t / H), head = (int)(t % H);
+  int b = 0, hi = B;                // cu_q[b] <= tok < cu_q[hi]
+  if (tok < __ldg(cu_q) || tok >= __ldg(cu_q + B)) return;
+  while (hi - b > 1) {
+    const int mid = (b + hi) >> 1;
+    if (__ldg(cu_q + mid) <= tok) b = mid;
+    else hi = mid;
+  }
+  const int q0 = __ldg(cu_q + b), q_len = __ldg(cu_q + b + 1) - q0, L = __ldg(seq_lens + b);
+  if (q0 < 0 || q_len < 0 || q_len > n || q0 + q_len > total_q || tok < q0 || tok >= q0 + q_len ||
+      L < 0 || (long long)L > (long long)max_blocks * 16)
+    return;                         // a skipped sequence: its rows are left alone
+  const int pair_q = 2 * kBlockM >> gl, tile_q = kBlockM >> gl;
+  const int i = tok - q0, pair = i / pair_q, in = i % pair_q;
+  const int row = (in / tile_q) * kBlockM + ((in % tile_q) << gl) + (head & ((1 << gl) - 1));
+  const size_t slot0 = (((size_t)b * (H >> gl) + (head >> gl)) * num_pairs + pair) * parts * (2 * kBlockM) + row;
+  const float4* ps = reinterpret_cast<const float4*>(part_s);
+  float M = -INFINITY;
+  for (int x = lane; x < parts; x += 32) M = fmaxf(M, __ldg(ps + slot0 + (size_t)x * (2 * kBlockM)).x);
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+  float l = 0.f, lp = 0.f, y[kVec];
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) y[e] = 0.f;
+#pragma unroll 8
+  for (int x = 0; x < parts; ++x) {
+    const size_t at = slot0 + (size_t)x * (2 * kBlockM);
+    const float4 st = __ldg(ps + at);
+    const float* po = part_o + at * D + lane * kVec;
+    float v[kVec];
+    if constexpr (kVec == 4) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(po));
+      v[0] = w.x;
+      v[1] = w.y;
+      v[2] = w.z;
+      v[3] = w.w;
+    } else {
+      const float2 w = __ldg(reinterpret_cast<const float2*>(po));
+      v[0] = w.x;
+      v[1] = w.y;
+    }
+    // (a part that saw no key has left its O unwritten: whatever was read is dropped)
+    const bool seen = st.x != -INFINITY;
+    const float f = seen ? ptx::ex2(st.x - M) : 0.f;
+    l += seen ? f * st.y : 0.f;
+    lp += seen ? f * st.z : 0.f;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) y[e] = seen ? fmaf(f, v[e], y[e]) : y[e];
+  }
+  const float inv = lp > 0.f ? 1.f / lp : (lp == 0.f ? 0.f : lp);
+  const size_t orow = (size_t)tok * H + head;
+  if (FA_IN_BOUNDS(orow, (size_t)total_q * H, status)) {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(o + orow * D + lane * kVec);
+#pragma unroll
+    for (int e = 0; e < kVec / 2; ++e) dst[e] = ptx::pack_bf16x2(y[2 * e] * inv, y[2 * e + 1] * inv);
+    if (lane == 0 && lse != nullptr)
+      lse[(size_t)head * total_q + tok] = l > 0.f ? (M + __log2f(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
+  }
+}
+
 // WIN launches take a window, sinks and packed heads; KV8 ones page caches in
 // e4m3 (see fwd_bf16_kernel).
 template <int D, bool PAGED, bool FP8, bool WIN = false, bool KV8 = false>
@@ -1418,9 +1544,7 @@ cudaError_t launch(const FwdParams& p, cudaStream_t stream, const char** why) {
   // most 128) are rows of one tile, token by token.  K and V are then read once
   // for all of them, short chunks fill the 128 rows, and a tile spans fewer
   // tokens, so less of its diagonal and window edge is masked.
-  int gl = 0;
-  if (WIN)
-    while (gl < 7 && (p.H / p.Hkv) % (2 << gl) == 0) ++gl;
+  const int gl = WIN ? packed_heads_log2(p.H, p.Hkv) : 0;
   const int pair_q = 2 * kBlockM >> gl;   // tokens of a unit's two query tiles
   {
     const uint64_t dims[3] = {(uint64_t)D, (uint64_t)p.H, q_rows};
@@ -1466,7 +1590,16 @@ cudaError_t launch(const FwdParams& p, cudaStream_t stream, const char** why) {
     }
   }
   const int num_pairs = (int)(((long long)p.n + pair_q - 1) / pair_q);
-  const long long units = (long long)p.B * (p.H >> gl) * num_pairs;
+  int parts = 1;
+  if (KV8 && p.workspace != nullptr) {
+    // no more than one part per two K/V tiles that a unit can have
+    long long keys = p.max_blocks * 16ll;
+    if (p.causal && p.window > 0) keys = std::min(keys, (long long)p.window + pair_q + p.sinks + 2 * kBlockN);
+    parts = (int)std::max(1ll, std::min((long long)cache_parts(p.B, p.n, p.H, p.Hkv), keys / (2 * kBlockN)));
+  }
+  const long long units = (long long)p.B * (p.H >> gl) * num_pairs * parts;
+  float* const part_s = static_cast<float*>(p.workspace);
+  float* const part_o = part_s + units * 2 * kBlockM * 4;
   int sms = 0;
   {
     int dev = 0;
@@ -1515,12 +1648,26 @@ cudaError_t launch(const FwdParams& p, cudaStream_t stream, const char** why) {
         p.causal, lse_stride_h, lse_stride_b, p.block_table, p.seq_lens, p.max_blocks, p.num_pages,
         out_scale, counted ? 2 : sorted ? 1 : 0, num_split, p.status, p.window, p.sinks, gl,
         static_cast<const uint8_t*>(p.k), static_cast<const uint8_t*>(p.v),
-        static_cast<const uint8_t*>(p.k_scale), static_cast<const uint8_t*>(p.v_scale));
+        static_cast<const uint8_t*>(p.k_scale), static_cast<const uint8_t*>(p.v_scale), parts, part_s,
+        part_o);
     err = cudaGetLastError();
     if (err != cudaSuccess) *why = "fwd_bf16 launch";
+    if constexpr (KV8) {
+      if (err == cudaSuccess && parts > 1) {
+        const long long rows = (long long)p.total_q * p.H;
+        merge_parts_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(
+            part_s, part_o, static_cast<__nv_bfloat16*>(p.o), p.lse, p.cu_q, p.seq_lens, p.B, p.H,
+            p.total_q, p.n, p.max_blocks, num_pairs, parts, gl, p.status);
+        err = cudaGetLastError();
+        if (err != cudaSuccess) *why = "merge_parts launch";
+      }
+    }
     return err;
   };
   if constexpr (PAGED) {
+    if constexpr (KV8) {
+      if (parts > 1) return go(fwd_bf16_kernel<D, true, FP8, true, WIN, KV8, true>);
+    }
     return go(fwd_bf16_kernel<D, true, FP8, true, WIN, KV8>);
   } else if constexpr (FP8) {   // the C ABI's e4m3 entry is dense only
     if (varlen) {

@@ -70,8 +70,8 @@ struct Geo {
   static constexpr int kRows = 8 * NT;
   static constexpr int kTile = kPage * D;                        // K or V page, bytes
   // pages in flight per warp and CTAs per SM
-  static constexpr int kStages = NT > 1 ? 6 : STREAM ? 4 : 3;
-  static constexpr int kCtasPerSm = NT > 1 ? 2 : STREAM ? 3 : 4;
+  static constexpr int kStages = NT == 4 ? 6 : NT == 2 || STREAM ? 4 : 3;
+  static constexpr int kCtasPerSm = NT == 4 ? 2 : NT == 2 || STREAM ? 3 : 4;
   static constexpr int kRing = kWarps * kStages * 2 * kTile;
   static constexpr int kMerge = kWarps * kRows * D * 4;
   static constexpr int kBody = STREAM || kRing > kMerge ? kRing : kMerge;  // the merge reuses the ring
@@ -1112,7 +1112,8 @@ size_t stream_bytes(long long units) {
 
 size_t rows_e4m3_workspace(int num_seqs, int max_q, int H, int Hkv, int d) {
   const long long rows = (long long)max_q * (H / Hkv), units = (long long)num_seqs * Hkv;
-  if (rows > kRowsE4m3Max || num_seqs > kMaxSeqs) return 0;
+  if (rows > kRowsE4m3Max) return cache_parts_bytes(num_seqs, max_q, H, Hkv, d);
+  if (num_seqs > kMaxSeqs) return 0;
   if (d == 128)
     return rows <= 8 ? stream_bytes<128, 1>(units)
                      : rows <= 16 ? stream_bytes<128, 2>(units) : stream_bytes<128, 4>(units);
