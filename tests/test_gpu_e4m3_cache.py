@@ -732,12 +732,18 @@ def test_binding_refuses_tensors_the_c_entry_cannot_tell_apart():
     assert refused(1, good[1][:-1])
     assert refused(2, good[2].view(torch.uint8).bool())
     assert refused(3, good[3].transpose(1, 2))
+    assert refused(0, good[0].view(torch.float8_e5m2))
     assert refused(4, good[4].long())
     assert refused(4, good[4][:, ::2]) if good[4].shape[1] > 1 else True
     assert refused(5, good[5][:1])
     assert refused(q=q.float())
     assert refused(q=q.transpose(1, 2))
     assert refused(q=q.cpu())
+    for ws in (torch.empty(64, dtype=torch.uint8, device="cuda"), torch.empty(1 << 24, dtype=torch.uint8),
+               torch.empty((1 << 24, 2), dtype=torch.uint8, device="cuda")[:, 0]):
+        with pytest.raises(fb.FaError) as e:
+            fb.paged_decode_e4m3(q, *good, 0.1, workspace=ws)
+        assert e.value.status == fb.FA_ERR_WORKSPACE
     k = torch.zeros((2, 2, 64), dtype=torch.bfloat16, device="cuda")
     for bad in (k.float(), k[:1], k.cpu(), k.transpose(0, 1).contiguous().transpose(0, 1),
                 torch.zeros((2, 2, 128), dtype=torch.bfloat16, device="cuda")[:, :, ::2]):

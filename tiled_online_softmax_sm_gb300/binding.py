@@ -334,7 +334,7 @@ def forward_window(q, k, v, scale, window, sinks=0, stream=None):
     -> (o [B,n,H,d] bf16, lse [B,H,n] fp32)."""
     B, n, H, d = q.shape
     m, Hkv = k.shape[1:3]
-    _tensors("forward_window", q.get_device(), ("q", q, torch.bfloat16, (B, n, H, d)),
+    _check_tensors("forward_window", q.get_device(), ("q", q, torch.bfloat16, (B, n, H, d)),
              ("k", k, torch.bfloat16, (B, m, Hkv, d)), ("v", v, torch.bfloat16, (B, m, Hkv, d)))
     o = torch.empty_like(q)
     lse = torch.empty((B, H, n), dtype=torch.float32, device=q.device)
@@ -349,7 +349,7 @@ def forward_varlen_window(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max
     Tq, H, d = q.shape
     Tk, Hkv = k.shape[:2]
     S = cu_seqlens_q.shape[0] - 1
-    _tensors("forward_varlen_window", q.get_device(), ("q", q, torch.bfloat16, (Tq, H, d)),
+    _check_tensors("forward_varlen_window", q.get_device(), ("q", q, torch.bfloat16, (Tq, H, d)),
              ("k", k, torch.bfloat16, (Tk, Hkv, d)), ("v", v, torch.bfloat16, (Tk, Hkv, d)),
              ("cu_seqlens_q", cu_seqlens_q, torch.int32, (S + 1,)),
              ("cu_seqlens_k", cu_seqlens_k, torch.int32, (S + 1,)))
@@ -406,60 +406,76 @@ def paged_decode_fused(q, k_cache, v_cache, block_table, seq_lens, num_splits, s
     return o, lse
 
 
+_CODES = frozenset((torch.float8_e4m3fn, torch.uint8, torch.int8))
+_SCALES = frozenset((torch.uint8, torch.int8) +
+                    ((torch.float8_e8m0fnu,) if hasattr(torch, "float8_e8m0fnu") else ()))
+
+
 def _refuse(fn, device, *named):
-    """Raise for the first of (name, tensor, type, shape) that is not a contiguous CUDA tensor of
-    that type (1: any one-byte type) and shape on the current device: the C entry sees only its
-    address."""
+    """Raise for the first of (name, tensor, types, shape) that is not a contiguous tensor of one of
+    those types and that shape on the current CUDA device: the C entry sees only its address."""
     current = torch.cuda.current_device()
     if device != current:
         raise FaError(FA_ERR_INVALID_ARG, f"{fn}: the tensors are on device {device}, the current "
                                           f"one is {current}")
-    for name, t, kind, shape in named:
+    for name, t, kinds, shape in named:
         if t.get_device() != device:
             raise FaError(FA_ERR_INVALID_ARG, f"{fn}: {name} is on {t.device}, not cuda:{device}")
-        if t.dtype is not kind and not (kind == 1 and t.element_size() == 1 and t.dtype is not torch.bool):
+        if t.dtype not in kinds:
             raise FaError(FA_ERR_INVALID_ARG, f"{fn}: {name} has type {t.dtype}")
         if t.shape != shape or not t.is_contiguous():
             raise FaError(FA_ERR_INVALID_ARG, f"{fn}: {name} has shape {tuple(t.shape)} and strides "
                                               f"{t.stride()}, wanted contiguous {tuple(shape)}")
+    raise FaError(FA_ERR_INVALID_ARG, f"{fn}: tensors do not fit together")
 
 
-def _tensors(fn, device, *named):
-    """_refuse, for calls on the serving path: good tensors pass in 0.3 us each."""
+def _check_tensors(fn, device, *named):
+    """As _refuse, for good tensors too: (name, tensor, type, shape)."""
     ok = device == torch.cuda.current_device()
     for _, t, kind, shape in named:
-        ok = ok and (t.dtype is kind or kind == 1) and t.shape == shape and \
-            t.get_device() == device and t.is_contiguous()
-        if kind == 1:
-            ok = ok and t.element_size() == 1 and t.dtype is not torch.bool
+        ok = ok and t.dtype is kind and t.shape == shape and t.get_device() == device and \
+            t.is_contiguous()
     if not ok:
-        _refuse(fn, device, *named)
+        _refuse(fn, device, *((name, t, (kind,), shape) for name, t, kind, shape in named))
 
 
-def _e4m3_cache(fn, device, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens):
-    """Checks of the paged e4m3 cache's tensors -> (pages, Hkv, page, d, sequences, max_blocks)."""
-    shape = k_cache.shape
-    table = block_table.shape
+def _check_cache(fn, device, kc, vc, ks, vs, bt, sl):
+    """The paged e4m3 cache's tensors: code and scale caches, block table and lengths.  (Written
+    out: it runs on every call of the serving path, where a loop over them takes twice as long.)"""
+    shape, table = kc.shape, bt.shape
     if len(shape) != 4 or len(table) != 2:
         raise FaError(FA_ERR_INVALID_ARG, f"{fn}: k_cache has shape {tuple(shape)}, block_table "
                                           f"{tuple(table)}, wanted 4 and 2 dimensions")
     rows = shape[:3]
-    _tensors(fn, device, ("k_cache", k_cache, 1, shape), ("v_cache", v_cache, 1, shape),
-             ("k_scale", k_scale, 1, rows), ("v_scale", v_scale, 1, rows),
-             ("block_table", block_table, torch.int32, table),
-             ("seq_lens", seq_lens, torch.int32, table[:1]))
-    return (*shape, *table)
+    if not (kc.dtype in _CODES and vc.dtype in _CODES and ks.dtype in _SCALES and vs.dtype in _SCALES
+            and bt.dtype is torch.int32 and sl.dtype is torch.int32 and vc.shape == shape
+            and ks.shape == rows and vs.shape == rows and sl.shape == table[:1]
+            and kc.get_device() == device and vc.get_device() == device and ks.get_device() == device
+            and vs.get_device() == device and bt.get_device() == device and sl.get_device() == device
+            and kc.is_contiguous() and vc.is_contiguous() and ks.is_contiguous()
+            and vs.is_contiguous() and bt.is_contiguous() and sl.is_contiguous()
+            and device == torch.cuda.current_device()):
+        _refuse(fn, device, ("k_cache", kc, _CODES, shape), ("v_cache", vc, _CODES, shape),
+                ("k_scale", ks, _SCALES, rows), ("v_scale", vs, _SCALES, rows),
+                ("block_table", bt, (torch.int32,), table),
+                ("seq_lens", sl, (torch.int32,), table[:1]))
+
+
+def _check_rows(fn, device, name, t, kind, shape):
+    if not (t.dtype is kind and t.shape == shape and t.get_device() == device and t.is_contiguous()):
+        _refuse(fn, device, (name, t, (kind,), shape))
 
 
 def paged_kv_write_e4m3(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                         cu_seqlens, stream=None):
     """Quantise new rows k, v [T,Hkv,d] bf16 (token strides may be larger than Hkv*d) into the
-    cache [P,Hkv,16,d] (float8_e4m3fn or any 1-byte type) and its scale bytes [P,Hkv,16]."""
+    cache [P,Hkv,16,d] (float8_e4m3fn, uint8 or int8) and its scale bytes [P,Hkv,16]."""
     fn = "paged_kv_write_e4m3"
     device = k.get_device()
-    P, Hkv, page, d, S, max_blocks = _e4m3_cache(fn, device, k_cache, v_cache, k_scale, v_scale,
-                                                 block_table, seq_lens)
-    _tensors(fn, device, ("cu_seqlens", cu_seqlens, torch.int32, (S + 1,)))
+    _check_cache(fn, device, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
+    P, Hkv, page, d = k_cache.shape
+    S, max_blocks = block_table.shape
+    _check_rows(fn, device, "cu_seqlens", cu_seqlens, torch.int32, (S + 1,))
     T = k.shape[0]
     strides = []
     for name, t in (("k", k), ("v", v)):
@@ -470,9 +486,11 @@ def paged_kv_write_e4m3(k, v, k_cache, v_cache, k_scale, v_scale, block_table, s
                                               f"{tuple(t.shape)} and strides {st}, wanted bf16 "
                                               f"{(T, Hkv, d)} with dense heads")
         strides.append(st[0] if T > 1 else Hkv * d)
-    fa_paged_kv_write_e4m3(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
-                           cu_seqlens, S, T, Hkv, d, strides[0], strides[1], page, P, max_blocks,
-                           stream)
+    lib = _lib or load()
+    _check(lib.fa_paged_kv_write_e4m3(
+        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(), S,
+        T, Hkv, d, strides[0], strides[1], page, P, max_blocks, _stream(stream)))
 
 
 def paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens,
@@ -480,24 +498,34 @@ def paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
     """The last n_s cached rows of every sequence -> (k, v) [total,Hkv,d] bf16."""
     fn = "paged_kv_read_e4m3"
     device = k_cache.get_device()
-    P, Hkv, page, d, S, max_blocks = _e4m3_cache(fn, device, k_cache, v_cache, k_scale, v_scale,
-                                                 block_table, seq_lens)
-    _tensors(fn, device, ("cu_seqlens", cu_seqlens, torch.int32, (S + 1,)))
+    _check_cache(fn, device, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
+    P, Hkv, page, d = k_cache.shape
+    S, max_blocks = block_table.shape
+    _check_rows(fn, device, "cu_seqlens", cu_seqlens, torch.int32, (S + 1,))
     k = torch.empty((total, Hkv, d), dtype=torch.bfloat16, device=k_cache.device)
     v = torch.empty_like(k)
-    fa_paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, k,
-                          v, S, total, Hkv, d, page, P, max_blocks, stream)
+    lib = _lib or load()
+    _check(lib.fa_paged_kv_read_e4m3(
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(), k.data_ptr(),
+        v.data_ptr(), S, total, Hkv, d, page, P, max_blocks, _stream(stream)))
     return k, v
 
 
-def _e4m3_workspace(workspace, device, S, max_q, H, Hkv, d, max_blocks):
-    """The caller's workspace, a new one where few units share long sequences, or none."""
-    if workspace is None and max_blocks >= 32 and \
-            (max_q * H > 32 * Hkv or (S * Hkv <= 38 and max_blocks >= 128)):
+def _e4m3_workspace(fn, workspace, q, S, max_q, H, Hkv, d, max_blocks):
+    """Address and bytes of the caller's workspace, of a new one where few units share long
+    sequences, or of none; and the tensor, to be kept until the call is queued."""
+    if workspace is None:
+        if max_blocks < 32 or (max_q * H <= 32 * Hkv and (S * Hkv > 38 or max_blocks < 128)):
+            return None, 0, None
         need = fa_paged_e4m3_workspace_size(S, max_q, H, Hkv, d)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return workspace, 0 if workspace is None else workspace.numel()
+        if not need:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != q.get_device() or not workspace.is_contiguous():
+        raise FaError(FA_ERR_WORKSPACE, f"{fn}: the workspace is on {workspace.device} with strides "
+                                        f"{workspace.stride()}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale,
@@ -505,16 +533,20 @@ def paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_le
     """q [S,H,d]; e4m3 cache [P,Hkv,16,d] with scale bytes [P,Hkv,16] -> (o [S,H,d], lse [S,H])."""
     fn = "paged_decode_e4m3"
     device = q.get_device()
-    P, Hkv, page, d, S, max_blocks = _e4m3_cache(fn, device, k_cache, v_cache, k_scale, v_scale,
-                                                 block_table, seq_lens)
+    _check_cache(fn, device, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
+    P, Hkv, page, d = k_cache.shape
+    S, max_blocks = block_table.shape
     H = q.shape[1]
-    _tensors(fn, device, ("q", q, torch.bfloat16, (S, H, d)))
+    _check_rows(fn, device, "q", q, torch.bfloat16, (S, H, d))
     o = torch.empty_like(q)
     lse = torch.empty((S, H), dtype=torch.float32, device=q.device)
-    workspace, size = _e4m3_workspace(workspace, q.device, S, 1, H, Hkv, d, max_blocks)
-    fa_paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse, S,
-                         H, Hkv, d, page, P, max_blocks, scale, window, sinks, workspace, size,
-                         stream)
+    ws, ws_bytes, keep = _e4m3_workspace(fn, workspace, q, S, 1, H, Hkv, d, max_blocks)
+    lib = _lib or load()
+    _check(lib.fa_paged_decode_e4m3(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
+        lse.data_ptr(), S, H, Hkv, d, page, P, max_blocks, scale, window, sinks, ws, ws_bytes,
+        _stream(stream)))
     return o, lse
 
 
@@ -524,17 +556,21 @@ def paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_l
     """q [Tq,H,d] packed by cu_seqlens_q over the e4m3 cache -> (o [Tq,H,d], lse [H,Tq])."""
     fn = "paged_prefill_e4m3"
     device = q.get_device()
-    P, Hkv, page, d, S, max_blocks = _e4m3_cache(fn, device, k_cache, v_cache, k_scale, v_scale,
-                                                 block_table, seq_lens)
+    _check_cache(fn, device, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
+    P, Hkv, page, d = k_cache.shape
+    S, max_blocks = block_table.shape
     Tq, H = q.shape[:2]
-    _tensors(fn, device, ("q", q, torch.bfloat16, (Tq, H, d)),
-             ("cu_seqlens_q", cu_seqlens_q, torch.int32, (S + 1,)))
+    _check_rows(fn, device, "q", q, torch.bfloat16, (Tq, H, d))
+    _check_rows(fn, device, "cu_seqlens_q", cu_seqlens_q, torch.int32, (S + 1,))
     o = torch.empty_like(q)
     lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
-    workspace, size = _e4m3_workspace(workspace, q.device, S, max_seqlen_q, H, Hkv, d, max_blocks)
-    fa_paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
-                          cu_seqlens_q, o, lse, S, Tq, max_seqlen_q, H, Hkv, d, page, P,
-                          max_blocks, scale, causal, window, sinks, workspace, size, stream)
+    ws, ws_bytes, keep = _e4m3_workspace(fn, workspace, q, S, max_seqlen_q, H, Hkv, d, max_blocks)
+    lib = _lib or load()
+    _check(lib.fa_paged_prefill_e4m3(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens_q.data_ptr(),
+        o.data_ptr(), lse.data_ptr(), S, Tq, max_seqlen_q, H, Hkv, d, page, P, max_blocks, scale,
+        1 if causal else 0, window, sinks, ws, ws_bytes, _stream(stream)))
     return o, lse
 
 
