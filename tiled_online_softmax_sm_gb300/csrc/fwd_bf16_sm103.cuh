@@ -129,6 +129,33 @@ struct Cfg {
                                           : ptx::idesc_bf16_f32(128, kON, false, true);
 };
 
+// One work unit: a pair of 128-row query tiles of one (sequence, head).
+// A split unit (dense, the last partial wave only) is one query tile whose
+// K/V tiles are halved between the two softmax warpgroups: both Q slots hold
+// the same rows, tile 1 starts at K/V tile kv_first[1], and warpgroup 0 merges
+// the two (m, l, O) states at the end, reading O_1 from tensor memory.
+struct Unit {
+  int b, h, hk;
+  int q_len, kv_len, q_row0, k_row0, q_start0;
+  int q_start[2];  // first query row (in the sequence) of each tile
+  int kv_first[2]; // first K/V tile of each tile
+  int n_kv[2];     // K/V tiles each query tile needs (0: tile inactive)
+  bool rows;       // the unit holds at least one valid query row
+  bool bad;        // varlen offsets outside the buffers
+  bool split;      // the two tiles are one query tile over two key ranges
+  // WIN: the unit's K/V tiles are a list of n_list entries, the nw tiles from
+  // w0 on, rotated by rot, and then the sinks' tiles 0, 1, ...  Tile i skips
+  // entry skip[i] (-1: none): tile 0 the last one, when all of it lies behind
+  // its rows, tile 1 the first one, when all of it lies before their windows.
+  // KV8 launches of few units cut the list into parts for several CTAs: a part
+  // starts at entry list0 of the whole list, and n_list and skip are the part's.
+  int n_list, w0, nw, rot;
+  int list0;
+  int skip[2];
+  int key_sink, key_lo, key_hi;  // keys some row of the unit sees: [0, key_sink), [key_lo, key_hi)
+  int index;       // the unit's number (-1: no more units)
+};
+
 // Varlen and paged launches with at most this many (sequence, query pair)
 // combinations get a persistent grid over a heaviest-first list of them.
 // (KV8 instances have less shared memory left for the list.)
@@ -155,34 +182,12 @@ struct Shared {
   uint64_t raw_full[3];     // KV8: e4m3 tile staged
   uint64_t raw_empty[3];    // KV8: staged tile widened
   float mstat[KV8 ? 1 : kBlockM][3];  // split unit: (m, l, l_p) of each row of warpgroup 1
+  // windowed launches: the next units, worked out ahead by warp 2
+  Unit units[2];
+  uint64_t unit_full[2];
+  uint64_t unit_empty[2];
   uint32_t tmem_base;
   int abort;
-};
-
-// One work unit: a pair of 128-row query tiles of one (sequence, head).
-// A split unit (dense, the last partial wave only) is one query tile whose
-// K/V tiles are halved between the two softmax warpgroups: both Q slots hold
-// the same rows, tile 1 starts at K/V tile kv_first[1], and warpgroup 0 merges
-// the two (m, l, O) states at the end, reading O_1 from tensor memory.
-struct Unit {
-  int b, h, hk;
-  int q_len, kv_len, q_row0, k_row0, q_start0;
-  int q_start[2];  // first query row (in the sequence) of each tile
-  int kv_first[2]; // first K/V tile of each tile
-  int n_kv[2];     // K/V tiles each query tile needs (0: tile inactive)
-  bool rows;       // the unit holds at least one valid query row
-  bool bad;        // varlen offsets outside the buffers
-  bool split;      // the two tiles are one query tile over two key ranges
-  // WIN: the unit's K/V tiles are a list of n_list entries, the nw tiles from
-  // w0 on, rotated by rot, and then the sinks' tiles 0, 1, ...  Tile i skips
-  // entry skip[i] (-1: none): tile 0 the last one, when all of it lies behind
-  // its rows, tile 1 the first one, when all of it lies before their windows.
-  // KV8 launches of few units cut the list into parts for several CTAs: a part
-  // starts at entry list0 of the whole list, and n_list and skip are the part's.
-  int n_list, w0, nw, rot;
-  int list0;
-  int skip[2];
-  int key_sink, key_lo, key_hi;  // keys some row of the unit sees: [0, key_sink), [key_lo, key_hi)
 };
 
 // Entries of the unit's K/V tile list, and the K/V tile of entry j.
@@ -486,6 +491,9 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 const uint8_t* __restrict__ k_scale, const uint8_t* __restrict__ v_scale, int parts,
                 float* __restrict__ part_s, float* __restrict__ part_o) {
   using C = Cfg<D, FP8, KV8>;
+  // (KV8 instances work the units out in every role: with the ring, and the
+  // registers it takes, their chunks were 10 % slower; the window's 4 % faster.)
+  constexpr bool kUnitRing = WIN && !KV8;
   static_assert(!KV8 || (PAGED && VAR && WIN && !FP8), "KV8 instances are paged, with windows");
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared<KV8> sh;
@@ -561,7 +569,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   // about half a unit's time.
   const int num_units =
       (VAR && sched_sorted ? Hg * sh.n_order : BH * num_pairs + (VAR ? 0 : num_split)) * (PARTS ? parts : 1);
-  auto whole_unit = [&](int u) {
+  auto whole_unit = [&](int u) __attribute__((always_inline)) {
     if (VAR && WIN && sched_sorted == 2) {
       const int c = u / Hg;
       int lo = 0, hi = B - 1;   // the first sequence whose pairs end past c
@@ -583,12 +591,11 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     if constexpr (WIN) return R;
     return u < base ? R : split_unit(R, (u - base) & 1);
   };
-  auto unit_at = [&](int u) {
-    if constexpr (PARTS) {
-      return cut_unit(whole_unit(u / parts), u % parts, parts);
-    } else {
-      return whole_unit(u);
-    }
+  auto unit_at = [&](int u) __attribute__((always_inline)) {
+    Unit U = whole_unit(PARTS ? u / parts : u);
+    if constexpr (PARTS) U = cut_unit(U, u % parts, parts);
+    U.index = u;
+    return U;
   };
 #define FA_UNIT(u) unit_at(u)
   // k-th unit of this CTA: waves of gridDim.x units in snake order (even waves
@@ -615,9 +622,23 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   const uint32_t bar_fix = ptx::smem_u32(&sh.fix);
   const uint32_t bar_mf = ptx::smem_u32(&sh.merge_full);
   const uint32_t bar_me = ptx::smem_u32(&sh.merge_empty);
+  const uint32_t bar_uf = ptx::smem_u32(&sh.unit_full[0]);
+  const uint32_t bar_ue = ptx::smem_u32(&sh.unit_empty[0]);
   const uint32_t bar_rf = ptx::smem_u32(&sh.raw_full[0]);
   const uint32_t bar_re = ptx::smem_u32(&sh.raw_empty[0]);
   volatile int* abort_flag = &sh.abort;
+  // kUnitRing: units come from the ring in shared memory (their divisions and loads
+  // would otherwise stand between one unit's end and the next one's start, in
+  // every role).  False when there are no more, or when a wait ran out.
+  auto fetch_unit = [&](int t, Unit& U, bool& ok) __attribute__((always_inline)) -> bool {
+    const int e = t & 1;
+    // (the MMA issuer is one lane, the other roles are whole warps)
+    ok = __all_sync(warp == 1 ? 1u : 0xffffffffu,
+                    ptx::mbar_wait(bar_uf + 8 * e, (t >> 1) & 1, status, abort_flag));
+    if (!ok) return false;
+    U = sh.units[e];
+    return U.index >= 0;
+  };
 
   if (threadIdx.x == 0) {
     #pragma unroll
@@ -636,6 +657,12 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     for (int s = 0; s < C::kRawStages; ++s) {
       ptx::mbar_init(bar_rf + 8 * s, 1);
       ptx::mbar_init(bar_re + 8 * s, 4);
+    }
+    if constexpr (kUnitRing) {
+      for (int e = 0; e < 2; ++e) {
+        ptx::mbar_init(bar_uf + 8 * e, 1);
+        ptx::mbar_init(bar_ue + 8 * e, 10);   // one arrival per reading warp
+      }
     }
     ptx::mbar_init(bar_drain, 1);
     ptx::mbar_init(bar_fix, 1);
@@ -685,12 +712,19 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       int nfix = 0;               // V tiles zero-fixed (paged)
       bool fix_pending = false;
       bool ok = true;
-      for (int k = 0; k * (int)gridDim.x < num_units && ok; ++k) {
-        const int u = unit_of(k);
-        if (u >= num_units) continue;
-        const Unit U = FA_UNIT(u);
-        if (U.bad && lane == 0) atomicExch(status, kDevInvalidArg);  // skip it, touch nothing
-        if (!U.rows) continue;
+      for (int k = 0; (kUnitRing || k * (int)gridDim.x < num_units) && ok; ++k) {
+        Unit U;
+        if constexpr (kUnitRing) {
+          if (!fetch_unit(k, U, ok)) break;
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar_ue + 8 * (k & 1));
+        } else {
+          const int u = unit_of(k);
+          if (u >= num_units) continue;
+          U = FA_UNIT(u);
+          if (U.bad && lane == 0) atomicExch(status, kDevInvalidArg);  // skip it, touch nothing
+          if (!U.rows) continue;
+        }
         #pragma unroll
         for (int i = 0; i < 2 && ok; ++i) {
           if (U.n_kv[i] == 0) continue;
@@ -890,11 +924,17 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         ++np[i];
         return true;
       };
-      for (int k = 0; k * (int)gridDim.x < num_units && ok; ++k) {
-        const int u = unit_of(k);
-        if (u >= num_units) continue;
-        const Unit U = FA_UNIT(u);
-        if (!U.rows) continue;
+      for (int k = 0; (kUnitRing || k * (int)gridDim.x < num_units) && ok; ++k) {
+        Unit U;
+        if constexpr (kUnitRing) {
+          if (!fetch_unit(k, U, ok)) break;
+          ptx::mbar_arrive(bar_ue + 8 * (k & 1));
+        } else {
+          const int u = unit_of(k);
+          if (u >= num_units) continue;
+          U = FA_UNIT(u);
+          if (!U.rows) continue;
+        }
         const int n_kv_max = list_size<WIN>(U);
         if (n_kv_max == 0) continue;
         #pragma unroll
@@ -1016,6 +1056,26 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       // no tcgen05.mma may still run when the tensor memory is released
       ptx::tc_commit(bar_drain);
       ptx::mbar_wait(bar_drain, 0, nullptr);
+    } else if (kUnitRing && warp == 2 && lane == 0) {
+      // ---------------------------------------------------------- schedule
+      int t = 0;
+      for (int k = 0;; ++k) {
+        const bool more = k * (int)gridDim.x < num_units;
+        Unit U{};
+        U.index = -1;
+        if (more) {
+          const int u = unit_of(k);
+          if (u >= num_units) continue;
+          U = FA_UNIT(u);
+          if (U.bad) atomicExch(status, kDevInvalidArg);  // skipped, touches nothing
+          if (!U.rows) continue;
+        }
+        if (!ptx::mbar_wait(bar_ue + 8 * (t & 1), ((t >> 1) & 1) ^ 1, status, abort_flag)) break;
+        sh.units[t & 1] = U;
+        ptx::mbar_arrive(bar_uf + 8 * (t & 1));
+        ++t;
+        if (!more) break;
+      }
     }
   } else if (KV8 && warp >= 12) {
     if constexpr (KV8) {
@@ -1127,11 +1187,18 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         for (int w = 0; w < 4; ++w) dst[w] = v[w];
       }
     };
-    for (int k = 0; k * (int)gridDim.x < num_units && ok; ++k) {
-      const int u = unit_of(k);
-      if (u >= num_units) continue;
-      const Unit U = FA_UNIT(u);
-      if (!U.rows) continue;
+    for (int k = 0; (kUnitRing || k * (int)gridDim.x < num_units) && ok; ++k) {
+      Unit U;
+      if constexpr (kUnitRing) {
+        if (!fetch_unit(k, U, ok)) break;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar_ue + 8 * (k & 1));
+      } else {
+        const int u = unit_of(k);
+        if (u >= num_units) continue;
+        U = FA_UNIT(u);
+        if (!U.rows) continue;
+      }
       // (selects, not U.x[i]: a runtime index would put the unit in local memory)
       const int q_start = i == 0 ? U.q_start[0] : U.q_start[1];
       const int kv_first = i == 0 ? U.kv_first[0] : U.kv_first[1];
@@ -1402,7 +1469,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         // this part's state, for the merge behind this kernel: rows are numbered
         // by (sequence, head group, pair), part and row of the pair
         const size_t slot =
-            ((((size_t)U.b * Hg + U.h) * num_pairs + U.q_start0 / (2 * kBlockM >> gl)) * parts + u % parts) *
+            ((((size_t)U.b * Hg + U.h) * num_pairs + U.q_start0 / (2 * kBlockM >> gl)) * parts + U.index % parts) *
                 (2 * kBlockM) + i * kBlockM + r;
         if (row_valid) {
           *reinterpret_cast<float4*>(part_s + slot * 4) = make_float4(m_ref, l_run, l_p, 0.f);
