@@ -1081,13 +1081,23 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     if constexpr (KV8) {
       ptx::setmaxnreg_dec<kConvertRegs8>();
       // ---------------------------------------------------------- widening
-      // A staged tile's 16-byte units (16 codes of one row) are spread over the
-      // 128 threads, neighbours on neighbouring units; each becomes two 16-byte
-      // units of the bf16 tile, at the 128-byte-swizzled place the MMA reads.
-      // Threads in the upper half of a 128-wide row store their odd unit first,
-      // so that the eight lanes of a store phase touch all banks once.
+      // A staged tile's 16-byte units (16 codes of one row) become two 16-byte
+      // units each of the bf16 tile, at the 128-byte-swizzled place the MMA
+      // reads.  A thread takes two units a step.  At D = 128 they are units u
+      // and u ^ 4 of one row (u in the lower half for even rows, the upper for
+      // odd ones), so one scale serves both and the eight lanes of a load or
+      // store phase touch every bank once; at D = 64 they are unit u of two
+      // rows.
       constexpr int kUnits = D / 16;               // units per row
+      constexpr int kStepRows = 256 / kUnits;      // rows the 128 threads cover in a step
       const int tid = threadIdx.x - 12 * 32;
+      const int row0 = D == 128 ? tid >> 2 : tid >> 2;
+      const int un = D == 128 ? (tid & 3) + 4 * (row0 & 1) : tid & 3;
+      const uint32_t put0 = (D == 128 ? (row0 & 1) * 16384 : 0) + row0 * 128 +
+                            (((2 * (un & 3)) ^ (row0 & 7)) << 4);
+      // the second unit of a step, from the first: staged and widened
+      constexpr int kRaw2 = D == 128 ? 64 : 32 * D;
+      constexpr int kPut2 = D == 128 ? 16384 : 32 * 128;
       int lc = 0;
       bool ok = true;
       for (int k = 0; k * (int)gridDim.x < num_units && ok; ++k) {
@@ -1110,45 +1120,36 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           // weights never meet a NaN
           const int k0 = j * kBlockN;
           const bool whole = k0 + kBlockN <= U.key_hi && (k0 >= U.key_lo || k0 + kBlockN <= U.key_sink);
-          auto put = [&](int idx, const uint4& x, uint32_t b) __attribute__((always_inline)) {
-            const int row = idx / kUnits, un = idx % kUnits;
+          // (D = 128: the second unit is at the first's place with bit 6 of the
+          // staged and bit 14 of the widened offset flipped)
+          auto raw2 = [&](uint32_t o) { return D == 128 ? o ^ kRaw2 : o + kRaw2; };
+          auto put2 = [&](uint32_t o) { return D == 128 ? o ^ kPut2 : o + kPut2; };
+          auto put = [&](uint32_t o, const uint4& x, uint32_t b) __attribute__((always_inline)) {
             uint4 lo, hi;
             ptx::widen16(x, b, lo, hi);
-            uint8_t* rowp = tile + (un >> 2) * 16384 + row * 128;
-            const bool odd = un >> 2;
-            const int p0 = ((2 * (un & 3)) ^ (row & 7) ^ (odd ? 1 : 0)) << 4;
-            *reinterpret_cast<uint4*>(rowp + p0) = odd ? hi : lo;
-            *reinterpret_cast<uint4*>(rowp + (p0 ^ 16)) = odd ? lo : hi;
+            *reinterpret_cast<uint4*>(tile + o) = lo;
+            *reinterpret_cast<uint4*>(tile + (o ^ 16)) = hi;
           };
-          if (whole) {
-            // two units at a time, their loads first: 974 us with one and a
-            // branch in the loop, 668 so (16 x 512-token chunks)
-#pragma unroll 1
-            for (int it = 0; it < kUnits; it += 2) {
-              uint4 x[2];
-              uint32_t b[2];
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const int idx = (it + y) * 128 + tid;
-                x[y] = *reinterpret_cast<const uint4*>(raw + idx * 16);
-                b[y] = raw[128 * D + idx / kUnits];
-              }
-#pragma unroll
-              for (int y = 0; y < 2; ++y) put((it + y) * 128 + tid, x[y], b[y]);
+          auto hide = [&](int row, uint4& x, uint32_t& b) __attribute__((always_inline)) {
+            const int key = k0 + row;
+            if (!(key < U.key_sink || (key >= U.key_lo && key < U.key_hi))) {
+              x = make_uint4(0u, 0u, 0u, 0u);
+              b = 127u;
             }
-          } else {
+          };
 #pragma unroll 1
-            for (int it = 0; it < kUnits; ++it) {
-              const int idx = it * 128 + tid;
-              uint4 x = *reinterpret_cast<const uint4*>(raw + idx * 16);
-              uint32_t b = raw[128 * D + idx / kUnits];
-              const int key = k0 + idx / kUnits;
-              if (!(key < U.key_sink || (key >= U.key_lo && key < U.key_hi))) {
-                x = make_uint4(0u, 0u, 0u, 0u);
-                b = 127u;
-              }
-              put(idx, x, b);
+          for (int r = 0; r < kBlockN; r += kStepRows) {
+            const uint32_t from = (uint32_t)((row0 + r) * D + un * 16), to = put0 + (uint32_t)r * 128;
+            uint4 x0 = *reinterpret_cast<const uint4*>(raw + from);
+            uint4 x1 = *reinterpret_cast<const uint4*>(raw + raw2(from));
+            uint32_t b0 = raw[128 * D + row0 + r];
+            uint32_t b1 = D == 128 ? b0 : raw[128 * D + row0 + r + 32];
+            if (!whole) {
+              hide(row0 + r, x0, b0);
+              hide(D == 128 ? row0 + r : row0 + r + 32, x1, b1);
             }
+            put(to, x0, b0);
+            put(put2(to), x1, b1);
           }
           ptx::fence_proxy_async_smem();   // the MMA (and the next copy) come behind these accesses
           __syncwarp();
