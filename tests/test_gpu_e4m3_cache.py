@@ -483,8 +483,10 @@ def test_chunks_window(window, sinks, group):
 
 
 def test_chunk_equals_the_bf16_prefill_of_the_read_back_cache():
-    """Widening a tile is exact, so with one query head per kv head (no packing) the bits are
-    those of fa_paged_prefill on the rows read back into a bf16 cache."""
+    """Widening a tile is exact, so with one query head per kv head (no packing) the LSE's bits are
+    those of fa_paged_prefill on the rows read back into a bf16 cache, and at d = 64 O's too.  At
+    d = 128 O's divisor is the exact sum here, the rounded weights' there: 2^-9 apart, before each
+    is rounded to bf16 (half a step, 2^-8)."""
     rng = np.random.default_rng(30)
     lens, new = [300, 77, 513, 20], [200, 77, 60, 33]
     for d in (64, 128):
@@ -497,8 +499,12 @@ def test_chunk_equals_the_bf16_prefill_of_the_read_back_cache():
         fb.fa_paged_prefill_e4m3(q, *t, cu, o1, l1, 4, sum(new), max(new), 4, 4, d, 16, c.num_pages,
                                  c.table.shape[1], 0.1)
         o2, l2 = fb.paged_prefill(q, kc, vc, t[4], t[5], cu, max(new), 0.1)
-        assert torch.equal(o1.view(torch.int16), o2.view(torch.int16))
         assert torch.equal(l1.view(torch.int32), l2.view(torch.int32))
+        if d == 64:
+            assert torch.equal(o1.view(torch.int16), o2.view(torch.int16))
+        else:
+            o1, o2 = _f64(o1), _f64(o2)
+            assert (np.abs(o1 - o2) <= (2.0 ** -9 + 2 * 2.0 ** -8) * 1.01 * np.abs(o2)).all()
     assert fb.fa_get_device_status() == 0
 
 
