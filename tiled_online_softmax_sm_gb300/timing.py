@@ -13,7 +13,8 @@ replays of 20 launches, per launch.  Inputs smaller than L2 (the n=m=2048
 shapes, the fp32 case) stay L2-resident across launches; the long-context,
 decode, prefill and ragged inputs are larger than L2.  Rates use nominal work:
 4*n*m*d*H*B FLOPs (halved when causal; the ragged and paged rows sum their
-sequences), and for the decode the K and V bytes of every valid token.
+sequences, the windowed one its visible pairs), and for the decode the K and
+V bytes of every valid token (with their scale bytes in the e4m3 cache).
 Nothing is checked here; parity lives in the tests.
 
 --naive times instead the materialised-score path against fa_forward at N =
@@ -164,7 +165,56 @@ def rows(iters: int, warmup: int):
                                                      1), iters, warmup)
         fl = sum(4.0 * int(L) * int(L) * d * vcase.H / 2 for L in vcase.lens)
         out.append((f"ragged causal varlen 16 seqs H=16 d={d}", ms, fl / (ms * 1e9), "TFLOP/s"))
+    return out + _e4m3_cache_rows(iters, warmup) + _window_rows(iters, warmup)
+
+
+def _e4m3_cache_rows(iters, warmup):
+    """The e4m3 paged cache at the decode pool's and the chunks' sizes: the cache is filled by the
+    write it times first, then read back and attended."""
+    out = []
+    g = torch.Generator(device="cuda").manual_seed(I.BASE_SEED)
+    H, Hkv, d = 32, 8, 128
+    for S, seed, chunk in ((64, I.BASE_SEED, 1), (16, 63, 512)):
+        lens = I.uniform_lengths(seed, S, 512, 8192)
+        need = (lens + 15) // 16
+        pages, T = int(need.sum()), int(lens.sum())
+        bt = np.full((S, 512), -1, np.int32)
+        ids = np.random.default_rng(seed).permutation(pages).astype(np.int32)
+        for s, at in enumerate(np.cumsum(need) - need):
+            bt[s, :need[s]] = ids[at:at + need[s]]
+        bt, sl = torch.from_numpy(bt).cuda(), torch.from_numpy(lens.astype(np.int32)).cuda()
+        cu = torch.from_numpy(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)).cuda()
+        k, v = (torch.randn((T, Hkv, d), device="cuda", generator=g).bfloat16() for _ in range(2))
+        cache = [torch.zeros((pages, Hkv, 16, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        cache += [torch.zeros((pages, Hkv, 16), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        cache += [bt, sl]
+        ms = _median_ms(lambda: fb.paged_kv_write_e4m3(k, v, *cache, cu), iters, warmup)
+        if chunk == 1:
+            out.append((f"e4m3 cache write {T} tokens Hkv=8 d=128", ms, T * Hkv * 2 * (3 * d + 1) / (ms * 1e6), "GB/s"))
+            ms = _median_ms(lambda: fb.paged_kv_read_e4m3(*cache, cu, T), iters, warmup)
+            out.append((f"e4m3 cache read {T} tokens Hkv=8 d=128", ms, T * Hkv * 2 * (3 * d + 1) / (ms * 1e6), "GB/s"))
+            q = torch.randn((S, H, d), device="cuda", generator=g).bfloat16()
+            ms = _median_ms(lambda: fb.paged_decode_e4m3(q, *cache, I.fp32_scale(d)), iters, warmup)
+            out.append(("e4m3 paged decode 64 seqs H=32 Hkv=8", ms, T * Hkv * (2 * d + 2) / (ms * 1e6), "GB/s"))
+        else:
+            ql = np.minimum(lens, chunk)
+            cuq = torch.from_numpy(np.concatenate([[0], np.cumsum(ql)]).astype(np.int32)).cuda()
+            q = torch.randn((int(ql.sum()), H, d), device="cuda", generator=g).bfloat16()
+            ms = _median_ms(lambda: fb.paged_prefill_e4m3(q, *cache, cuq, chunk, I.fp32_scale(d)), iters, warmup)
+            fl = sum(4.0 * int(nq) * d * H * (int(L) - int(nq) / 2) for nq, L in zip(ql, lens))
+            out.append(("e4m3 paged prefill 16 x 512-token chunks H=32 Hkv=8", ms, fl / (ms * 1e9), "TFLOP/s"))
+        del k, v, cache
     return out
+
+
+def _window_rows(iters, warmup, n=8192, H=32, d=128, window=1024, sinks=4):
+    g = torch.Generator(device="cuda").manual_seed(I.BASE_SEED)
+    q, k, v = (torch.randn((1, n, H, d), device="cuda", generator=g).bfloat16() for _ in range(3))
+    ms = _median_ms(lambda: fb.forward_window(q, k, v, I.fp32_scale(d), window, sinks), iters, warmup)
+    p = np.arange(n)
+    pairs = (np.minimum(p + 1, window) + np.minimum(sinks, np.maximum(0, p + 1 - window))).sum()
+    return [(f"bf16 window {window} sinks {sinks} n=m={n} H={H} d={d}", ms, 4.0 * d * H * float(pairs) / (ms * 1e9),
+             "TFLOP/s")]
 
 
 def fp8_gemm_peak(n: int = 8192, reps: int = 10):
