@@ -48,7 +48,7 @@ DECODE_SPLITS = 8
 def workload_name(splits: int) -> str:
     return ("long-context causal prefill bf16 B=1 H=32 n=m=8192 d=dv=128 + paged GQA decode "
             f"bf16 64 seqs H=32 Hkv=8 d=128 page 16 ctx U[512,8192] split {splits}")
-FWD_KERNEL_SRC = os.path.join(ROOT, "tiled_online_softmax_sm_gb300", "csrc", "fwd_bf16_sm103.cu")
+FWD_KERNEL_SRC = os.path.join(ROOT, "tiled_online_softmax_sm_gb300", "csrc", "fwd_bf16_sm103.cuh")
 DEC_KERNEL_SRC = os.path.join(ROOT, "tiled_online_softmax_sm_gb300", "csrc", "decode.cu")
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic.json")
 

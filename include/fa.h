@@ -366,7 +366,7 @@ fa_status fa_paged_gather(const void* k_cache, const void* v_cache, const int* b
  * NaN.  Caches written by other means may use any byte from 0 to 254.
  * Caches and scales are 16-byte aligned.
  * Supported: d in {64, 128}, page_size == 16; num_pages*Hkv*16 and rows*Hkv
- * below 2^31, max_blocks_per_seq below 2^27.
+ * below 2^31, max_blocks_per_seq below 2^26.
  * The block table, seq_lens and (where taken) cu_seqlens are as for
  * fa_paged_prefill: sequence s owns rows [cu_seqlens[s], cu_seqlens[s+1]) of
  * the packed tensors, and those n_s rows are the last n_s of its seq_lens[s]

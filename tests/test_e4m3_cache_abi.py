@@ -57,7 +57,7 @@ def test_cache_refusals(lib, call):
                dict(maxb=0), dict(kc=24), dict(vc=8), dict(ks=4), dict(vs=17), dict(bt=18),
                dict(sl=17)):
         assert call(lib, **kw) == fb.FA_ERR_INVALID_ARG, kw
-    for kw in (dict(d=96), dict(d=256), dict(page=32), dict(P=1 << 24), dict(maxb=1 << 27)):
+    for kw in (dict(d=96), dict(d=256), dict(page=32), dict(P=1 << 24), dict(maxb=1 << 26)):
         assert call(lib, **kw) == fb.FA_ERR_UNSUPPORTED, kw
     assert call(lib, S=0) == fb.FA_OK
 

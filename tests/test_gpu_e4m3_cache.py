@@ -695,6 +695,57 @@ def test_captured_step_replays_and_streams_do_not_mix():
     assert fb.fa_get_device_status() == 0
 
 
+def test_split_calls_captured_and_replayed():
+    """The two-launch forms (equal shares, cut chunks) in one graph, replayed beside eager calls on
+    another stream with a workspace of their own."""
+    rng = np.random.default_rng(23)
+    c = _cache(rng, [3000, 2500], 2, 128)
+    t = c.gpu()
+    q1 = E.bf16(rng.standard_normal((2, 8, 128)))[0].cuda()
+    q2 = E.bf16(rng.standard_normal((60, 8, 128)))[0].cuda()
+    cu = _i32([0, 20, 60])
+
+    def step():
+        return fb.paged_decode_e4m3(q1, *t, 0.1) + fb.paged_prefill_e4m3(q2, *t, cu, 40, 0.1, window=900)
+    want = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        got = step()
+    for _ in range(10):
+        with torch.cuda.stream(side):
+            g.replay()
+        eager = step()
+    torch.cuda.synchronize()
+    for a, b, e in zip(want, got, eager):
+        assert torch.equal(a, b) and torch.equal(a, e)
+    assert fb.fa_get_device_status() == 0
+
+
+def test_widest_windows_and_wild_offsets():
+    """Windows and sinks up to 2^31 - 1 mean what they say, with more queries than keys too; offsets
+    whose sums pass 32 bits are refused on the device and nothing is written."""
+    rng = np.random.default_rng(24)
+    big = 2 ** 31 - 1
+    c = _cache(rng, [100, 300], 2, 128, max_blocks=64)
+    for group in (1, 8):
+        q = E.bf16(rng.standard_normal((170, 2 * group, 128)))[0]
+        for w, s in ((big, 0), (big, big), (1023, big), (50, big)):
+            _chunk_check(c, q, [120, 50], True, w, s, P_ROUND)
+    q = E.bf16(rng.standard_normal((2, 8, 128)))[0]
+    _decode_check(c, q, big, big)
+    _decode_check(c, q, 40, big)
+    for n in (8, 90):           # short chunks and long ones
+        q = E.bf16(rng.standard_normal((2 * n, 8, 128)))[0].cuda()
+        for cu in ([0, big - 4, big], [0, -5, n], [big, 2, n], [-big, big, n], [big - 3, -big, n]):
+            o = torch.full((2 * n, 8, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+            fb.fa_paged_prefill_e4m3(q, *c.gpu(), _i32(cu), o, None, 2, 2 * n, n, 8, 2, 128, 16,
+                                     c.num_pages, 64, 0.1)
+            assert fb.fa_get_device_status() == fb.FA_ERR_INVALID_ARG, cu
+            assert (o[n:] == 9.0).all(), cu
+
+
 def test_offsets_past_32_bits():
     """Pages whose byte offset passes 2^32 are written, read back and attended."""
     pages, Hkv, d = 270000, 8, 128                 # 4.4 GB a cache

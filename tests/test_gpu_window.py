@@ -138,6 +138,25 @@ def test_captured_and_replayed_on_another_stream():
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
 
 
+def test_widest_windows():
+    big = 2 ** 31 - 1
+    for n, m in ((200, 300), (300, 200)):
+        for w, s in ((big, 0), (big, big), (60, big)):
+            _dense_check(np.random.default_rng(n), 1, n, m, 4, 2, 64, w, s)
+
+
+def test_wild_offsets_are_refused():
+    """Offsets whose sums pass 32 bits: the sequence is skipped and nothing is written."""
+    big = 2 ** 31 - 1
+    q, k, v = (torch.zeros((100, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    for cu in ([0, big - 4, big], [big, 5, 10], [-big, big, 60], [big - 3, -big, 60]):
+        o = torch.full((100, 2, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+        fb.fa_forward_varlen_window(q, k, v, o, None, _i32(cu), _i32([0, 50, 100]), 2, 100, 100, 60, 60,
+                                    2, 2, 64, 64, 0.1, 20, 1)
+        assert fb.fa_get_device_status() == fb.FA_ERR_INVALID_ARG, cu
+        assert (o[60:] == 9.0).all(), cu
+
+
 def test_bad_offsets_set_the_status():
     rng = np.random.default_rng(5)
     q, k, v = (E.bf16(rng.standard_normal((100, 2, 64)))[0].cuda() for _ in range(3))

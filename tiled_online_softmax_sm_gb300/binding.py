@@ -512,11 +512,13 @@ def paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
     return k, v
 
 
-def _e4m3_workspace(fn, workspace, q, S, max_q, H, Hkv, d, max_blocks):
+def _e4m3_workspace(fn, workspace, q, S, max_q, H, Hkv, d, max_blocks, stream):
     """Address and bytes of the caller's workspace, of a new one where few units share long
-    sequences, or of none; and the tensor, to be kept until the call is queued."""
+    sequences, or of none; and the tensor, to be kept until the call is queued.  (None on a stream
+    that is not torch's current one: a new one could be given out again before the call is done.)"""
     if workspace is None:
-        if max_blocks < 32 or (max_q * H <= 32 * Hkv and (S * Hkv > 38 or max_blocks < 128)):
+        if stream is not None or max_blocks < 32 or (
+                max_q * H <= 32 * Hkv and (S * Hkv > 38 or max_blocks < 128)):
             return None, 0, None
         need = fa_paged_e4m3_workspace_size(S, max_q, H, Hkv, d)
         if not need:
@@ -540,7 +542,7 @@ def paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_le
     _check_rows(fn, device, "q", q, torch.bfloat16, (S, H, d))
     o = torch.empty_like(q)
     lse = torch.empty((S, H), dtype=torch.float32, device=q.device)
-    ws, ws_bytes, keep = _e4m3_workspace(fn, workspace, q, S, 1, H, Hkv, d, max_blocks)
+    ws, ws_bytes, keep = _e4m3_workspace(fn, workspace, q, S, 1, H, Hkv, d, max_blocks, stream)
     lib = _lib or load()
     _check(lib.fa_paged_decode_e4m3(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
@@ -564,7 +566,8 @@ def paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_l
     _check_rows(fn, device, "cu_seqlens_q", cu_seqlens_q, torch.int32, (S + 1,))
     o = torch.empty_like(q)
     lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
-    ws, ws_bytes, keep = _e4m3_workspace(fn, workspace, q, S, max_seqlen_q, H, Hkv, d, max_blocks)
+    ws, ws_bytes, keep = _e4m3_workspace(fn, workspace, q, S, max_seqlen_q, H, Hkv, d,
+                                         max_blocks, stream)
     lib = _lib or load()
     _check(lib.fa_paged_prefill_e4m3(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),

@@ -249,8 +249,8 @@ fa_status fa_forward_window(const void* q, const void* k, const void* v, void* o
   int* sp = nullptr;
   if ((st = status_ptr(&sp)) != FA_OK) return st;
   fa::FwdParams p{q, k, v, o, lse, nullptr, nullptr, B, H, Hkv, n, m, d, dv, 0, 0, scale, 1, sp};
-  p.window = window;
-  p.sinks = window > 0 ? sinks : 0;
+  p.window = window >= m ? 0 : window;   // reaching back over every key: none
+  p.sinks = p.window > 0 ? sinks : 0;
   const char* why = nullptr;
   cudaError_t e = fa::launch_fwd_window(p, static_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess) return cuda_fail(e, why ? why : "fa_forward_window launch");
@@ -288,8 +288,8 @@ fa_status fa_forward_varlen_window(const void* q, const void* k, const void* v, 
   if ((st = status_ptr(&sp)) != FA_OK) return st;
   fa::FwdParams p{q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, num_seqs, H, Hkv,
                   max_seqlen_q, max_seqlen_k, d, dv, total_q, total_k, scale, 1, sp};
-  p.window = window;
-  p.sinks = window > 0 ? sinks : 0;
+  p.window = window >= total_k ? 0 : window;   // reaching back over every key: none
+  p.sinks = p.window > 0 ? sinks : 0;
   const char* why = nullptr;
   cudaError_t e = fa::launch_fwd_window(p, static_cast<cudaStream_t>(stream), &why);
   if (e != cudaSuccess) return cuda_fail(e, why ? why : "fa_forward_varlen_window launch");
@@ -519,7 +519,7 @@ fa_status check_cache(const char* fn, const void* k_cache, const void* v_cache, 
     return fail(FA_ERR_INVALID_ARG, "%s: empty page pool or block table", fn);
   // cache rows (page * Hkv + head) * 16 and token positions are 32-bit
   if ((long long)num_pages * Hkv * 16 > 0x7fffffffLL || (long long)total * Hkv > 0x7fffffffLL ||
-      max_blocks_per_seq > 0x7ffffff)
+      max_blocks_per_seq > 0x3ffffff)
     return fail(FA_ERR_UNSUPPORTED, "%s: page pool, block table or rows too large", fn);
   if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale) ||
       (reinterpret_cast<uintptr_t>(block_table) & 3u) ||
@@ -535,6 +535,9 @@ fa_status check_window(const char* fn, int causal, int window, int sinks) {
     return fail(FA_ERR_INVALID_ARG, "%s: a window needs causal=1", fn);
   return FA_OK;
 }
+
+// A window that reaches back over every key there can be is none.
+int effective_window(int window, long long keys) { return window >= keys ? 0 : window; }
 
 fa_status check_heads(const char* fn, const void* q, const void* o, const float* lse, int H,
                       int Hkv, float scale) {
@@ -642,6 +645,7 @@ fa_status fa_paged_decode_e4m3(const void* q, const void* k_cache, const void* v
     return fail(FA_ERR_UNSUPPORTED, "%s: num_seqs*H must stay below 2^28", fn);
   if ((st = check_e4m3_workspace(fn, workspace, workspace_bytes, num_seqs, 1, H, Hkv, d)) != FA_OK)
     return st;
+  window = effective_window(window, max_blocks_per_seq * 16ll);
   int* sp = nullptr;
   if ((st = status_ptr(&sp)) != FA_OK) return st;
   fa::PagedE4m3Params p{q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, nullptr, o,
@@ -679,6 +683,7 @@ fa_status fa_paged_prefill_e4m3(const void* q, const void* k_cache, const void* 
   if ((st = check_e4m3_workspace(fn, workspace, workspace_bytes, num_seqs, max_seqlen_q, H, Hkv,
                                  d)) != FA_OK)
     return st;
+  window = effective_window(window, max_blocks_per_seq * 16ll);
   int* sp = nullptr;
   if ((st = status_ptr(&sp)) != FA_OK) return st;
   const char* why = nullptr;

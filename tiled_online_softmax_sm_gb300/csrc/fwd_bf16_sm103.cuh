@@ -364,7 +364,7 @@ __device__ __forceinline__ Unit make_unit(int b, int h, int t, int H, int Hkv, i
     U.q_len = __ldg(cu_q + U.b + 1) - U.q_row0;
     U.k_row0 = 0;
     U.kv_len = __ldg(seq_lens + U.b);
-    U.bad = U.q_row0 < 0 || U.q_len < 0 || U.q_row0 + U.q_len > total_q || U.kv_len < 0 ||
+    U.bad = U.q_row0 < 0 || U.q_len < 0 || (long long)U.q_row0 + U.q_len > total_q || U.kv_len < 0 ||
             (long long)U.kv_len > (long long)max_blocks * 16;   // wide: max_blocks may pass 2^27
     if (WIN) U.bad = U.bad || U.q_len > n;
   } else if (cu_q != nullptr) {
@@ -372,8 +372,8 @@ __device__ __forceinline__ Unit make_unit(int b, int h, int t, int H, int Hkv, i
     U.q_len = __ldg(cu_q + U.b + 1) - U.q_row0;
     U.k_row0 = __ldg(cu_k + U.b);
     U.kv_len = __ldg(cu_k + U.b + 1) - U.k_row0;
-    U.bad = U.q_row0 < 0 || U.q_len < 0 || U.q_row0 + U.q_len > total_q || U.k_row0 < 0 ||
-            U.kv_len < 0 || U.k_row0 + U.kv_len > total_k;
+    U.bad = U.q_row0 < 0 || U.q_len < 0 || (long long)U.q_row0 + U.q_len > total_q || U.k_row0 < 0 ||
+            U.kv_len < 0 || (long long)U.k_row0 + U.kv_len > total_k;
   }
   const int tile_q = WIN ? kBlockM >> gl : kBlockM;   // tokens per query tile
   U.q_start0 = t * 2 * tile_q;
@@ -390,7 +390,7 @@ __device__ __forceinline__ Unit make_unit(int b, int h, int t, int H, int Hkv, i
       int keys = U.kv_len;
       if (causal) keys = min(U.kv_len, min(qs + tile_q, U.q_len) + diff);
       hi[i] = (!U.rows || qs >= U.q_len || keys <= 0) ? 0 : (keys + kBlockN - 1) / kBlockN;
-      const int lo_key = causal && window > 0 ? max(0, qs + diff + 1 - window) : 0;
+      const int lo_key = causal && window > 0 ? (int)max(0ll, (long long)qs + diff + 1 - window) : 0;
       lo[i] = lo_key / kBlockN;
       if (hi[i] > 0) lo_last = lo_key;
       if (i == 0) {
@@ -1549,7 +1549,7 @@ merge_parts_kernel(const float* __restrict__ part_s, const float* __restrict__ p
     else hi = mid;
   }
   const int q0 = __ldg(cu_q + b), q_len = __ldg(cu_q + b + 1) - q0, L = __ldg(seq_lens + b);
-  if (q0 < 0 || q_len < 0 || q_len > n || q0 + q_len > total_q || tok < q0 || tok >= q0 + q_len ||
+  if (q0 < 0 || q_len < 0 || q_len > n || (long long)q0 + q_len > total_q || tok < q0 || tok >= q0 + q_len ||
       L < 0 || (long long)L > (long long)max_blocks * 16)
     return;                         // a skipped sequence: its rows are left alone
   const int pair_q = 2 * kBlockM >> gl, tile_q = kBlockM >> gl;

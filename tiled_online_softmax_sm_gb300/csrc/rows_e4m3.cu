@@ -670,8 +670,7 @@ rows_cluster_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         const float rk = ptx::ld_cluster_f32(ptx::cluster_map(ar, k));
         const float lk = ptx::ld_cluster_f32(ptx::cluster_map(al, k));
         const float4 z = ptx::ld_cluster_f32x4(ptx::cluster_map(ab, k));
-        
-        sum += lk * ptx::ex2(mk - M);
+        sum += lk * ptx::ex2(mk - M); 
         const float f = ptx::ex2(rk - R);
         y.x += z.x * f;
         y.y += z.y * f;
