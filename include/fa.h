@@ -413,7 +413,8 @@ fa_status fa_paged_kv_read_e4m3(const void* k_cache, const void* v_cache, const 
  * fa_paged_e4m3_workspace_size — bytes of the optional workspace of
  * fa_paged_decode_e4m3 (max_seqlen_q 1) and fa_paged_prefill_e4m3: partials of
  * a few long sequences whose keys are split over the GPU.  0 where the calls
- * use none (enough work without splitting) or for invalid sizes.
+ * use none (enough work without splitting) or for invalid sizes.  (A prefill of
+ * fewer rows than the bound may run without the workspace it was sized for.)
  */
 size_t fa_paged_e4m3_workspace_size(int num_seqs, int max_seqlen_q, int H, int Hkv, int d);
 

@@ -723,6 +723,23 @@ def test_split_calls_captured_and_replayed():
     assert fb.fa_get_device_status() == 0
 
 
+@pytest.mark.parametrize("bound", [8, 40, 512, 8192, 2 ** 31 - 1])
+def test_workspace_of_a_larger_bound_on_the_chunk(bound):
+    """max_seqlen_q may be any upper bound (a captured step's), with the workspace sized for it,
+    although the form that the rows at hand take may want a larger one."""
+    rng = np.random.default_rng(25)
+    c = _cache(rng, [2500], 1, 128)
+    q = E.bf16(rng.standard_normal((8, 8, 128)))[0].cuda()
+    cu = _i32([0, 8])
+    ref = E.attend(_f64(q), c.rows["k"][0], c.rows["v"][0], 0.1, True, 0, 0, c.vexp[0])
+    need = fb.fa_paged_e4m3_workspace_size(1, bound, 8, 1, 128)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+    for w in (ws, None):
+        o, lse = fb.paged_prefill_e4m3(q, *c.gpu(), cu, bound, 0.1, workspace=w)
+        E.check(_f64(o), _f64(lse).T, ref, 128, P_ROUND)
+    assert fb.fa_get_device_status() == 0
+
+
 def test_widest_windows_and_wild_offsets():
     """Windows and sinks up to 2^31 - 1 mean what they say, with more queries than keys too; offsets
     whose sums pass 32 bits are refused on the device and nothing is written."""

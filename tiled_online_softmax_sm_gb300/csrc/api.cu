@@ -677,12 +677,18 @@ fa_status fa_paged_prefill_e4m3(const void* q, const void* k_cache, const void* 
                    &nothing);
   if (st != FA_OK || nothing || max_seqlen_q == 0) return st;
   if (q == nullptr || o == nullptr) return fail(FA_ERR_INVALID_ARG, "%s: null q/o", fn);
-  if (max_seqlen_q > total_q) max_seqlen_q = total_q;   // no sequence has more
-  if ((long long)num_seqs * max_seqlen_q * H > 0xfffffffLL)
-    return fail(FA_ERR_UNSUPPORTED, "%s: num_seqs*max_seqlen_q*H must stay below 2^28", fn);
   if ((st = check_e4m3_workspace(fn, workspace, workspace_bytes, num_seqs, max_seqlen_q, H, Hkv,
                                  d)) != FA_OK)
     return st;
+  if (max_seqlen_q > total_q) {   // no sequence has more
+    max_seqlen_q = total_q;
+    // a workspace made for the larger bound may be too small for the form that
+    // this one takes, which then runs without
+    if (workspace_bytes < fa::rows_e4m3_workspace(num_seqs, max_seqlen_q, H, Hkv, d))
+      workspace = nullptr;
+  }
+  if ((long long)num_seqs * max_seqlen_q * H > 0xfffffffLL)
+    return fail(FA_ERR_UNSUPPORTED, "%s: num_seqs*max_seqlen_q*H must stay below 2^28", fn);
   window = effective_window(window, max_blocks_per_seq * 16ll);
   int* sp = nullptr;
   if ((st = status_ptr(&sp)) != FA_OK) return st;
