@@ -725,6 +725,21 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           if (U.bad && lane == 0) atomicExch(status, kDevInvalidArg);  // skip it, touch nothing
           if (!U.rows) continue;
         }
+        // KV8: the page that this lane copies of tile j (pages outside the unit's
+        // visible keys may be unlisted: any page does).  At D = 128, where two
+        // staged tiles cover less of a copy's latency, it is looked up a tile
+        // ahead, for K and V at once.  us without and with, at D = 128: 64
+        // sequences x 9 tokens 266, 252, 16 x 512 541, 537; at D = 64, 16 x 512
+        // 512, 533.
+        constexpr bool kAhead = KV8 && D == 128;
+        auto look_up = [&](int j) -> int {
+          const int key = j * kBlockN + lane * 16;
+          const bool seen = lane < kBlockN / 16 && key < U.kv_len &&
+                            (key < U.key_sink || (key + 16 > U.key_lo && key < U.key_hi));
+          return seen ? __ldg(block_table + (size_t)U.b * max_blocks + j * (kBlockN / 16) + lane) : 0;
+        };
+        int page = 0, page_next = 0;
+        if (kAhead && list_size<WIN>(U) > 0) page_next = look_up(list_tile<WIN, PARTS>(U, 0));
         #pragma unroll
         for (int i = 0; i < 2 && ok; ++i) {
           if (U.n_kv[i] == 0) continue;
@@ -754,11 +769,8 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             const int npages = (min(kBlockN, U.kv_len - j * kBlockN) + 15) / 16;
             if (lane == 0) ptx::mbar_arrive_expect_tx(bar, npages * (16 * D + 16));
             __syncwarp();
-            // (pages outside the unit's visible keys may be unlisted: any page does)
             if (lane < npages) {
-              const int key = j * kBlockN + lane * 16;
-              const bool seen = key < U.key_sink || (key + 16 > U.key_lo && key < U.key_hi);
-              int id = seen ? __ldg(block_table + (size_t)U.b * max_blocks + j * (kBlockN / 16) + lane) : 0;
+              int id = kAhead ? page : look_up(j);
               if (id < 0 || id >= num_pages) {
                 atomicExch(status, kDevBadBlockTable);
                 id = 0;
@@ -845,7 +857,14 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           }
         };
         const int n_kv_max = list_size<WIN>(U);
-        if (WIN || !U.split) {
+        if constexpr (kAhead) {
+          for (int j = 0; j < n_kv_max && ok; ++j) {
+            page = page_next;
+#pragma unroll 1
+            for (int which = 0; which < 2 && ok; ++which) ok = issue_kv(which, list_tile<WIN, PARTS>(U, j));
+            page_next = j + 1 < n_kv_max ? look_up(list_tile<WIN, PARTS>(U, j + 1)) : 0;
+          }
+        } else if (WIN || !U.split) {
           for (int j = 0; j < n_kv_max && ok; ++j)
             for (int which = 0; which < 2 && ok; ++which) ok = issue_kv(which, list_tile<WIN, PARTS>(U, j));  // K then V
         } else {
