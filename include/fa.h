@@ -467,7 +467,8 @@ fa_status fa_paged_decode_e4m3(const void* q, const void* k_cache, const void* v
  * output is then unspecified.
  * Cache contents of keys that none of a sequence's queries sees are never
  * used; a NaN in a key that one query sees may reach others of its sequence.
- * Chunks of at most 32 rows (max_seqlen_q * H / Hkv) run as
+ * Chunks of at most 16 rows (max_seqlen_q * H / Hkv; 32 at d = 64 and where
+ * H / Hkv is no power of two) run as
  * fa_paged_decode_e4m3 does; larger ones on the tcgen05 path of fa_forward,
  * their K/V tiles widened to bf16 (exactly) on the way to the tensor cores.
  * Supported: H / Hkv <= 32; num_seqs*max_seqlen_q*H below 2^28.

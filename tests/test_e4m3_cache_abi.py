@@ -144,10 +144,16 @@ def test_workspace_size(lib):
     assert size(64, 1, 32, 8, 128) == (152 * 3 * 4 + 64 * 8) * 8 * 132 * 4 + 1025 * 4
     assert size(64, 4, 32, 8, 128) == (152 * 3 * 4 + 64 * 8) * 16 * 132 * 4 + 1025 * 4
     assert size(3, 1, 9, 1, 64) == (152 * 3 * 4 + 3) * 16 * 68 * 4 + 1025 * 4
-    # chunks above 32 rows: units of 256 rows, cut into parts that fill 152 SMs once (one
+    # chunks on the forward: units of 256 rows, cut into parts that fill 152 SMs once (one
     # sequence) or twice, of 256 rows x (d values of O; m, l, l_p and a gap)
     assert size(1, 64, 32, 8, 128) == 8 * 19 * 256 * 132 * 4
     assert size(4, 512, 32, 8, 64) == 0
+    # 32 rows a kv head: the forward at d = 128 for groups of a power of two, else the rows kernels
+    assert size(2, 8, 32, 8, 128) == 2 * 8 * 19 * 256 * 132 * 4
+    assert size(2, 8, 32, 8, 64) == (152 * 2 * 4 + 2 * 8) * 32 * 68 * 4 + 1025 * 4
+    assert size(2, 8, 24, 8, 128) == (152 * 2 * 4 + 2 * 8) * 32 * 132 * 4 + 1025 * 4
+    assert size(2, 1, 256, 8, 128) == (152 * 2 * 4 + 2 * 8) * 32 * 132 * 4 + 1025 * 4
+    assert size(2, 1, 512, 8, 128) == 0
     assert size(2, 65, 16, 4, 64) == 16 * 19 * 256 * 68 * 4
     for bad in ((0, 1, 32, 8, 128), (4, 0, 32, 8, 128), (4, 1, 30, 8, 128), (4, 1, 32, 8, 96),
                 (1025, 1, 32, 8, 128), (-1, 1, 8, 8, 64)):

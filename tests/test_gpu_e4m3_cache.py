@@ -12,8 +12,16 @@ from tiled_online_softmax_sm_gb300 import binding as fb
 import _e4m3 as E
 
 pytestmark = pytest.mark.gpu
-W_ROUND = 2.0 ** -11           # up to 32 rows (tokens x group) per kv head: weights rounded to f16
-P_ROUND = 2.0 ** -7 * 1.01     # more: P rounded to bf16 (2^-8) in the value product and in O's divisor
+W_ROUND = 2.0 ** -11           # the rows kernels: weights rounded to f16
+P_ROUND = 2.0 ** -7 * 1.01     # the forward: P rounded to bf16 (2^-8) in the value product and in O's divisor
+
+
+def _rounding(max_q, group, d):
+    """The weights' rounding in the kernels that the entry takes for max_q tokens of `group` heads."""
+    rows = max_q * group
+    if max_q == 1 or rows <= 16 or rows <= 32 and (d == 64 or group & (group - 1)):
+        return W_ROUND
+    return P_ROUND
 
 
 def _i32(a):
@@ -412,11 +420,12 @@ def test_decode_timeout_is_recorded_and_the_next_call_runs(monkeypatch):
 
 
 # --------------------------------------------------------------------- chunks
-def _chunk_check(c, q, new, causal=True, window=0, sinks=0, rounding=W_ROUND, what=""):
+def _chunk_check(c, q, new, causal=True, window=0, sinks=0, rounding=None, what=""):
     """With a workspace (the keys of few units are split) and without one."""
     scale = E.softmax_scale(c.d)
     cu = np.concatenate([[0], np.cumsum(new)])
     S, (Tq, H, d), mq, t = len(c.lens), q.shape, int(max(new)), c.gpu()
+    rounding = rounding or _rounding(mq, H // c.Hkv, d)
     refs = []
     qd = q.double().numpy()
     for s in range(S):
@@ -443,7 +452,7 @@ def test_short_chunks(d, group, causal):
     lens, new = [1, 16, 17, 130, 0, 300, 5], [1, 4, 3, 8, 2, 0, 8]   # the last: more queries than keys
     c = _cache(rng, lens, 2, d)
     q = E.bf16(rng.standard_normal((sum(new), 2 * group, d)))[0]
-    _chunk_check(c, q, new, causal, rounding=W_ROUND if 8 * group <= 32 else P_ROUND)
+    _chunk_check(c, q, new, causal, rounding=_rounding(8, group, d))
     assert fb.fa_get_device_status() == 0
 
 

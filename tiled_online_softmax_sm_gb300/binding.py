@@ -517,9 +517,12 @@ def _e4m3_workspace(fn, workspace, q, S, max_q, H, Hkv, d, max_blocks, stream):
     sequences, or of none; and the tensor, to be kept until the call is queued.  (None on a stream
     that is not torch's current one: a new one could be given out again before the call is done.)"""
     if workspace is None:
-        if stream is not None or max_blocks < 32 or (
-                max_q * H <= 32 * Hkv and (S * Hkv > 38 or max_blocks < 128)):
+        if stream is not None or max_blocks < 32:
             return None, 0, None
+        if S * Hkv > 38 or max_blocks < 128:   # then the rows kernels use none
+            G = H // Hkv
+            if max_q == 1 or max_q * G <= 16 or (max_q * G <= 32 and (d == 64 or G & (G - 1))):
+                return None, 0, None
         need = fa_paged_e4m3_workspace_size(S, max_q, H, Hkv, d)
         if not need:
             return None, 0, None

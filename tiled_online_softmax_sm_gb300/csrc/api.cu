@@ -694,7 +694,7 @@ fa_status fa_paged_prefill_e4m3(const void* q, const void* k_cache, const void* 
   if ((st = status_ptr(&sp)) != FA_OK) return st;
   const char* why = nullptr;
   cudaError_t e;
-  if ((long long)max_seqlen_q * (H / Hkv) <= fa::kRowsE4m3Max) {
+  if (fa::rows_e4m3_form(max_seqlen_q, H, Hkv, d)) {
     fa::PagedE4m3Params p{q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                           cu_seqlens_q, o, lse, num_seqs, total_q, max_seqlen_q, H, Hkv, d,
                           num_pages, max_blocks_per_seq, scale, causal, window, sinks, sp};

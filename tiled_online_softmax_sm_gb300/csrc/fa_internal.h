@@ -198,8 +198,21 @@ struct PagedE4m3Params {
 
 cudaError_t launch_kv_write_e4m3(const KvRowsParams& p, cudaStream_t stream);
 cudaError_t launch_kv_read_e4m3(const KvRowsParams& p, cudaStream_t stream);
-// Query rows (tokens x grouped heads) of one kv head that the split kernel takes.
+// Query rows (tokens x grouped heads) of one kv head that the rows kernels can take.
 constexpr int kRowsE4m3Max = 32;
+// Whether a call takes the rows kernels: decode always, chunks of up to 16 rows
+// a kv head, and of up to 32 except at d = 128 where the forward packs all heads
+// of a group into one tile (a power of two of them; otherwise it reads K and V
+// once more for each part of the group).  us of the rows kernels and of the
+// forward, d = 128, 8 kv heads of 4, [512, 8192] tokens: 64 x 4 new tokens 158,
+// 252; 64 x 8 322, 252; 16 x 8 104, 83; 1 x 8192 with 8 27, 25; 64 x 8 with
+// groups of 3 320, 870; d = 64, 64 x 8 158, 230.
+inline bool rows_e4m3_form(int max_q, int H, int Hkv, int d) {
+  const int g = H / Hkv;
+  const long long rows = (long long)max_q * g;
+  if (max_q == 1 || rows <= 16) return true;
+  return rows <= kRowsE4m3Max && (d == 64 || (g & (g - 1)) != 0);
+}
 size_t rows_e4m3_workspace(int num_seqs, int max_q, int H, int Hkv, int d);
 cudaError_t launch_rows_e4m3(const PagedE4m3Params& p, cudaStream_t stream, const char** why);
 cudaError_t launch_fwd_f32(const FwdParams& p, cudaStream_t stream);

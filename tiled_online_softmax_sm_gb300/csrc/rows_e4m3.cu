@@ -1111,8 +1111,8 @@ size_t stream_bytes(long long units) {
 
 size_t rows_e4m3_workspace(int num_seqs, int max_q, int H, int Hkv, int d) {
   const long long rows = (long long)max_q * (H / Hkv), units = (long long)num_seqs * Hkv;
-  if (rows > kRowsE4m3Max) return cache_parts_bytes(num_seqs, max_q, H, Hkv, d);
-  if (num_seqs > kMaxSeqs) return 0;
+  if (!rows_e4m3_form(max_q, H, Hkv, d)) return cache_parts_bytes(num_seqs, max_q, H, Hkv, d);
+  if (num_seqs > kMaxSeqs || rows > kRowsE4m3Max) return 0;
   if (d == 128)
     return rows <= 8 ? stream_bytes<128, 1>(units)
                      : rows <= 16 ? stream_bytes<128, 2>(units) : stream_bytes<128, 4>(units);
