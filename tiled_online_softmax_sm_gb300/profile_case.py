@@ -12,6 +12,11 @@ Workloads (sizes as in the bench and the parity tests):
   fp8_c3     causal e4m3 forward, B=1 H=32 n=m=8192 d=128
   prefill_c4 paged prefill: 512-token chunks of 16 sequences of the decode pool
   fwd_f32    fp32 forward, n=m=256 d=64
+  write_e4m3, read_e4m3  the decode pool's K/V rows into and out of an e4m3 paged cache
+  decode_e4m3  paged grouped-head decode over it, 64 sequences, H=32 Hkv=8
+  draft_e4m3   4 new tokens of 16 sequences over an e4m3 cache
+  prefill_e4m3 512-token chunks of those sequences
+  window_c3    causal bf16 forward, n=m=8192 H=32 d=128, window 1024 with 4 sinks
 Inputs come from the same seeded generators; nothing is checked here.
 """
 from __future__ import annotations
@@ -30,6 +35,28 @@ def _dev(t):
     if t.dtype == "bf16":
         return torch.from_numpy(t.data.view(np.int16)).cuda().view(torch.bfloat16)
     return torch.from_numpy(t.data).cuda()
+
+
+def e4m3_cache(seed: int, S: int, Hkv: int = 8, d: int = 128):
+    """Random K/V rows of S sequences of [512, 8192] tokens, an empty e4m3 paged cache with room for
+    them (randomly ordered pages, table 512 wide), and the sequences' lengths and offsets."""
+    g = torch.Generator(device="cuda").manual_seed(I.BASE_SEED)
+    lens = I.uniform_lengths(seed, S, 512, 8192)
+    need = (lens + 15) // 16
+    pages, T = int(need.sum()), int(lens.sum())
+    table = np.full((S, 512), -1, np.int32)
+    ids = np.random.default_rng(seed).permutation(pages).astype(np.int32)
+    for s, at in enumerate(np.cumsum(need) - need):
+        table[s, :need[s]] = ids[at:at + need[s]]
+    k, v = (torch.randn((T, Hkv, d), device="cuda", generator=g).bfloat16() for _ in range(2))
+    cache = [torch.zeros((pages, Hkv, 16, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    cache += [torch.zeros((pages, Hkv, 16), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    cache += [torch.from_numpy(table).cuda(), torch.from_numpy(lens.astype(np.int32)).cuda()]
+    return k, v, cache, offsets(lens), lens
+
+
+def offsets(n):
+    return torch.from_numpy(np.concatenate([[0], np.cumsum(n)]).astype(np.int32)).cuda()
 
 
 def make(name: str, splits: int = 8):
@@ -94,6 +121,22 @@ def make(name: str, splits: int = 8):
         lse = torch.empty((c.B, c.H, c.n), dtype=torch.float32, device="cuda")
         return lambda: fb.fa_forward_f32(q, k, v, o, lse, c.B, c.H, c.Hkv, c.n, c.m, c.d, c.dv,
                                          c.scale, 0)
+    if name in ("write_e4m3", "read_e4m3", "decode_e4m3", "draft_e4m3", "prefill_e4m3"):
+        S, seed, n = {"draft_e4m3": (16, 63, 4), "prefill_e4m3": (16, 63, 512)}.get(
+            name, (64, I.BASE_SEED, 1))
+        k, v, cache, cu, lens = e4m3_cache(seed, S)
+        write = lambda: fb.paged_kv_write_e4m3(k, v, *cache, cu)  # noqa: E731
+        write()
+        nq = np.minimum(lens, n)
+        q = torch.randn((int(nq.sum()), 32, 128), device="cuda").bfloat16()
+        sc, cuq = I.fp32_scale(128), offsets(nq)
+        return {"write_e4m3": write,
+                "read_e4m3": lambda: fb.paged_kv_read_e4m3(*cache, cu, int(lens.sum())),
+                "decode_e4m3": lambda: fb.paged_decode_e4m3(q, *cache, sc)}.get(
+                    name, lambda: fb.paged_prefill_e4m3(q, *cache, cuq, n, sc))
+    if name == "window_c3":
+        q, k, v = (torch.randn((1, 8192, 32, 128), device="cuda").bfloat16() for _ in range(3))
+        return lambda: fb.forward_window(q, k, v, I.fp32_scale(128), 1024, 4)
     raise SystemExit(f"unknown workload {name}")
 
 

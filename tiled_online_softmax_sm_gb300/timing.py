@@ -35,6 +35,7 @@ import torch
 
 from . import binding as fb
 from . import inputs as I
+from .profile_case import e4m3_cache, offsets
 
 
 def _dev(t):
@@ -175,19 +176,8 @@ def _e4m3_cache_rows(iters, warmup):
     g = torch.Generator(device="cuda").manual_seed(I.BASE_SEED)
     H, Hkv, d = 32, 8, 128
     for S, seed, chunk in ((64, I.BASE_SEED, 1), (16, 63, 512)):
-        lens = I.uniform_lengths(seed, S, 512, 8192)
-        need = (lens + 15) // 16
-        pages, T = int(need.sum()), int(lens.sum())
-        bt = np.full((S, 512), -1, np.int32)
-        ids = np.random.default_rng(seed).permutation(pages).astype(np.int32)
-        for s, at in enumerate(np.cumsum(need) - need):
-            bt[s, :need[s]] = ids[at:at + need[s]]
-        bt, sl = torch.from_numpy(bt).cuda(), torch.from_numpy(lens.astype(np.int32)).cuda()
-        cu = torch.from_numpy(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)).cuda()
-        k, v = (torch.randn((T, Hkv, d), device="cuda", generator=g).bfloat16() for _ in range(2))
-        cache = [torch.zeros((pages, Hkv, 16, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
-        cache += [torch.zeros((pages, Hkv, 16), dtype=torch.uint8, device="cuda") for _ in range(2)]
-        cache += [bt, sl]
+        k, v, cache, cu, lens = e4m3_cache(seed, S, Hkv, d)
+        T = int(lens.sum())
         ms = _median_ms(lambda: fb.paged_kv_write_e4m3(k, v, *cache, cu), iters, warmup)
         if chunk == 1:
             out.append((f"e4m3 cache write {T} tokens Hkv=8 d=128", ms, T * Hkv * 2 * (3 * d + 1) / (ms * 1e6), "GB/s"))
@@ -198,7 +188,7 @@ def _e4m3_cache_rows(iters, warmup):
             out.append(("e4m3 paged decode 64 seqs H=32 Hkv=8", ms, T * Hkv * (2 * d + 2) / (ms * 1e6), "GB/s"))
         else:
             ql = np.minimum(lens, chunk)
-            cuq = torch.from_numpy(np.concatenate([[0], np.cumsum(ql)]).astype(np.int32)).cuda()
+            cuq = offsets(ql)
             q = torch.randn((int(ql.sum()), H, d), device="cuda", generator=g).bfloat16()
             ms = _median_ms(lambda: fb.paged_prefill_e4m3(q, *cache, cuq, chunk, I.fp32_scale(d)), iters, warmup)
             fl = sum(4.0 * int(nq) * d * H * (int(L) - int(nq) / 2) for nq, L in zip(ql, lens))
