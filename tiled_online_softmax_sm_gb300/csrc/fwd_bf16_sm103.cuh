@@ -97,6 +97,13 @@ constexpr float kLn2 = 0.6931471805599453f;
 // does not depend on the threshold; 12, 16 and 24 measured the same speed.
 constexpr float kRescaleThreshold = 8.0f;
 constexpr float kRaiseSum = 256.0f;   // 2^kRescaleThreshold
+// WIN instances (bf16 P, whose exponent reaches as far as fp32's) take a higher
+// one: raises are rare on data with a few long keys, and with them the passes
+// over a tile for its max.  4 x 2048-token chunks over the e4m3 cache, window
+// 2048, key norms spread by 2^(0.3 N(0, 1)): 535-607 us from one draw of the data
+// to the next with 8, 510-512 with 24.
+constexpr float kRescaleThresholdWin = 24.0f;
+constexpr float kRaiseSumWin = 16777216.0f;
 
 // Tile geometry for head dim D and operand type (bf16, or e4m3 with FP8).
 template <int D, bool FP8 = false, bool KV8 = false>
@@ -1330,7 +1337,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           const float ref = m_ref == -INFINITY ? 0.f : m_ref;
           if constexpr (FP8) lsum = exp_pass<true>(sr, s_col, sc2, ptx::f2_bits(-ref, -ref));
           else lsum = exp_pack_bf16<false>(sr, s_col, sc2, ptx::f2_bits(-ref, -ref), pp);
-          full = __any_sync(0xffffffffu, !(lsum <= kRaiseSum) || m_ref == -INFINITY);
+          full = __any_sync(0xffffffffu, !(lsum <= (WIN ? kRaiseSumWin : kRaiseSum)) || m_ref == -INFINITY);
           max_first = full;
           if constexpr (!FP8) {
             if (full) load_s(true);
@@ -1340,7 +1347,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         if (full) {
           const float m_tile = (have_mred ? mred : row_max(sr)) * scale_log2;   // scale > 0: max commutes with it
           const bool raise =
-              m_tile > m_ref + kRescaleThreshold || (m_ref == -INFINITY && m_tile > -INFINITY);
+              m_tile > m_ref + (WIN ? kRescaleThresholdWin : kRescaleThreshold) || (m_ref == -INFINITY && m_tile > -INFINITY);
           float alpha = 1.f;
           if (raise) {
             alpha = m_ref == -INFINITY ? 1.f : ptx::ex2(m_ref - m_tile);
