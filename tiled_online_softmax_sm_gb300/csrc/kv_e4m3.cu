@@ -115,42 +115,61 @@ kv_write_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __rest
   uint8_t* scales = is_v ? v_scale : k_scale;
   const long long row0 = (slot / kPage) * Hkv * kPage + slot % kPage;
 
+  const size_t first = (size_t)(row0 + (long long)(h0 + sub) * kPage);   // step 0's cache row
+  static_assert(kSteps % 2 == 0, "steps are taken two at a time");
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    // magnitudes as 15-bit integers order like the values; adding 0x80 carries
-    // into bit 15 exactly for inf and NaN (magnitude >= 0x7f80)
-    uint32_t mag[4], odd = 0u;
+  for (int i = 0; i < kSteps; i += 2) {
+    uint32_t w[2][4] = {{x[i].x, x[i].y, x[i].z, x[i].w},
+                        {x[i + 1].x, x[i + 1].y, x[i + 1].z, x[i + 1].w}};
+    // Magnitudes as 15-bit integers order like the values.  The maxima of the
+    // two steps' rows share a register on their way through the warp.
+    auto row_maxima = [&]() __attribute__((always_inline)) -> uint32_t {
+      uint32_t m[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      mag[e] = w[e] & 0x7fff7fffu;
-      odd |= (mag[e] + 0x00800080u) & 0x80008000u;
+      for (int r = 0; r < 2; ++r)
+        m[r] = __vmaxu2(__vmaxu2(w[r][0] & 0x7fff7fffu, w[r][1] & 0x7fff7fffu),
+                        __vmaxu2(w[r][2] & 0x7fff7fffu, w[r][3] & 0x7fff7fffu));
+      uint32_t mx = __vmaxu2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+#pragma unroll
+      for (int off = kLanes / 2; off > 0; off >>= 1)
+        mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      return mx;
+    };
+    uint32_t mx = row_maxima();
+    // (adding 0x80 carries into bit 15 exactly for magnitudes of inf and NaN)
+    if (__any_sync(0xffffffffu, ((mx + 0x00800080u) & 0x80008000u) != 0u)) {
+      // rare: inf and NaN become NaN and stay out of the maximum
+      uint32_t nan[2][4] = {};
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if ((w[r][e] & 0x7fffu) >= 0x7f80u) { w[r][e] &= 0xffff0000u; nan[r][e] |= 0x7fffu; }
+          if (((w[r][e] >> 16) & 0x7fffu) >= 0x7f80u) { w[r][e] &= 0xffffu; nan[r][e] |= 0x7fff0000u; }
+        }
+      mx = row_maxima();
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[r][e] |= nan[r][e];
     }
-    if (odd) {   // rare: inf and NaN become NaN and stay out of the maximum
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if ((mag[e] & 0x7fffu) >= 0x7f80u) { w[e] |= 0x7fffu; mag[e] &= 0x7fff0000u; }
-        if ((mag[e] >> 16) >= 0x7f80u) { w[e] |= 0x7fff0000u; mag[e] &= 0x7fffu; }
+    for (int r = 0; r < 2; ++r) {
+      const int amax = (int)(r == 0 ? mx & 0xffffu : mx >> 16);
+      const int b = max(0, (amax >> 7) - 8 + ((amax & 0x7f) > 0x60 ? 1 : 0));
+      const float inv = __uint_as_float((uint32_t)(254 - b) << 23);   // 2^-(b - 127), exact
+      uint32_t code[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        code[e] = ptx::pack_e4m3x2(__uint_as_float(w[r][e] << 16) * inv,
+                                   __uint_as_float(w[r][e] & 0xffff0000u) * inv);
+      const int h = h0 + (i + r) * kRows + sub;
+      const size_t row = first + (size_t)((i + r) * kRows * kPage);
+      if (h < Hkv && FA_IN_BOUNDS(row, (size_t)num_pages * Hkv * kPage, status)) {
+        *reinterpret_cast<uint2*>(cache + row * D + col) =
+            make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+        if (col == 0) scales[row] = (uint8_t)b;
       }
-    }
-    uint32_t mx = __vmaxu2(__vmaxu2(mag[0], mag[1]), __vmaxu2(mag[2], mag[3]));
-#pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1)
-      mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    const int amax = (int)max(mx & 0xffffu, mx >> 16);
-    const int b = max(0, (amax >> 7) - 8 + ((amax & 0x7f) > 0x60 ? 1 : 0));
-    const float inv = __uint_as_float((uint32_t)(254 - b) << 23);   // 2^-(b - 127), exact
-    uint32_t code[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      code[e] = ptx::pack_e4m3x2(__uint_as_float(w[e] << 16) * inv,
-                                 __uint_as_float(w[e] & 0xffff0000u) * inv);
-    const int h = h0 + i * kRows + sub;
-    const size_t row = (size_t)(row0 + (long long)h * kPage);
-    if (h < Hkv && FA_IN_BOUNDS(row, (size_t)num_pages * Hkv * kPage, status)) {
-      *reinterpret_cast<uint2*>(cache + row * D + col) =
-          make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
-      if (col == 0) scales[row] = (uint8_t)b;
     }
   }
 }
