@@ -13,7 +13,7 @@
 //     b = max(0, E - 8 + (f > 0x60)).
 // inf and NaN do not enter the maximum; e4m3 has no inf, so both become its NaN.
 //
-// Both kernels: one warp per (token, K or V, up to 8 heads).  A row is d/8
+// Both kernels: one warp per (token, K or V, up to 8 heads; both at D = 64).  A row is d/8
 // lanes of 16 bytes of bf16 (write) or d/16 lanes of 16 codes (read), so a
 // warp's loads and stores are whole 32-byte sectors.  The token's sequence is
 // found by a 32-way search of cu_seqlens (two rounds for up to 1024
@@ -32,6 +32,11 @@ namespace {
 constexpr int kPage = 16;
 constexpr int kHeads = 8;    // heads per warp
 constexpr int kWarps = 4;
+
+// How many of K and V a warp takes: both at D = 64, where one's heads are a
+// short piece of work next to finding the token's place.
+template <int D>
+constexpr int kPerWarp = D == 64 ? 2 : 1;
 
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
   uint4 v;
@@ -89,36 +94,37 @@ kv_write_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __rest
                 int total, int Hkv, int num_pages, int max_blocks, int* status) {
   constexpr int kLanes = D / 8;            // lanes per row
   constexpr int kRows = 32 / kLanes;       // rows per warp step
-  constexpr int kSteps = kHeads / kRows;
+  constexpr int kSteps = kHeads / kRows;   // of K or V
+  constexpr int kAll = kPerWarp<D> * kSteps;
+  constexpr int kItems = 2 / kPerWarp<D>;
   const int lane = threadIdx.x & 31;
   const int blocks_h = (Hkv + kHeads - 1) / kHeads;
   const uint32_t item = blockIdx.x * (uint32_t)kWarps + (threadIdx.x >> 5);   // below 2^32
-  const uint32_t row_t = item / (uint32_t)(2 * blocks_h);
+  const uint32_t row_t = item / (uint32_t)(kItems * blocks_h);
   if (row_t >= (uint32_t)total) return;
   const int t = (int)row_t;
-  const int part = (int)(item - row_t * (uint32_t)(2 * blocks_h));
-  const bool is_v = part >= blocks_h;
+  const int part = (int)(item - row_t * (uint32_t)(kItems * blocks_h));
+  const bool is_v = part >= blocks_h;      // (both at once: false, then the second half)
   const int h0 = (is_v ? part - blocks_h : part) * kHeads;
   const int sub = lane / kLanes, col = (lane % kLanes) * 8;
-  const __nv_bfloat16* src = (is_v ? v + t * v_stride : k + t * k_stride) + col;
-
-  uint4 x[kSteps];
+  uint4 x[kAll];
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int h = h0 + i * kRows + sub;
+  for (int i = 0; i < kAll; ++i) {
+    const bool v_row = is_v || i >= kSteps;
+    const __nv_bfloat16* src = (v_row ? v + t * v_stride : k + t * k_stride) + col;
+    const int h = h0 + i % kSteps * kRows + sub;
     x[i] = h < Hkv ? ld_stream(src + h * D) : make_uint4(0u, 0u, 0u, 0u);
   }
   const long long slot = token_slot(t, cu, seq_lens, block_table, num_seqs, total, max_blocks,
                                     num_pages, status, lane);
   if (slot < 0) return;
-  uint8_t* cache = is_v ? v_cache : k_cache;
-  uint8_t* scales = is_v ? v_scale : k_scale;
   const long long row0 = (slot / kPage) * Hkv * kPage + slot % kPage;
-
   const size_t first = (size_t)(row0 + (long long)(h0 + sub) * kPage);   // step 0's cache row
   static_assert(kSteps % 2 == 0, "steps are taken two at a time");
 #pragma unroll
-  for (int i = 0; i < kSteps; i += 2) {
+  for (int i = 0; i < kAll; i += 2) {
+    uint8_t* cache = is_v || i >= kSteps ? v_cache : k_cache;
+    uint8_t* scales = is_v || i >= kSteps ? v_scale : k_scale;
     uint32_t w[2][4] = {{x[i].x, x[i].y, x[i].z, x[i].w},
                         {x[i + 1].x, x[i + 1].y, x[i + 1].z, x[i + 1].w}};
     // Magnitudes as 15-bit integers order like the values.  The maxima of the
@@ -163,8 +169,9 @@ kv_write_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __rest
       for (int e = 0; e < 4; ++e)
         code[e] = ptx::pack_e4m3x2(__uint_as_float(w[r][e] << 16) * inv,
                                    __uint_as_float(w[r][e] & 0xffff0000u) * inv);
-      const int h = h0 + (i + r) * kRows + sub;
-      const size_t row = first + (size_t)((i + r) * kRows * kPage);
+      const int step = (i + r) % kSteps;
+      const int h = h0 + step * kRows + sub;
+      const size_t row = first + (size_t)(step * kRows * kPage);
       if (h < Hkv && FA_IN_BOUNDS(row, (size_t)num_pages * Hkv * kPage, status)) {
         *reinterpret_cast<uint2*>(cache + row * D + col) =
             make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
@@ -184,36 +191,38 @@ kv_read_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ 
                int max_blocks, int* status) {
   constexpr int kLanes = D / 16;           // lanes per row, 16 codes each
   constexpr int kRows = 32 / kLanes;
-  constexpr int kSteps = kHeads / kRows;
+  constexpr int kSteps = kHeads / kRows;   // of K or V
+  constexpr int kAll = kPerWarp<D> * kSteps;
+  constexpr int kItems = 2 / kPerWarp<D>;
   const int lane = threadIdx.x & 31;
   const int blocks_h = (Hkv + kHeads - 1) / kHeads;
   const uint32_t item = blockIdx.x * (uint32_t)kWarps + (threadIdx.x >> 5);   // below 2^32
-  const uint32_t row_t = item / (uint32_t)(2 * blocks_h);
+  const uint32_t row_t = item / (uint32_t)(kItems * blocks_h);
   if (row_t >= (uint32_t)total) return;
   const int t = (int)row_t;
-  const int part = (int)(item - row_t * (uint32_t)(2 * blocks_h));
-  const bool is_v = part >= blocks_h;
+  const int part = (int)(item - row_t * (uint32_t)(kItems * blocks_h));
+  const bool is_v = part >= blocks_h;      // (both at once: false, then the second half)
   const int h0 = (is_v ? part - blocks_h : part) * kHeads;
   const int sub = lane / kLanes, col = (lane % kLanes) * 16;
   const long long slot = token_slot(t, cu, seq_lens, block_table, num_seqs, total, max_blocks,
                                     num_pages, status, lane);
   if (slot < 0) return;
-  const uint8_t* cache = is_v ? v_cache : k_cache;
-  const uint8_t* scales = is_v ? v_scale : k_scale;
-  __nv_bfloat16* out = is_v ? v : k;
   const long long row0 = (slot / kPage) * Hkv * kPage + slot % kPage;
-  uint4 x[kSteps];
-  uint32_t b[kSteps];
+  uint4 x[kAll];
+  uint32_t b[kAll];
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int h = h0 + i * kRows + sub;
+  for (int i = 0; i < kAll; ++i) {
+    const uint8_t* cache = is_v || i >= kSteps ? v_cache : k_cache;
+    const uint8_t* scales = is_v || i >= kSteps ? v_scale : k_scale;
+    const int h = h0 + i % kSteps * kRows + sub;
     const size_t row = (size_t)(row0 + (long long)(h < Hkv ? h : 0) * kPage);
     x[i] = ld_stream(cache + row * D + col);
     b[i] = __ldg(scales + row);
   }
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int h = h0 + i * kRows + sub;
+  for (int i = 0; i < kAll; ++i) {
+    __nv_bfloat16* out = is_v || i >= kSteps ? v : k;
+    const int h = h0 + i % kSteps * kRows + sub;
     const float s = ptx::exp2_byte(b[i]);
     const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
     uint32_t r[8];
@@ -232,10 +241,16 @@ kv_read_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ 
   }
 }
 
+// Warps of a launch.
+long long rows_items(const KvRowsParams& p) {
+  const int per_token = p.d == 64 ? 2 / kPerWarp<64> : 2 / kPerWarp<128>;
+  return (long long)p.total * per_token * ((p.Hkv + kHeads - 1) / kHeads);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_write_e4m3(const KvRowsParams& p, cudaStream_t stream) {
-  const long long items = (long long)p.total * 2 * ((p.Hkv + kHeads - 1) / kHeads);
+  const long long items = rows_items(p);
   auto kernel = p.d == 128 ? kv_write_kernel<128> : kv_write_kernel<64>;
   kernel<<<(unsigned)((items + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(
       static_cast<const __nv_bfloat16*>(p.k), static_cast<const __nv_bfloat16*>(p.v), p.k_stride,
@@ -246,7 +261,7 @@ cudaError_t launch_kv_write_e4m3(const KvRowsParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_kv_read_e4m3(const KvRowsParams& p, cudaStream_t stream) {
-  const long long items = (long long)p.total * 2 * ((p.Hkv + kHeads - 1) / kHeads);
+  const long long items = rows_items(p);
   auto kernel = p.d == 128 ? kv_read_kernel<128> : kv_read_kernel<64>;
   kernel<<<(unsigned)((items + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(
       static_cast<const uint8_t*>(p.k_cache), static_cast<const uint8_t*>(p.v_cache),
