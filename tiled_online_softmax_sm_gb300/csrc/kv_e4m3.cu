@@ -13,12 +13,13 @@
 //     b = max(0, E - 8 + (f > 0x60)).
 // inf and NaN do not enter the maximum; e4m3 has no inf, so both become its NaN.
 //
-// Both kernels: one warp per (token, K or V, up to 8 heads; both at D = 64).  A row is d/8
+// Both kernels: one warp per (token, up to 8 heads).  A row is d/8
 // lanes of 16 bytes of bf16 (write) or d/16 lanes of 16 codes (read), so a
 // warp's loads and stores are whole 32-byte sectors.  The token's sequence is
 // found by a 32-way search of cu_seqlens (two rounds for up to 1024
 // sequences); in the write kernel the row loads are in flight behind it.
-// Bound by memory traffic: 3 bytes a value plus one byte a row.
+// Bound by memory traffic: 3 bytes a value plus one byte a row; 6.4 TB/s both ways
+// (295725 tokens, 8 heads, d = 128: 0.94 of a plain copy).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -30,13 +31,17 @@ namespace fa {
 namespace {
 
 constexpr int kPage = 16;
-constexpr int kHeads = 8;    // heads per warp
 constexpr int kWarps = 4;
 
-// How many of K and V a warp takes: both at D = 64, where one's heads are a
-// short piece of work next to finding the token's place.
-template <int D>
-constexpr int kPerWarp = D == 64 ? 2 : 1;
+// A warp's share: HEADS rows of K and of V.
+template <int D, int HEADS, bool WRITE>
+struct Share {
+  static constexpr int kLanes = WRITE ? D / 8 : D / 16;     // lanes per row
+  static constexpr int kRows = 32 / kLanes;                 // rows per warp step
+  static constexpr int kSteps = HEADS / kRows;              // of K, and then as many of V
+  static constexpr int kAll = 2 * kSteps;
+  static_assert(HEADS % kRows == 0, "whole steps");
+};
 
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
   uint4 v;
@@ -84,7 +89,7 @@ __device__ __forceinline__ long long token_slot(int t, const int* __restrict__ c
 }
 
 // Lanes of row `sub` hold 8 values each (4 words of bf16 pairs).
-template <int D>
+template <int D, int HEADS>
 __global__ void __launch_bounds__(kWarps * 32)
 kv_write_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                 long long k_stride, long long v_stride, uint8_t* __restrict__ k_cache,
@@ -92,26 +97,20 @@ kv_write_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __rest
                 uint8_t* __restrict__ v_scale, const int* __restrict__ block_table,
                 const int* __restrict__ seq_lens, const int* __restrict__ cu, int num_seqs,
                 int total, int Hkv, int num_pages, int max_blocks, int* status) {
-  constexpr int kLanes = D / 8;            // lanes per row
-  constexpr int kRows = 32 / kLanes;       // rows per warp step
-  constexpr int kSteps = kHeads / kRows;   // of K or V
-  constexpr int kAll = kPerWarp<D> * kSteps;
-  constexpr int kItems = 2 / kPerWarp<D>;
+  using P = Share<D, HEADS, true>;
+  constexpr int kLanes = P::kLanes, kRows = P::kRows, kSteps = P::kSteps, kAll = P::kAll;
   const int lane = threadIdx.x & 31;
-  const int blocks_h = (Hkv + kHeads - 1) / kHeads;
+  const int blocks_h = (Hkv + HEADS - 1) / HEADS;
   const uint32_t item = blockIdx.x * (uint32_t)kWarps + (threadIdx.x >> 5);   // below 2^32
-  const uint32_t row_t = item / (uint32_t)(kItems * blocks_h);
+  const uint32_t row_t = item / (uint32_t)blocks_h;
   if (row_t >= (uint32_t)total) return;
   const int t = (int)row_t;
-  const int part = (int)(item - row_t * (uint32_t)(kItems * blocks_h));
-  const bool is_v = part >= blocks_h;      // (both at once: false, then the second half)
-  const int h0 = (is_v ? part - blocks_h : part) * kHeads;
+  const int h0 = (int)(item - row_t * (uint32_t)blocks_h) * HEADS;
   const int sub = lane / kLanes, col = (lane % kLanes) * 8;
   uint4 x[kAll];
 #pragma unroll
   for (int i = 0; i < kAll; ++i) {
-    const bool v_row = is_v || i >= kSteps;
-    const __nv_bfloat16* src = (v_row ? v + t * v_stride : k + t * k_stride) + col;
+    const __nv_bfloat16* src = (i >= kSteps ? v + t * v_stride : k + t * k_stride) + col;
     const int h = h0 + i % kSteps * kRows + sub;
     x[i] = h < Hkv ? ld_stream(src + h * D) : make_uint4(0u, 0u, 0u, 0u);
   }
@@ -120,11 +119,8 @@ kv_write_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __rest
   if (slot < 0) return;
   const long long row0 = (slot / kPage) * Hkv * kPage + slot % kPage;
   const size_t first = (size_t)(row0 + (long long)(h0 + sub) * kPage);   // step 0's cache row
-  static_assert(kSteps % 2 == 0, "steps are taken two at a time");
 #pragma unroll
   for (int i = 0; i < kAll; i += 2) {
-    uint8_t* cache = is_v || i >= kSteps ? v_cache : k_cache;
-    uint8_t* scales = is_v || i >= kSteps ? v_scale : k_scale;
     uint32_t w[2][4] = {{x[i].x, x[i].y, x[i].z, x[i].w},
                         {x[i + 1].x, x[i + 1].y, x[i + 1].z, x[i + 1].w}};
     // Magnitudes as 15-bit integers order like the values.  The maxima of the
@@ -169,6 +165,8 @@ kv_write_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __rest
       for (int e = 0; e < 4; ++e)
         code[e] = ptx::pack_e4m3x2(__uint_as_float(w[r][e] << 16) * inv,
                                    __uint_as_float(w[r][e] & 0xffff0000u) * inv);
+      uint8_t* cache = i + r >= kSteps ? v_cache : k_cache;
+      uint8_t* scales = i + r >= kSteps ? v_scale : k_scale;
       const int step = (i + r) % kSteps;
       const int h = h0 + step * kRows + sub;
       const size_t row = first + (size_t)(step * kRows * kPage);
@@ -181,7 +179,7 @@ kv_write_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __rest
   }
 }
 
-template <int D>
+template <int D, int HEADS>
 __global__ void __launch_bounds__(kWarps * 32)
 kv_read_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
                const uint8_t* __restrict__ k_scale, const uint8_t* __restrict__ v_scale,
@@ -189,20 +187,15 @@ kv_read_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ 
                const int* __restrict__ cu, __nv_bfloat16* __restrict__ k,
                __nv_bfloat16* __restrict__ v, int num_seqs, int total, int Hkv, int num_pages,
                int max_blocks, int* status) {
-  constexpr int kLanes = D / 16;           // lanes per row, 16 codes each
-  constexpr int kRows = 32 / kLanes;
-  constexpr int kSteps = kHeads / kRows;   // of K or V
-  constexpr int kAll = kPerWarp<D> * kSteps;
-  constexpr int kItems = 2 / kPerWarp<D>;
+  using P = Share<D, HEADS, false>;
+  constexpr int kLanes = P::kLanes, kRows = P::kRows, kSteps = P::kSteps, kAll = P::kAll;
   const int lane = threadIdx.x & 31;
-  const int blocks_h = (Hkv + kHeads - 1) / kHeads;
+  const int blocks_h = (Hkv + HEADS - 1) / HEADS;
   const uint32_t item = blockIdx.x * (uint32_t)kWarps + (threadIdx.x >> 5);   // below 2^32
-  const uint32_t row_t = item / (uint32_t)(kItems * blocks_h);
+  const uint32_t row_t = item / (uint32_t)blocks_h;
   if (row_t >= (uint32_t)total) return;
   const int t = (int)row_t;
-  const int part = (int)(item - row_t * (uint32_t)(kItems * blocks_h));
-  const bool is_v = part >= blocks_h;      // (both at once: false, then the second half)
-  const int h0 = (is_v ? part - blocks_h : part) * kHeads;
+  const int h0 = (int)(item - row_t * (uint32_t)blocks_h) * HEADS;
   const int sub = lane / kLanes, col = (lane % kLanes) * 16;
   const long long slot = token_slot(t, cu, seq_lens, block_table, num_seqs, total, max_blocks,
                                     num_pages, status, lane);
@@ -212,8 +205,8 @@ kv_read_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ 
   uint32_t b[kAll];
 #pragma unroll
   for (int i = 0; i < kAll; ++i) {
-    const uint8_t* cache = is_v || i >= kSteps ? v_cache : k_cache;
-    const uint8_t* scales = is_v || i >= kSteps ? v_scale : k_scale;
+    const uint8_t* cache = i >= kSteps ? v_cache : k_cache;
+    const uint8_t* scales = i >= kSteps ? v_scale : k_scale;
     const int h = h0 + i % kSteps * kRows + sub;
     const size_t row = (size_t)(row0 + (long long)(h < Hkv ? h : 0) * kPage);
     x[i] = ld_stream(cache + row * D + col);
@@ -221,7 +214,7 @@ kv_read_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ 
   }
 #pragma unroll
   for (int i = 0; i < kAll; ++i) {
-    __nv_bfloat16* out = is_v || i >= kSteps ? v : k;
+    __nv_bfloat16* out = i >= kSteps ? v : k;
     const int h = h0 + i % kSteps * kRows + sub;
     const float s = ptx::exp2_byte(b[i]);
     const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -241,34 +234,47 @@ kv_read_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ 
   }
 }
 
-// Warps of a launch.
-long long rows_items(const KvRowsParams& p) {
-  const int per_token = p.d == 64 ? 2 / kPerWarp<64> : 2 / kPerWarp<128>;
-  return (long long)p.total * per_token * ((p.Hkv + kHeads - 1) / kHeads);
+template <int HEADS>
+unsigned blocks(const KvRowsParams& p) {
+  const long long items = (long long)p.total * ((p.Hkv + HEADS - 1) / HEADS);
+  return (unsigned)((items + kWarps - 1) / kWarps);
 }
 
-}  // namespace
-
-cudaError_t launch_kv_write_e4m3(const KvRowsParams& p, cudaStream_t stream) {
-  const long long items = rows_items(p);
-  auto kernel = p.d == 128 ? kv_write_kernel<128> : kv_write_kernel<64>;
-  kernel<<<(unsigned)((items + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(
+template <int D, int HEADS>
+void write(const KvRowsParams& p, cudaStream_t stream) {
+  kv_write_kernel<D, HEADS><<<blocks<HEADS>(p), kWarps * 32, 0, stream>>>(
       static_cast<const __nv_bfloat16*>(p.k), static_cast<const __nv_bfloat16*>(p.v), p.k_stride,
       p.v_stride, static_cast<uint8_t*>(p.k_cache), static_cast<uint8_t*>(p.v_cache),
       static_cast<uint8_t*>(p.k_scale), static_cast<uint8_t*>(p.v_scale), p.block_table,
       p.seq_lens, p.cu, p.num_seqs, p.total, p.Hkv, p.num_pages, p.max_blocks, p.status);
-  return cudaGetLastError();
 }
 
-cudaError_t launch_kv_read_e4m3(const KvRowsParams& p, cudaStream_t stream) {
-  const long long items = rows_items(p);
-  auto kernel = p.d == 128 ? kv_read_kernel<128> : kv_read_kernel<64>;
-  kernel<<<(unsigned)((items + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(
+template <int D, int HEADS>
+void read(const KvRowsParams& p, cudaStream_t stream) {
+  kv_read_kernel<D, HEADS><<<blocks<HEADS>(p), kWarps * 32, 0, stream>>>(
       static_cast<const uint8_t*>(p.k_cache), static_cast<const uint8_t*>(p.v_cache),
       static_cast<const uint8_t*>(p.k_scale), static_cast<const uint8_t*>(p.v_scale),
       p.block_table, p.seq_lens, p.cu, static_cast<__nv_bfloat16*>(const_cast<void*>(p.k)),
       static_cast<__nv_bfloat16*>(const_cast<void*>(p.v)), p.num_seqs, p.total, p.Hkv,
       p.num_pages, p.max_blocks, p.status);
+}
+
+}  // namespace
+
+// Heads per warp: 512 values of K and of V (four heads at d = 128, eight at
+// d = 64), or half as many where the other half of the lanes would have no row.
+// us for 64 x [512, 8192] tokens, with one or both of K and V a warp and eight
+// heads, and with this: d = 128, 8 heads, write 264, 263, read 270, 265; 2
+// heads, write 210, 92, read 176, 93; d = 64, 8 heads, write 174, 133, read 166,
+// 149; 2 heads, write 169, 91, read 141, 91.
+cudaError_t launch_kv_write_e4m3(const KvRowsParams& p, cudaStream_t stream) {
+  if (p.d == 128) p.Hkv <= 2 ? write<128, 2>(p, stream) : write<128, 4>(p, stream);
+  else (p.Hkv - 1) % 8 < 4 ? write<64, 4>(p, stream) : write<64, 8>(p, stream);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_read_e4m3(const KvRowsParams& p, cudaStream_t stream) {
+  p.d == 128 ? read<128, 4>(p, stream) : read<64, 8>(p, stream);
   return cudaGetLastError();
 }
 
