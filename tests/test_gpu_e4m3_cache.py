@@ -704,6 +704,41 @@ def test_captured_step_replays_and_streams_do_not_mix():
     assert fb.fa_get_device_status() == 0
 
 
+@pytest.mark.parametrize("Hkv", [1, 2, 3, 4, 5, 8, 12])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("offset", [0, 8])
+def test_heads_and_alignments_of_the_rows(Hkv, d, offset):
+    """Every split of the heads over warps, inputs and outputs 16 and 32 bytes aligned, rows in
+    front of the first and behind the last sequence left alone."""
+    rng = np.random.default_rng(Hkv + d + offset)
+    c = _cache(rng, [40, 7], Hkv, d)
+    kc, vc, ks, vs, bt, sl = c.gpu()
+    new = [33, 7]
+    T = sum(new) + 3
+    src = [torch.zeros(T * Hkv * d + offset, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    k, v = (x[offset:].view(T, Hkv, d) for x in src)
+    for x in (k, v):
+        x.copy_(E.bf16(rng.standard_normal((T, Hkv, d)))[0])
+    k[5, 0, 3], v[9, Hkv - 1, 1] = float("inf"), float("nan")
+    cu = _i32([1, 34, 41])
+    fb.paged_kv_write_e4m3(k, v, kc, vc, ks, vs, bt, sl, cu)
+    out = [torch.full((T * Hkv * d + offset,), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    ko, vo = (x[offset:].view(T, Hkv, d) for x in out)
+    fb.fa_paged_kv_read_e4m3(kc, vc, ks, vs, bt, sl, cu, ko, vo, 2, T, Hkv, d, 16, c.num_pages,
+                             c.table.shape[1])
+    assert fb.fa_get_device_status() == 0
+    for x, y, buf in ((k, ko, out[0]), (v, vo, out[1])):
+        assert (buf[:offset] == 7.0).all() and (y[0] == 7.0).all() and (y[41:] == 7.0).all()
+        a, b = x[1:41].double(), y[1:41].double()
+        bad = ~torch.isfinite(a)
+        assert torch.equal(torch.isnan(b), bad)
+        # half a step of 4 significant bits, or of the row's smallest code (2^-9 of the scale, whose
+        # 448-fold is below twice the row's largest)
+        top = torch.where(bad, 0.0, a).abs().amax(-1, keepdim=True)
+        err = torch.where(bad, 0.0, a - b).abs()
+        assert (err <= torch.maximum(a.abs().nan_to_num(posinf=0) * 2.0 ** -4, top / 224 * 2.0 ** -10)).all()
+
+
 def test_split_calls_captured_and_replayed():
     """The two-launch forms (equal shares, cut chunks) in one graph, replayed beside eager calls on
     another stream with a workspace of their own."""

@@ -18,8 +18,9 @@
 // warp's loads and stores are whole 32-byte sectors.  The token's sequence is
 // found by a 32-way search of cu_seqlens (two rounds for up to 1024
 // sequences); in the write kernel the row loads are in flight behind it.
-// Bound by memory traffic: 3 bytes a value plus one byte a row; 6.4 TB/s both ways
-// (295725 tokens, 8 heads, d = 128: 0.94 of a plain copy).
+// Bound by memory traffic: 3 bytes a value plus one byte a row; 6.5 TB/s
+// written and 6.7 read back (64 sequences, 8 heads, d = 128: 0.95 and 0.98 of a
+// plain copy).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -201,6 +202,9 @@ kv_read_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ 
                                     num_pages, status, lane);
   if (slot < 0) return;
   const long long row0 = (slot / kPage) * Hkv * kPage + slot % kPage;
+  // Whole 32-byte sectors a store where the outputs allow it: 232 against 250 us
+  // for 64 prefixes (259 MB of codes and scales, d = 128).
+  const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
   uint4 x[kAll];
   uint32_t b[kAll];
 #pragma unroll
@@ -228,8 +232,13 @@ kv_read_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ 
     const size_t row = (size_t)t * Hkv + h;
     if (h < Hkv && FA_IN_BOUNDS(row, (size_t)total * Hkv, status)) {
       uint4* dst = reinterpret_cast<uint4*>(out + row * D + col);
-      dst[0] = make_uint4(r[0], r[1], r[2], r[3]);
-      dst[1] = make_uint4(r[4], r[5], r[6], r[7]);
+      const uint4 lo = make_uint4(r[0], r[1], r[2], r[3]), hi = make_uint4(r[4], r[5], r[6], r[7]);
+      if (wide) {
+        ptx::st_global_v8(dst, lo, hi);
+      } else {
+        dst[0] = lo;
+        dst[1] = hi;
+      }
     }
   }
 }
@@ -264,9 +273,9 @@ void read(const KvRowsParams& p, cudaStream_t stream) {
 // Heads per warp: 512 values of K and of V (four heads at d = 128, eight at
 // d = 64), or half as many where the other half of the lanes would have no row.
 // us for 64 x [512, 8192] tokens, with one or both of K and V a warp and eight
-// heads, and with this: d = 128, 8 heads, write 264, 263, read 270, 265; 2
-// heads, write 210, 92, read 176, 93; d = 64, 8 heads, write 174, 133, read 166,
-// 149; 2 heads, write 169, 91, read 141, 91.
+// heads, and with this: d = 128, 8 heads, write 264, 261, read 270, 252; 2
+// heads, write 210, 87, read 176, 90; d = 64, 8 heads, write 174, 133, read 166,
+// 130; 2 heads, write 169, 86, read 141, 87.
 cudaError_t launch_kv_write_e4m3(const KvRowsParams& p, cudaStream_t stream) {
   if (p.d == 128) p.Hkv <= 2 ? write<128, 2>(p, stream) : write<128, 4>(p, stream);
   else (p.Hkv - 1) % 8 < 4 ? write<64, 4>(p, stream) : write<64, 8>(p, stream);
