@@ -736,7 +736,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         // visible keys may be unlisted: any page does).  At D = 128, where two
         // staged tiles cover less of a copy's latency, it is looked up a tile
         // ahead, for K and V at once.  us without and with, at D = 128: 64
-        // sequences x 9 tokens 266, 252, 16 x 512 541, 537; at D = 64, 16 x 512
+        // sequences x 32 tokens 272, 256, 16 x 512 506, 495; at D = 64, 16 x 512
         // 512, 533.
         constexpr bool kAhead = KV8 && D == 128;
         auto look_up = [&](int j) -> int {
@@ -1117,7 +1117,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       constexpr int kUnits = D / 16;               // units per row
       constexpr int kStepRows = 256 / kUnits;      // rows the 128 threads cover in a step
       const int tid = threadIdx.x - 12 * 32;
-      const int row0 = D == 128 ? tid >> 2 : tid >> 2;
+      const int row0 = tid >> 2;
       const int un = D == 128 ? (tid & 3) + 4 * (row0 & 1) : tid & 3;
       const uint32_t put0 = (D == 128 ? (row0 & 1) * 16384 : 0) + row0 * 128 +
                             (((2 * (un & 3)) ^ (row0 & 7)) << 4);
@@ -1385,7 +1385,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         // (KV8 at d = 128: the exact sum divides.  The cached V is off by 2^-4
         // itself, so half a bf16 step in such rows does not show, and the 128
         // adds per row were 17 % of the time: 643 against 536 us for 16 x
-        // 512-token chunks.)
+        // 512-token chunks, before other steps made that 493.)
         if constexpr (!FP8 && !C::kOnes && !KV8) l_p += sum_packed_bf16(pp);
       }
       if (!ok) break;
