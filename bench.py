@@ -295,7 +295,7 @@ def config_table(peaks):
             return None   # a few microseconds: bound by latency, not by a pipe
         if unit == "GB/s":
             return round(rate / peaks["hbm_gbs"], 4)
-        if name.startswith("e4m3"):
+        if name.startswith("e4m3 B="):   # e4m3 operands (the cache rows multiply in f16 or bf16)
             return round(rate / (fp8_peak or 2.0 * peaks["bf16_tflops"]), 4)
         return round(rate / peaks["bf16_tflops"], 4)
 
@@ -303,7 +303,7 @@ def config_table(peaks):
                             "frac": frac(name, rate, unit)}}
              for name, ms, rate, unit in timing.rows(20, 5)}
     for name in table:
-        if name.startswith("e4m3"):
+        if name.startswith("e4m3 B="):   # e4m3 operands (the cache rows multiply in f16 or bf16)
             table[name]["gpu"]["peak"] = fp8_note
     c1 = I.c1_fp32()
     c1_flops = 4.0 * 256 * 256 * 64

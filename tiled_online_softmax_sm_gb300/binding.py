@@ -520,7 +520,7 @@ def _e4m3_workspace(fn, workspace, q, S, max_q, H, Hkv, d, max_blocks, stream):
         if stream is not None or max_blocks < 32:
             return None, 0, None
         if S * Hkv > 38 or max_blocks < 128:   # then the rows kernels use none
-            G = H // Hkv
+            G = H // max(Hkv, 1)
             if max_q == 1 or max_q * G <= 16 or (max_q * G <= 32 and (d == 64 or G & (G - 1))):
                 return None, 0, None
         need = fa_paged_e4m3_workspace_size(S, max_q, H, Hkv, d)

@@ -203,7 +203,7 @@ kv_read_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ 
   if (slot < 0) return;
   const long long row0 = (slot / kPage) * Hkv * kPage + slot % kPage;
   // Whole 32-byte sectors a store where the outputs allow it: 232 against 250 us
-  // for 64 prefixes (259 MB of codes and scales, d = 128).
+  // for 64 prefixes (518 MB of codes and scales, d = 128).
   const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
   uint4 x[kAll];
   uint32_t b[kAll];
