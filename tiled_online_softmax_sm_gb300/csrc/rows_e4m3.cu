@@ -17,9 +17,9 @@
 //       as a programmatic dependent, merges each unit's partials in a fixed
 //       order.
 //
-// Bound by HBM once there is work for all warps: a copy that skips all the
-// arithmetic takes 85 us for 64 sequences of [512, 8192] tokens (d = 128, 8 kv
-// heads of 4; 517 MB), this 85 (6.05 TB/s, 0.89 of a plain copy).  Below that
+// Bound by HBM once there is work for all warps: 64 sequences of [512, 8192]
+// tokens (d = 128, 8 kv heads of 4; 517 MB) take 83 us (6.2 TB/s, 0.91 of a plain
+// copy), and no less in a copy that skips all the arithmetic.  Below that
 // it is bound by the longest sequence's share: 16 sequences of 4 new tokens
 // take 47 us (134 MB, 0.42), of which the copies alone 35.
 //
@@ -503,8 +503,8 @@ __device__ __forceinline__ bool run_pages(const Args& a, const Seq& Q, int G,
 // Longest sequences first, since CTAs start in block order: the sequence of rank
 // s when they are counted into classes of length (four an octave, by index within
 // one).  Every CTA counts for itself; skipped when all clusters fit at once.  64
-// x [512, 8192] tokens, 8 kv heads: 101 us in index order, 82 so; 256 x [100,
-// 1000]: 60 and 62, and 83 when every pair of sequences was compared.
+// x [512, 8192] tokens, 8 kv heads: 101 us in index order, 80 so; 256 x [100,
+// 1000]: 60 and 59, and 83 when every pair of sequences was compared.
 constexpr int kClasses = 128;
 struct Order {
   uint32_t count[kMaxRanked / 32][kClasses / 4];   // bytes: of 32 sequences, then of those before them
