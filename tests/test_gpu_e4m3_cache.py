@@ -280,6 +280,19 @@ def test_decode_batches_of_many_units(num_seqs, lo, hi, window):
     assert fb.fa_get_device_status() == 0
 
 
+@pytest.mark.parametrize("num_seqs", [77, 255, 256, 257])
+@pytest.mark.parametrize("equal", [True, False])
+def test_decode_order_by_length(num_seqs, equal):
+    """Sequences counted into classes of length: all in one class, empty ones among them, a part of
+    the last 32, as many as are ordered and one more."""
+    rng = np.random.default_rng(num_seqs)
+    lens = [20] * num_seqs if equal else [int(x) for x in rng.integers(0, 70, num_seqs)]
+    c = _cache(rng, lens, 8, 64)
+    q = E.bf16(rng.standard_normal((num_seqs, 8, 64)))[0]
+    _decode_check(c, q)
+    assert fb.fa_get_device_status() == 0
+
+
 @pytest.mark.parametrize("window,sinks", [(0, 0), (700, 3)])
 def test_one_long_sequence_is_shared_by_every_warp(window, sinks):
     rng = np.random.default_rng(50)
