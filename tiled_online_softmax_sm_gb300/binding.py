@@ -125,6 +125,13 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+# The same for a device that is known to be the current one, and the current
+# device once there are tensors on one.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _check(rc: int):
     if rc != FA_OK:
         msg = load().fa_last_error()
@@ -454,7 +461,7 @@ def _check_cache(fn, device, kc, vc, ks, vs, bt, sl):
             and vs.get_device() == device and bt.get_device() == device and sl.get_device() == device
             and kc.is_contiguous() and vc.is_contiguous() and ks.is_contiguous()
             and vs.is_contiguous() and bt.is_contiguous() and sl.is_contiguous()
-            and device == torch.cuda.current_device()):
+            and device >= 0 and device == _current_device()):
         _refuse(fn, device, ("k_cache", kc, _CODES, shape), ("v_cache", vc, _CODES, shape),
                 ("k_scale", ks, _SCALES, rows), ("v_scale", vs, _SCALES, rows),
                 ("block_table", bt, (torch.int32,), table),
@@ -490,7 +497,8 @@ def paged_kv_write_e4m3(k, v, k_cache, v_cache, k_scale, v_scale, block_table, s
     _check(lib.fa_paged_kv_write_e4m3(
         k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
         v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(), S,
-        T, Hkv, d, strides[0], strides[1], page, P, max_blocks, _stream(stream)))
+        T, Hkv, d, strides[0], strides[1], page, P, max_blocks,
+        _current_raw_stream(device) if stream is None else _stream(stream)))
 
 
 def paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens,
@@ -508,7 +516,8 @@ def paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
     _check(lib.fa_paged_kv_read_e4m3(
         k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(), k.data_ptr(),
-        v.data_ptr(), S, total, Hkv, d, page, P, max_blocks, _stream(stream)))
+        v.data_ptr(), S, total, Hkv, d, page, P, max_blocks,
+        _current_raw_stream(device) if stream is None else _stream(stream)))
     return k, v
 
 
@@ -551,7 +560,7 @@ def paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_le
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
         v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
         lse.data_ptr(), S, H, Hkv, d, page, P, max_blocks, scale, window, sinks, ws, ws_bytes,
-        _stream(stream)))
+        _current_raw_stream(device) if stream is None else _stream(stream)))
     return o, lse
 
 
@@ -576,7 +585,8 @@ def paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_l
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
         v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens_q.data_ptr(),
         o.data_ptr(), lse.data_ptr(), S, Tq, max_seqlen_q, H, Hkv, d, page, P, max_blocks, scale,
-        1 if causal else 0, window, sinks, ws, ws_bytes, _stream(stream)))
+        1 if causal else 0, window, sinks, ws, ws_bytes,
+        _current_raw_stream(device) if stream is None else _stream(stream)))
     return o, lse
 
 
