@@ -527,15 +527,6 @@ decode_gather_kernel(const __grid_constant__ CUtensorMap tmK,
   }
 }
 
-// Failure-detection test hook: FA_TEST_FORCE_WAIT_TIMEOUT=1 in the
-// environment makes every decode warp skip its first page copy, so its
-// bounded wait expires (after ~1 s), FA_ERR_TIMEOUT is recorded and the warp
-// returns without writing its partials.  Unset in normal use.
-int skip_first_copy_for_tests() {
-  const char* v = getenv("FA_TEST_FORCE_WAIT_TIMEOUT");
-  return (v != nullptr && v[0] == '1') ? 1 : 0;
-}
-
 }  // namespace
 
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream, bool fused) {

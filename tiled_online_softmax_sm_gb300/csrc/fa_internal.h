@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
+#include <stdlib.h>
 
 namespace fa {
 
@@ -63,6 +64,15 @@ enum : int {
 #else
 #define FA_IN_BOUNDS(idx, limit, status) true
 #endif
+
+// Failure-detection test hook of the forward and the e4m3 rows kernels, as the
+// bf16 decode's: with FA_TEST_FORCE_WAIT_TIMEOUT=1 in the environment every warp
+// that copies K and V skips its first tile or page, the bounded waits for it
+// expire (after about 1 s) and FA_ERR_TIMEOUT is recorded.  Unset in normal use.
+inline int skip_first_copy_for_tests() {
+  const char* v = getenv("FA_TEST_FORCE_WAIT_TIMEOUT");
+  return (v != nullptr && v[0] == '1') ? 1 : 0;
+}
 
 // Forward problem.  Dense BSHD when cu_q == nullptr; otherwise packed varlen
 // (B = number of sequences, n/m = max lengths, token rows start at cu_q[b]).

@@ -496,7 +496,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 int sched_sorted, int num_split, int* status, int window, int sinks, int gl,
                 const uint8_t* __restrict__ raw_k, const uint8_t* __restrict__ raw_v,
                 const uint8_t* __restrict__ k_scale, const uint8_t* __restrict__ v_scale, int parts,
-                float* __restrict__ part_s, float* __restrict__ part_o) {
+                float* __restrict__ part_s, float* __restrict__ part_o, int skip_first_copy) {
   using C = Cfg<D, FP8, KV8>;
   // (KV8 instances work the units out in every role: with the ring, and the
   // registers it takes, their chunks were 10 % slower; the window's 4 % faster.)
@@ -719,6 +719,14 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       int nfix = 0;               // V tiles zero-fixed (paged)
       bool fix_pending = false;
       bool ok = true;
+      // A wait that runs out does so for the whole warp: a lane that gave up (or
+      // saw the abort flag) while another lane's poll succeeded would be missing
+      // from the full-mask __syncwarp and votes behind it, which nothing bounds.
+      // (Asked as "has any lane failed": all(...) cost e4m3 chunks 2 %, one lane
+      // polling for the warp 5 %.)
+      auto warp_wait = [&](uint32_t bar, uint32_t parity) __attribute__((always_inline)) -> bool {
+        return !__any_sync(0xffffffffu, !ptx::mbar_wait(bar, parity, status, abort_flag));
+      };
       for (int k = 0; (kUnitRing || k * (int)gridDim.x < num_units) && ok; ++k) {
         Unit U;
         if constexpr (kUnitRing) {
@@ -751,7 +759,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         for (int i = 0; i < 2 && ok; ++i) {
           if (U.n_kv[i] == 0) continue;
           // the previous unit's last S_i MMA must be done with Q_i
-          if (!(ok = ptx::mbar_wait(bar_qe + 8 * i, (nq[i] & 1) ^ 1, status, abort_flag))) break;
+          if (!(ok = warp_wait(bar_qe + 8 * i, (nq[i] & 1) ^ 1))) break;
           if (lane == 0) {
             const uint32_t dst = ptx::smem_u32(sQ + i * C::kTileBytes);
             ptx::mbar_arrive_expect_tx(bar_q + 8 * i, C::kTileBytes);
@@ -765,19 +773,21 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         // one K (which 0) or V (which 1) tile load into the next ring slot;
         // false if a wait failed
         auto issue_kv = [&](int which, int j) __attribute__((always_inline)) -> bool {
+          const bool skip = skip_first_copy && li == 0;   // test hook: this tile never arrives
           if constexpr (KV8) {
             // stage the tile's pages: lane pg copies page pg and its 16 scale bytes
             const int slot = li % C::kRawStages;
-            if (!ptx::mbar_wait(bar_re + 8 * slot, ((li / C::kRawStages) & 1) ^ 1, status, abort_flag))
-              return false;
-            __syncwarp();
+            int id = kAhead ? page : look_up(j);   // (read while the slot is waited for)
+            const bool freed =
+                ptx::mbar_wait(bar_re + 8 * slot, ((li / C::kRawStages) & 1) ^ 1, status, abort_flag);
             const uint32_t dst = ptx::smem_u32(sRaw + slot * C::kRawTile);
             const uint32_t bar = bar_rf + 8 * slot;
             const int npages = (min(kBlockN, U.kv_len - j * kBlockN) + 15) / 16;
-            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, npages * (16 * D + 16));
-            __syncwarp();
-            if (lane < npages) {
-              int id = kAhead ? page : look_up(j);
+            if (lane == 0 && freed && !skip) ptx::mbar_arrive_expect_tx(bar, npages * (16 * D + 16));
+            // (one vote for the wait's outcome and for lane 0's count: after a failure
+            // the count is left behind on a barrier that nothing waits for)
+            if (__any_sync(0xffffffffu, !freed)) return false;
+            if (lane < npages && !skip) {
               if (id < 0 || id >= num_pages) {
                 atomicExch(status, kDevBadBlockTable);
                 id = 0;
@@ -790,9 +800,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             return true;
           } else {
             const int slot = li % C::kStages;
-            if (!ptx::mbar_wait(bar_kve + 8 * slot, ((li / C::kStages) & 1) ^ 1, status, abort_flag))
-              return false;
-            __syncwarp();
+            if (!warp_wait(bar_kve + 8 * slot, ((li / C::kStages) & 1) ^ 1)) return false;
             uint8_t* tile = sKV + slot * C::kSlotBytes;
             const uint32_t dst = ptx::smem_u32(tile);
             const CUtensorMap* map = which == 0 ? &tmK : &tmV;
@@ -814,9 +822,9 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
               // lane 0 posts the byte count (the barrier's one arrival, so the
               // phase cannot complete before it), then lane pg looks up page
               // pg and issues its boxes: the page copies go out in parallel
-              if (lane == 0) ptx::mbar_arrive_expect_tx(bar, npages * 16 * C::kRowBytes);
+              if (lane == 0 && !skip) ptx::mbar_arrive_expect_tx(bar, npages * 16 * C::kRowBytes);
               __syncwarp();
-              if (lane < npages) {
+              if (lane < npages && !skip) {
                 const int pg = lane;
                 int id = __ldg(block_table + (size_t)U.b * max_blocks + j * (kBlockN / 16) + pg);
                 if (id < 0 || id >= num_pages) {
@@ -829,7 +837,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                   ptx::tma_load_2d(dst + c * 16384 + pg * 2048, map, C::kChunkElems * c, row, bar);
               }
             } else {
-              if (lane == 0) {
+              if (lane == 0 && !skip) {
                 ptx::mbar_arrive_expect_tx(bar, C::kTileBytes);
 #pragma unroll
                 for (int c = 0; c < C::kChunks; ++c) {
@@ -844,7 +852,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             }
             if (fix) {
               fix_pending = true;
-              if (!ptx::mbar_wait(bar_fix, nfix & 1, status, abort_flag)) return false;
+              if (!warp_wait(bar_fix, nfix & 1)) return false;
               fix_pending = false;
               ++nfix;
               const int zero_rows = kBlockN - rows_valid;
@@ -1747,7 +1755,7 @@ cudaError_t launch(const FwdParams& p, cudaStream_t stream, const char** why) {
         out_scale, counted ? 2 : sorted ? 1 : 0, num_split, p.status, p.window, p.sinks, gl,
         static_cast<const uint8_t*>(p.k), static_cast<const uint8_t*>(p.v),
         static_cast<const uint8_t*>(p.k_scale), static_cast<const uint8_t*>(p.v_scale), parts, part_s,
-        part_o);
+        part_o, skip_first_copy_for_tests());
     err = cudaGetLastError();
     if (err != cudaSuccess) *why = "fwd_bf16 launch";
     if constexpr (KV8) {

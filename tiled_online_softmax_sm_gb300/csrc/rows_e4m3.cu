@@ -54,7 +54,6 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
-#include <stdlib.h>
 
 #include "fa_internal.h"
 #include "ptx.cuh"
@@ -1046,14 +1045,6 @@ rows_merge_kernel(const Args a, int warps) {
     if (lane == 0 && a.lse != nullptr)
       a.lse[tok * a.lse_row + head * a.lse_head] = l == 0.f ? -INFINITY : (M + __log2f(l)) * kLn2;
   }
-}
-
-// Failure-detection test hook, as the bf16 decode's: with
-// FA_TEST_FORCE_WAIT_TIMEOUT=1 every warp skips its first page copy, its
-// bounded wait expires and FA_ERR_TIMEOUT is recorded.  Unset in normal use.
-int skip_first_copy_for_tests() {
-  const char* v = getenv("FA_TEST_FORCE_WAIT_TIMEOUT");
-  return (v != nullptr && v[0] == '1') ? 1 : 0;
 }
 
 template <int D, int NT>
