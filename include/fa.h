@@ -169,8 +169,10 @@ fa_status fa_forward_varlen(const void* q, const void* k, const void* v, void* o
  * K/V tiles between the sinks and the window are never loaded, so the work is
  * linear in n for a fixed window.
  * Supported: d == dv in {64, 128}; pointers 16-byte aligned; dense: B*n, B*m
- * and H*n below 2^31; packed: H*total_q below 2^31, num_seqs*max_seqlen_q*H
- * below 2^36.
+ * and H*n below 2^31; packed: H*total_q below 2^31; both: fewer than 2^30 work
+ * units (a batch element or sequence, empty ones among them; 2^a query heads of
+ * one kv head, the largest power of two that divides H / Hkv, 128 at most;
+ * 256 / 2^a query tokens, counted up to n or max_seqlen_q).
  */
 fa_status fa_forward_window(const void* q, const void* k, const void* v, void* o, float* lse,
                             int B, int H, int Hkv, int n, int m, int d, int dv, float scale,

@@ -246,6 +246,9 @@ fa_status fa_forward_window(const void* q, const void* k, const void* v, void* o
     return fail(FA_ERR_UNSUPPORTED, "%s: d=%d dv=%d (supported: d == dv in {64, 128})", fn, d, dv);
   if ((st = check_rows(B, H, n, m, fn)) != FA_OK) return st;
   if (B == 0 || n == 0) return FA_OK;
+  if (fa::packed_units(B, n, H, Hkv) > 0x3fffffffLL)
+    return fail(FA_ERR_UNSUPPORTED, "%s: the (batch element, head group, 256 query rows) units must "
+                "stay below 2^30", fn);
   int* sp = nullptr;
   if ((st = status_ptr(&sp)) != FA_OK) return st;
   fa::FwdParams p{q, k, v, o, lse, nullptr, nullptr, B, H, Hkv, n, m, d, dv, 0, 0, scale, 1, sp};
@@ -281,9 +284,10 @@ fa_status fa_forward_varlen_window(const void* q, const void* k, const void* v, 
     return fail(FA_ERR_UNSUPPORTED, "%s: d=%d dv=%d (supported: d == dv in {64, 128})", fn, d, dv);
   if (num_seqs == 0 || max_seqlen_q == 0 || total_q == 0) return FA_OK;
   if (max_seqlen_q > total_q) max_seqlen_q = total_q;   // no sequence has more
-  if ((long long)H * total_q > 0x7fffffffLL || (long long)num_seqs * max_seqlen_q * H > 0xfffffffffLL)
-    return fail(FA_ERR_UNSUPPORTED, "%s: H*total_q must stay below 2^31, num_seqs*max_seqlen_q*H "
-                "below 2^36", fn);
+  if ((long long)H * total_q > 0x7fffffffLL ||
+      fa::packed_units(num_seqs, max_seqlen_q, H, Hkv) > 0x3fffffffLL)
+    return fail(FA_ERR_UNSUPPORTED, "%s: H*total_q must stay below 2^31, the (sequence, head group, "
+                "256 query rows) units below 2^30", fn);
   int* sp = nullptr;
   if ((st = status_ptr(&sp)) != FA_OK) return st;
   fa::FwdParams p{q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, num_seqs, H, Hkv,

@@ -113,23 +113,27 @@ inline int packed_heads_log2(int H, int Hkv) {
   return gl;
 }
 
-// Parts that each unit (sequence, head group, pair of query tiles) of a chunk
+// Work units of a launch that packs heads: (sequence, head group, pair of query
+// tiles).  The kernels number them in 32 bits.
+inline long long packed_units(int num_seqs, int max_q, int H, int Hkv) {
+  const int gl = packed_heads_log2(H, Hkv);
+  const long long pair_q = 256 >> gl;
+  return (long long)num_seqs * (H >> gl) * ((max_q + pair_q - 1) / pair_q);
+}
+
+// Parts that each unit of a chunk
 // launch over the e4m3 cache is cut into: as many as fill the SMs where units
 // are few, twice as many for several sequences (whose lengths may differ), and
 // 1 from 152 units on.
 inline int cache_parts(int num_seqs, int max_q, int H, int Hkv) {
-  const int gl = packed_heads_log2(H, Hkv);
-  const long long pair_q = 256 >> gl;
-  const long long units = (long long)num_seqs * (H >> gl) * ((max_q + pair_q - 1) / pair_q);
+  const long long units = packed_units(num_seqs, max_q, H, Hkv);
   if (units <= 0 || units > 152) return 1;
   return (int)((num_seqs == 1 ? 152 : 304) / units);
 }
 inline size_t cache_parts_bytes(int num_seqs, int max_q, int H, int Hkv, int d) {
   const int parts = cache_parts(num_seqs, max_q, H, Hkv);
   if (parts <= 1) return 0;
-  const int gl = packed_heads_log2(H, Hkv);
-  const long long pair_q = 256 >> gl;
-  return (size_t)num_seqs * (H >> gl) * ((max_q + pair_q - 1) / pair_q) * parts * 256 * (d + 4) * 4;
+  return (size_t)packed_units(num_seqs, max_q, H, Hkv) * parts * 256 * (d + 4) * 4;
 }
 
 struct DecodeParams {
