@@ -168,6 +168,8 @@ fa_status fa_forward_varlen(const void* q, const void* k, const void* v, void* o
  *           without one)
  * K/V tiles between the sinks and the window are never loaded, so the work is
  * linear in n for a fixed window.
+ * A row whose visible scores hold a NaN gets O = LSE = NaN (never the LSE = -inf
+ * of a row that sees no key).
  * Supported: d == dv in {64, 128}; pointers 16-byte aligned; dense: B*n, B*m
  * and H*n below 2^31; packed: H*total_q below 2^31; both: fewer than 2^30 work
  * units (a batch element or sequence, empty ones among them; 2^a query heads of
@@ -469,6 +471,8 @@ fa_status fa_paged_decode_e4m3(const void* q, const void* k_cache, const void* v
  * output is then unspecified.
  * Cache contents of keys that none of a sequence's queries sees are never
  * used; a NaN in a key that one query sees may reach others of its sequence.
+ * A row whose visible scores hold a NaN gets O = LSE = NaN, with a workspace or
+ * without, as in fa_paged_decode_e4m3.
  * Chunks of at most 16 rows (max_seqlen_q * H / Hkv; 32 at d = 64 and where
  * H / Hkv is no power of two) run as
  * fa_paged_decode_e4m3 does; larger ones on the tcgen05 path of fa_forward,

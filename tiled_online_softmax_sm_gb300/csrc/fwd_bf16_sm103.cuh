@@ -1530,7 +1530,9 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         // O's divisor (bf16: the rounded sum, positive exactly when l_run is:
         // a normal fp32 p rounds to a normal bf16) and the LSE's l
         const float l_o = FP8 || (KV8 && !C::kOnes) ? l_run : l_p;
-        const float inv = l_o > 0.f ? out_scale / l_o : 0.f;
+        // (WIN: a sum that is NaN stays NaN, in O and in the LSE, as in the merges;
+        // without it the LSE would say that the row sees no key)
+        const float inv = l_o > 0.f ? out_scale / l_o : (WIN && l_o != 0.f ? l_o : 0.f);
         uint4* dst = reinterpret_cast<uint4*>(o + orow * D);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -1547,7 +1549,8 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const size_t li = (size_t)U.b * lse_stride_b + (size_t)head * lse_stride_h +
                           (U.q_row0 - (cu_q ? 0 : U.b * n)) + qi;
         if (lse != nullptr && FA_IN_BOUNDS(li, (size_t)total_q * H, status))
-          lse[li] = l_run > 0.f ? (m_ref + __log2f(l_run)) * kLn2 : -INFINITY;
+          lse[li] = l_run > 0.f ? (m_ref + __log2f(l_run)) * kLn2
+                                : (WIN && l_run != 0.f ? l_run : -INFINITY);
       }
     }
   }
@@ -1615,8 +1618,9 @@ merge_parts_kernel(const float* __restrict__ part_s, const float* __restrict__ p
       v[0] = w.x;
       v[1] = w.y;
     }
-    // (a part that saw no key has left its O unwritten: whatever was read is dropped)
-    const bool seen = st.x != -INFINITY;
+    // (a part that saw no key has left its O unwritten: whatever was read is dropped;
+    // one whose scores are all NaN has no reference either, but a sum)
+    const bool seen = st.y != 0.f;
     const float f = seen ? ptx::ex2(st.x - M) : 0.f;
     l += seen ? f * st.y : 0.f;
     lp += seen ? f * st.z : 0.f;
