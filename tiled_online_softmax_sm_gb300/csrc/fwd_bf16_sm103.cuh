@@ -1390,11 +1390,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         // that key's V row back to within fp32 rounding, where the exact sum
         // would leave the rounding of that key's p (up to 2^-8 relative) in O.
         // Done after the hand-off, while the MMAs run.
-        // (KV8 at d = 128: the exact sum divides.  The cached V is off by 2^-4
-        // itself, so half a bf16 step in such rows does not show, and the 128
-        // adds per row were 17 % of the time: 643 against 536 us for 16 x
-        // 512-token chunks, before other steps made that 493.)
-        if constexpr (!FP8 && !C::kOnes && !KV8) l_p += sum_packed_bf16(pp);
+        if constexpr (!FP8 && !C::kOnes) l_p += sum_packed_bf16(pp);
       }
       if (!ok) break;
 
@@ -1511,7 +1507,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             ((((size_t)U.b * Hg + U.h) * num_pairs + U.q_start0 / (2 * kBlockM >> gl)) * parts + U.index % parts) *
                 (2 * kBlockM) + i * kBlockM + r;
         if (row_valid) {
-          *reinterpret_cast<float4*>(part_s + slot * 4) = make_float4(m_ref, l_run, C::kOnes ? l_p : l_run, 0.f);
+          *reinterpret_cast<float4*>(part_s + slot * 4) = make_float4(m_ref, l_run, l_p, 0.f);
           if (nkv > 0) {
             uint4* dst = reinterpret_cast<uint4*>(part_o + slot * D);
 #pragma unroll
@@ -1529,7 +1525,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       if (row_valid && FA_IN_BOUNDS(orow, (size_t)total_q * H, status)) {
         // O's divisor (bf16: the rounded sum, positive exactly when l_run is:
         // a normal fp32 p rounds to a normal bf16) and the LSE's l
-        const float l_o = FP8 || (KV8 && !C::kOnes) ? l_run : l_p;
+        const float l_o = FP8 ? l_run : l_p;
         // (WIN: a sum that is NaN stays NaN, in O and in the LSE, as in the merges;
         // without it the LSE would say that the row sees no key)
         const float inv = l_o > 0.f ? out_scale / l_o : (WIN && l_o != 0.f ? l_o : 0.f);
