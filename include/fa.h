@@ -445,8 +445,12 @@ size_t fa_paged_e4m3_workspace_size(int num_seqs, int max_seqlen_q, int H, int H
  * the others may be anything.  Cache contents of keys no query sees are never
  * used, NaN included.  Device status as fa_paged_decode (bad page ids are
  * skipped; a bad seq_lens[s] is treated as an empty sequence).
- * K, V and the softmax weights enter the tensor cores in f16 (codes exactly,
- * weights rounded to 11 bits), accumulation is fp32.
+ * K, V and the softmax weights enter the tensor cores in f16: codes exactly;
+ * weights, each times its V row's 2^(byte - 127), rounded to 11 bits, fewer
+ * below 2^-21 of the row's largest such product, and to zero below 2^-32 of it.
+ * (So a V row whose scale is far above what its codes need, which this library
+ * does not write, hides the others' share when its key has weight.)
+ * Accumulation is fp32.
  * Supported: H / Hkv <= 32; num_seqs*H below 2^28.
  */
 fa_status fa_paged_decode_e4m3(const void* q, const void* k_cache, const void* v_cache,

@@ -37,10 +37,12 @@
 //   x = S * 2^(k exponent) * (scale log2 e, Q's power of two), masked
 //   p = 2^(x - m) for the sum l, w = 2^(x + v exponent - r) for the values
 //   O^T += V^T w  A = V codes widened to f16 (exact), B = w in f16
-// The V scales ride on the weights, so m and r are separate references: w is
-// at most 2^8 and a weight only underflows when its token's contribution is
-// 2^-32 of the largest one's.  Both are raised lazily, when a score passes
-// them by more than 8 (log2 units): a vote per page instead of reductions.
+// The V scales ride on the weights, so m and r are separate references.  Both
+// are raised lazily, when a score has come to pass the row's largest at the last
+// raise by more than 8 (log2 units): a vote per page instead of reductions.  m
+// is raised to that largest, r to 2^7 below it, so w uses f16's upper range: it
+// is at most 2^15, exact to 11 bits down to 2^-21 of the largest weight times
+// 2^(v exponent), and zero below 2^-32 of it.
 // O = 2^(r - m) acc / l, in fp32, rounded once to bf16.
 //
 // The lanes' shares of a row are chosen so that no shuffle or ldmatrix is
@@ -67,7 +69,8 @@ constexpr int kWarps = 4;             // warps per CTA
 constexpr int kMaxRanked = 256;       // cluster launches with more sequences keep index order
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRaise = 8.f;         // log2 units a score may pass its reference by
+constexpr float kRaise = 8.f;         // log2 units a score may pass the largest at the last raise by
+constexpr float kUnder = 7.f;         // log2 units r lies below that largest
 // The references of a row that has seen no key: finite, so that 2^(x - m) is 0
 // for a masked x = -inf without a guard, and below every score of finite rows.
 constexpr float kNone = -1e30f;
@@ -350,7 +353,7 @@ __device__ __forceinline__ void absorb(const Args& a, const Seq& Q, int G, const
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       raise = raise || xs[t][e] > S.m[t][e & 1] + kRaise ||
-              xs[t][e] + vf[e >> 1] > S.r[t][e & 1] + kRaise;
+              xs[t][e] + vf[e >> 1] > S.r[t][e & 1] + (kUnder + kRaise);
   if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -363,7 +366,7 @@ __device__ __forceinline__ void absorb(const Args& a, const Seq& Q, int G, const
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
           mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, off));
         }
-        const float mn = fmaxf(S.m[t][e], mx), ro = fmaxf(S.r[t][e], mo);
+        const float mn = fmaxf(S.m[t][e], mx), ro = fmaxf(S.r[t][e], mo - kUnder);
         S.l[t][e] *= ptx::ex2(S.m[t][e] - mn);   // (from none: 0 * 0)
         const float al = ptx::ex2(S.r[t][e] - ro);
         S.m[t][e] = mn;
