@@ -238,8 +238,9 @@ struct Query {
       mx = max(mx & 0xffffu, mx >> 16);
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // multiply by 2^e with the largest element landing in [2^14, 2^15)
-      const int e = min(127, 141 - (int)(mx >> 7));
+      // multiply by 2^e with the largest element landing in [2^14, 2^15) (below it
+      // for rows under 2^-106, where a larger e would make fac a subnormal)
+      const int e = min(120, 141 - (int)(mx >> 7));
       const float up = __uint_as_float((uint32_t)(e + 127) << 23);
 #pragma unroll
       for (int u = 0; u < D / 16; ++u)
@@ -322,7 +323,10 @@ __device__ __forceinline__ void absorb(const Args& a, const Seq& Q, int G, const
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) xs[t][e] = s[t][e] * kf[e >> 1] * q.fac[t][e & 1];
+    for (int e = 0; e < 4; ++e)
+      // the powers of two first: s times K's alone may overflow where Q's takes it
+      // back.  (Bounded, so that a row of zeros has score 0 whatever its scale.)
+      xs[t][e] = s[t][e] * fminf(kf[e >> 1] * q.fac[t][e & 1], 3.4028234e38f);
   if (!whole) {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
