@@ -35,15 +35,16 @@
 //                 scaled per row by a power of two (exact: bf16 has 8 bits,
 //                 f16 11; elements 2^-29 below their row's largest lose bits)
 //   x = S * 2^(k exponent) * (scale log2 e, Q's power of two), masked
-//   p = 2^(x - m) for the sum l, w = 2^(x + v exponent - r) for the values
+//   p = 2^(x - m) for the sum l, w = 2^(x - m + v exponent - r) for the values
 //   O^T += V^T w  A = V codes widened to f16 (exact), B = w in f16
-// The V scales ride on the weights, so m and r are separate references.  Both
-// are raised lazily, when a score has come to pass the row's largest at the last
-// raise by more than 8 (log2 units): a vote per page instead of reductions.  m
-// is raised to that largest, r to 2^7 below it, so w uses f16's upper range: it
-// is at most 2^15, exact to 11 bits down to 2^-21 of the largest weight times
+// The V scales ride on the weights, so the weights have a reference of their own,
+// r, kept relative to m (small numbers: at scores of 2^20 a sum of score and
+// exponent would be off by 2^-4).  Both are raised lazily, when an exponent of p
+// or w passes 15: a vote per page instead of reductions.  m is raised to the
+// largest score, r to 7 below the largest weighted one, so w uses f16's upper
+// range: it is at most 2^15, exact to 11 bits down to 2^-21 of the largest weight times
 // 2^(v exponent), and zero below 2^-32 of it.
-// O = 2^(r - m) acc / l, in fp32, rounded once to bf16.
+// O = 2^r acc / l, in fp32, rounded once to bf16.
 //
 // The lanes' shares of a row are chosen so that no shuffle or ldmatrix is
 // needed: lane (r = lane / 4, c = lane % 4) reads tokens r, r + 8 of K at dims
@@ -69,10 +70,11 @@ constexpr int kWarps = 4;             // warps per CTA
 constexpr int kMaxRanked = 256;       // cluster launches with more sequences keep index order
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRaise = 8.f;         // log2 units a score may pass the largest at the last raise by
-constexpr float kUnder = 7.f;         // log2 units r lies below that largest
-// The references of a row that has seen no key: finite, so that 2^(x - m) is 0
-// for a masked x = -inf without a guard, and below every score of finite rows.
+constexpr float kTop = 15.f;          // largest exponent of p and w (f16 holds up to 2^16)
+constexpr float kUnder = 7.f;         // how far r lies below the largest weighted score when raised
+// The reference of a row that has seen no key (its r is 0): finite, so that
+// 2^(x - m) is 0 for a masked x = -inf without a guard, and below every score of
+// finite rows.
 constexpr float kNone = -1e30f;
 
 template <int D, int NT, bool STREAM>
@@ -186,8 +188,8 @@ struct State {
         acc[t][i][0] = acc[t][i][1] = acc[t][i][2] = acc[t][i][3] = 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[t][e] = r[t][e] = kNone;
-        l[t][e] = 0.f;
+        m[t][e] = kNone;
+        r[t][e] = l[t][e] = 0.f;
       }
     }
   }
@@ -319,7 +321,6 @@ __device__ __forceinline__ void absorb(const Args& a, const Seq& Q, int G, const
   const float kf[2] = {ptx::exp2_byte(sc[r]), ptx::exp2_byte(sc[r + 8])};
   const float vf[2] = {ptx::log2_byte(sc[16 + r]), ptx::log2_byte(sc[24 + r])};
   float xs[NT][4];
-  bool raise = false;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -352,28 +353,45 @@ __device__ __forceinline__ void absorb(const Args& a, const Seq& Q, int G, const
       }
     }
   }
+  float xp[NT][4], xw[NT][4];   // the exponents of p and w
+  auto exponents = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        xp[t][e] = xs[t][e] - S.m[t][e & 1];
+        xw[t][e] = xp[t][e] + (vf[e >> 1] - S.r[t][e & 1]);
+      }
+  };
+  exponents();
+  float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      raise = raise || xs[t][e] > S.m[t][e & 1] + kRaise ||
-              xs[t][e] + vf[e >> 1] > S.r[t][e & 1] + (kUnder + kRaise);
-  if (__any_sync(0xffffffffu, raise)) {
+    for (int e = 0; e < 4; ++e) top[e & 1] = ptx::fmax3(top[e & 1], xp[t][e], xw[t][e]);
+  if (__any_sync(0xffffffffu, fmaxf(top[0], top[1]) > kTop)) {
+    float mn[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float mx = fmaxf(xs[t][e], xs[t][e + 2]);
-        float mo = fmaxf(xs[t][e] + vf[0], xs[t][e + 2] + vf[1]);
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-          mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, off));
-        }
-        const float mn = fmaxf(S.m[t][e], mx), ro = fmaxf(S.r[t][e], mo - kUnder);
-        S.l[t][e] *= ptx::ex2(S.m[t][e] - mn);   // (from none: 0 * 0)
-        const float al = ptx::ex2(S.r[t][e] - ro);
-        S.m[t][e] = mn;
+        for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        mn[t][e] = fmaxf(S.m[t][e], mx);
+      }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float up = S.m[t][e] - mn[t][e];
+        float mo = fmaxf(xs[t][e] - mn[t][e] + vf[0], xs[t][e + 2] - mn[t][e] + vf[1]);
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) mo = fmaxf(mo, __shfl_xor_sync(0xffffffffu, mo, off));
+        const float ro = fmaxf(S.r[t][e] + up, mo - kUnder);
+        S.l[t][e] *= ptx::ex2(up);   // (from none: 0 * 0)
+        const float al = ptx::ex2(S.r[t][e] + up - ro);
+        S.m[t][e] = mn[t][e];
         S.r[t][e] = ro;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
@@ -381,6 +399,7 @@ __device__ __forceinline__ void absorb(const Args& a, const Seq& Q, int G, const
           S.acc[t][i][e + 2] *= al;
         }
       }
+    exponents();
   }
   uint32_t wb[NT][2];
 #pragma unroll
@@ -388,8 +407,8 @@ __device__ __forceinline__ void absorb(const Args& a, const Seq& Q, int G, const
     float w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      S.l[t][e & 1] += ptx::ex2(xs[t][e] - S.m[t][e & 1]);
-      w[e] = ptx::ex2(xs[t][e] + (vf[e >> 1] - S.r[t][e & 1]));
+      S.l[t][e & 1] += ptx::ex2(xp[t][e]);
+      w[e] = ptx::ex2(xw[t][e]);
     }
     wb[t][0] = ptx::movmatrix_trans(ptx::pack_f16x2(w[0], w[1]));
     wb[t][1] = ptx::movmatrix_trans(ptx::pack_f16x2(w[2], w[3]));
@@ -406,6 +425,10 @@ __device__ __forceinline__ void absorb(const Args& a, const Seq& Q, int G, const
 #pragma unroll
       for (int t = 0; t < NT; ++t) ptx::mma_f16_16816(S.acc[t][2 * u + hlf], fa, wb[t][0], wb[t][1]);
     }
+}
+
+__device__ __forceinline__ float max4(float a, float b, float c, float d) {
+  return fmaxf(fmaxf(a, b), fmaxf(c, d));
 }
 
 // A warp's ring of pages in flight.
@@ -665,10 +688,10 @@ rows_cluster_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int row = 8 * t + 2 * c + e;
-      float ro = s_r[0][row];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) ro = fmaxf(ro, s_r[w][row]);
-      const float f = ptx::ex2(S.r[t][e] - ro);
+      const float M = max4(s_m[0][row], s_m[1][row], s_m[2][row], s_m[3][row]);
+      const float ro = max4(s_r[0][row] + s_m[0][row], s_r[1][row] + s_m[1][row],
+                            s_r[2][row] + s_m[2][row], s_r[3][row] + s_m[3][row]) - M;
+      const float f = ptx::ex2(S.r[t][e] + (S.m[t][e] - M) - ro);
       float4* dst = reinterpret_cast<float4*>(buf + ((size_t)warp * kRows + row) * D + r * (D / 8));
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
@@ -681,8 +704,9 @@ rows_cluster_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       M = fmaxf(M, s_m[w][row]);
-      R = fmaxf(R, s_r[w][row]);
+      R = fmaxf(R, s_r[w][row] + s_m[w][row]);
     }
+    R -= M;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
       sum += s_l[w][row] * ptx::ex2(s_m[w][row] - M);
@@ -731,23 +755,25 @@ rows_cluster_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       const uint32_t am = ptx::smem_u32(&s_cm[row]), ar = ptx::smem_u32(&s_cr[row]),
                      al = ptx::smem_u32(&s_cl[row]), ab = ptx::smem_u32(buf + 4 * v);
       for (int k = 0; k < C; ++k) {
-        M = fmaxf(M, ptx::ld_cluster_f32(ptx::cluster_map(am, k)));
-        R = fmaxf(R, ptx::ld_cluster_f32(ptx::cluster_map(ar, k)));
+        const float mk = ptx::ld_cluster_f32(ptx::cluster_map(am, k));
+        M = fmaxf(M, mk);
+        R = fmaxf(R, ptx::ld_cluster_f32(ptx::cluster_map(ar, k)) + mk);
       }
+      R -= M;
       for (int k = 0; k < C; ++k) {
         const float mk = ptx::ld_cluster_f32(ptx::cluster_map(am, k));
         const float rk = ptx::ld_cluster_f32(ptx::cluster_map(ar, k));
         const float lk = ptx::ld_cluster_f32(ptx::cluster_map(al, k));
         const float4 z = ptx::ld_cluster_f32x4(ptx::cluster_map(ab, k));
-        sum += lk * ptx::ex2(mk - M); 
-        const float f = ptx::ex2(rk - R);
+        sum += lk * ptx::ex2(mk - M);
+        const float f = ptx::ex2(rk + (mk - M) - R);
         y.x += z.x * f;
         y.y += z.y * f;
         y.z += z.z * f;
         y.w += z.w * f;
       }
     }
-    const float f = sum > 0.f ? ptx::ex2(R - M) / sum : (sum == 0.f ? 0.f : sum);
+    const float f = sum > 0.f ? ptx::ex2(R) / sum : (sum == 0.f ? 0.f : sum);
     const size_t tok = (size_t)(Q.q0 + row / G);
     const size_t orow = tok * a.H + g * G + row % G;
     if (FA_IN_BOUNDS(orow, (size_t)a.total_q * a.H, a.status)) {
@@ -925,11 +951,11 @@ rows_stream_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
 }
 
 // Merge of the stream form: a block per (unit, row), or a warp where few
-// sharers meet.  M = max m_k, R = max r_k, l = sum 2^(m_k - M) l_k,
-// O = 2^(R - M) / l * sum 2^(r_k - R) O_k; warp w of a block takes partials w,
-// w + 8, ..., and the warps' sums are added in order.  Latency counts here: the
-// list's offsets come from the stream kernel, and partials are loaded eight
-// at a time.
+// sharers meet.  M = max m_k, R = max (r_k + m_k) - M, l = sum 2^(m_k - M) l_k,
+// O = 2^R / l * sum 2^(r_k + (m_k - M) - R) O_k (a rounding of R cancels); warp w
+// of a block takes partials w, w + 8, ..., and the warps' sums are added in
+// order.  Latency counts here: the list's offsets come from the stream kernel,
+// and partials are loaded eight at a time.
 constexpr int kMergeWarps = 8;
 template <int D, int NT, int WPP>
 __global__ void __launch_bounds__(kMergeWarps * 32)
@@ -969,7 +995,7 @@ rows_merge_kernel(const Args a, int warps) {
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int w = k0 + u * WPP;
-      st[u] = make_float4(kNone, kNone, 0.f, 0.f);
+      st[u] = make_float4(kNone, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < kVec; ++i) v[u][i] = 0.f;
       if (w <= w1) {
@@ -995,7 +1021,7 @@ rows_merge_kernel(const Args a, int warps) {
   for (int w = w0 + (WPP == 1 ? lane : (int)threadIdx.x); w <= w1; w += WPP * 32) {
     const float4 x = __ldcg(ps + slot0 + (size_t)w * kRows);
     M = fmaxf(M, x.x);
-    R = fmaxf(R, x.y);
+    R = fmaxf(R, x.y + x.x);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -1014,6 +1040,7 @@ rows_merge_kernel(const Args a, int warps) {
       R = fmaxf(R, s_mr[w][1]);
     }
   }
+  R -= M;
   float l = 0.f, y[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) y[i] = 0.f;
@@ -1021,7 +1048,7 @@ rows_merge_kernel(const Args a, int warps) {
     if (k > w0 + part) fetch(k);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const float f = ptx::ex2(st[u].y - R);
+      const float f = ptx::ex2(st[u].y + (st[u].x - M) - R);
       l += st[u].z * ptx::ex2(st[u].x - M);
 #pragma unroll
       for (int i = 0; i < kVec; ++i) y[i] = fmaf(v[u][i], f, y[i]);
@@ -1041,7 +1068,7 @@ rows_merge_kernel(const Args a, int warps) {
     }
   }
   if (!live) return;
-  const float f = l > 0.f ? ptx::ex2(R - M) / l : (l == 0.f ? 0.f : l);
+  const float f = l > 0.f ? ptx::ex2(R) / l : (l == 0.f ? 0.f : l);
   const size_t tok = (size_t)(Q.q0 + row / G);
   const int head = g * G + row % G;
   const size_t orow = tok * a.H + head;
