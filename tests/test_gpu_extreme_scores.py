@@ -52,3 +52,34 @@ def test_equal_scores(d, new, group, L, score):
         bound = 2.0 ** -8 * np.abs(mean) + (2.0 ** -8 + L * 2.0 ** -23) * a
         assert (np.abs(o - mean) <= bound).all(), f"O off by {np.abs(o - mean).max()}"
         assert (np.abs(lse - (x + np.log(L))) <= 2.0 ** -21 * (abs(x) + 20)).all()
+
+
+# (Not -1e31 on the tcgen05 forward: it takes the rounded reference off the exact product of score
+# and log2(e) scale.  Up to 2^-25 of the product is left, which past 2^31 no exponential can hold; a
+# power of two leaves nothing.)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,group,score", [(1, 1, -1e31), (1, 12, -1e31), (3, 4, -1e31), (1, 1, -2.0 ** 120),
+                                             (1, 12, -2.0 ** 120), (3, 4, -2.0 ** 120), (60, 4, -2.0 ** 120)])
+@pytest.mark.parametrize("L", [1, 2500])
+def test_most_negative_scores(d, new, group, L, score):
+    """A row all of whose scores lie near the end of fp32's range is not one that sees no key."""
+    test_equal_scores(d, new, group, L, score)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,group", [(1, 1), (1, 12), (3, 4), (60, 4)])
+def test_scores_from_end_to_end(d, new, group):
+    """Scores from -2^120 to 2^120 in one row: the largest takes all."""
+    rng = np.random.default_rng(d)
+    L = 2500
+    k = np.zeros((L, 1, d))
+    k[:, 0, 3] = -2.0 ** 60 * rng.choice([0.0, 0.5, 1.0], L)
+    best = 1700
+    k[best, 0, 3] = 2.0 ** 60
+    v = E.bf16(rng.standard_normal((L, 1, d)))[1]
+    q = np.zeros((new, group, d))
+    q[:, :, 3] = 2.0 ** 60
+    c = E.Cache(rng, [k], [v], max_blocks=160)
+    for o, lse in _run(c, E.bf16(q)[0], new, d):
+        assert (o == c.rows["v"][0][best, 0]).all()     # codes times a power of two are bf16 values
+        assert (np.abs(lse / 2.0 ** 120 - 1) <= 2.0 ** -21).all()

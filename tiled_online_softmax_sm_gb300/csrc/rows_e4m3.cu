@@ -75,7 +75,7 @@ constexpr float kUnder = 7.f;         // how far r lies below the largest weight
 // The reference of a row that has seen no key (its r is 0): finite, so that
 // 2^(x - m) is 0 for a masked x = -inf without a guard, and below every score of
 // finite rows.
-constexpr float kNone = -1e30f;
+constexpr float kNone = -3.4e38f;
 
 template <int D, int NT, bool STREAM>
 struct Geo {
