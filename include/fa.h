@@ -416,11 +416,20 @@ fa_status fa_paged_kv_read_e4m3(const void* k_cache, const void* v_cache, const 
 /*
  * fa_paged_e4m3_workspace_size — bytes of the optional workspace of
  * fa_paged_decode_e4m3 (max_seqlen_q 1) and fa_paged_prefill_e4m3: partials of
- * a few long sequences whose keys are split over the GPU.  0 where the calls
- * use none (enough work without splitting) or for invalid sizes.  (A prefill of
- * fewer rows than the bound may run without the workspace it was sized for.)
+ * a few long sequences whose keys are split over the GPU.  Enough for every
+ * table width and window of these sizes (for batches whose sequences are too
+ * many to be split, too, although no call of theirs uses it); 0 where the form
+ * that takes them has no partials, or for invalid sizes.  (A prefill of fewer
+ * rows than the bound may run without the workspace it was sized for.)
+ *
+ * fa_paged_e4m3_workspace_used — the same bytes where a call with these
+ * arguments splits its keys when it is given them, 0 where it runs without:
+ * enough work as it is, or contexts (max_blocks_per_seq, or the window and
+ * sinks) too short.  max_seqlen_q counts up to the call's total_q.
  */
 size_t fa_paged_e4m3_workspace_size(int num_seqs, int max_seqlen_q, int H, int Hkv, int d);
+size_t fa_paged_e4m3_workspace_used(int num_seqs, int max_seqlen_q, int H, int Hkv, int d,
+                                    int max_blocks_per_seq, int causal, int window, int sinks);
 
 /*
  * fa_paged_decode_e4m3 — one query token per sequence against the e4m3 paged
@@ -435,8 +444,9 @@ size_t fa_paged_e4m3_workspace_size(int num_seqs, int max_seqlen_q, int H, int H
  *   sinks   keys from the start that stay visible under a window (ignored
  *           without one)
  *   workspace  device scratch of at least fa_paged_e4m3_workspace_size() bytes,
- *           256-byte aligned, or NULL.  A call normally runs in one launch, a
- *           thread-block cluster per (sequence, kv head) that splits the keys
+ *           256-byte aligned, or NULL; of any size where num_seqs * Hkv is
+ *           above 38: no such call uses it.  A call normally runs in one launch,
+ *           a thread-block cluster per (sequence, kv head) that splits the keys
  *           and merges; with a workspace, a few long sequences are instead cut
  *           into equal shares for every warp of the GPU, with a merge launch
  *           behind.  The workspace needs no initialisation; calls on one
@@ -468,7 +478,8 @@ fa_status fa_paged_decode_e4m3(const void* q, const void* k_cache, const void* v
  *   window, sinks  as fa_paged_decode_e4m3, for each query from its own
  *                  position p: keys j <= p with j > p - window or j < sinks;
  *                  a window needs causal = 1
- *   workspace      as fa_paged_decode_e4m3
+ *   workspace      as fa_paged_decode_e4m3 (of any size only for the chunks that
+ *                  run as it does)
  * A sequence with bad offsets, more than max_seqlen_q queries or a bad
  * seq_lens[s] is skipped (its rows are not written) and sets
  * FA_ERR_INVALID_ARG.  Bad page ids set FA_ERR_BAD_BLOCK_TABLE; the sequence's

@@ -15,6 +15,7 @@ points.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -39,7 +40,7 @@ EXPORTED = ("fa_forward", "fa_forward_fp8", "fa_forward_f32", "fa_forward_varlen
             "fa_paged_decode", "fa_paged_decode_fused", "fa_paged_decode_noalloc", "fa_paged_gather", "fa_split_combine",
             "fa_forward_window", "fa_forward_varlen_window",
             "fa_paged_kv_write_e4m3", "fa_paged_kv_read_e4m3", "fa_paged_e4m3_workspace_size",
-            "fa_paged_decode_e4m3", "fa_paged_prefill_e4m3",
+            "fa_paged_e4m3_workspace_used", "fa_paged_decode_e4m3", "fa_paged_prefill_e4m3",
             "fa_last_error",
             "fa_get_device_status")
 FA_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -89,6 +90,8 @@ def load(path: str = LIB_PATH):
         lib.fa_paged_prefill_e4m3.argtypes = [P] * 10 + [I, I, I, I, I, I, I, I, I, F, I, I, I, P, Z, P]
         lib.fa_paged_e4m3_workspace_size.argtypes = [I] * 5
         lib.fa_paged_e4m3_workspace_size.restype = Z
+        lib.fa_paged_e4m3_workspace_used.argtypes = [I] * 9
+        lib.fa_paged_e4m3_workspace_used.restype = Z
         lib.fa_last_error.argtypes = []
         lib.fa_last_error.restype = ctypes.c_char_p
         lib.fa_get_device_status.argtypes = [P, ctypes.POINTER(I)]
@@ -252,6 +255,13 @@ def fa_paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_l
 
 def fa_paged_e4m3_workspace_size(num_seqs, max_seqlen_q, H, Hkv, d) -> int:
     return int(load().fa_paged_e4m3_workspace_size(num_seqs, max_seqlen_q, H, Hkv, d))
+
+
+def fa_paged_e4m3_workspace_used(num_seqs, max_seqlen_q, H, Hkv, d, max_blocks_per_seq, causal=True,
+                                 window=0, sinks=0) -> int:
+    return int(load().fa_paged_e4m3_workspace_used(num_seqs, max_seqlen_q, H, Hkv, d,
+                                                   max_blocks_per_seq, int(causal), int(window),
+                                                   int(sinks)))
 
 
 def fa_paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, o, lse,
@@ -521,18 +531,21 @@ def paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
     return k, v
 
 
-def _e4m3_workspace(fn, workspace, q, S, max_q, H, Hkv, d, max_blocks, stream):
-    """Address and bytes of the caller's workspace, of a new one where few units share long
-    sequences, or of none; and the tensor, to be kept until the call is queued.  (None on a stream
-    that is not torch's current one: a new one could be given out again before the call is done.)"""
+@functools.lru_cache(maxsize=4096)
+def _e4m3_workspace_used(*sizes):
+    """fa_paged_e4m3_workspace_used, which depends on the sizes alone (asked for every call of the
+    serving path, where the C call would take 1 us each time)."""
+    return int(load().fa_paged_e4m3_workspace_used(*sizes))
+
+
+def _e4m3_workspace(fn, workspace, q, S, max_q, H, Hkv, d, max_blocks, causal, window, sinks, stream):
+    """Address and bytes of the caller's workspace, of a new one where the call uses it, or of none;
+    and the tensor, to be kept until the call is queued.  (None on a stream that is not torch's
+    current one: a new one could be given out again before the call is done.)"""
     if workspace is None:
-        if stream is not None or max_blocks < 32:
+        if stream is not None:
             return None, 0, None
-        if S * Hkv > 38 or max_blocks < 128:   # then the rows kernels use none
-            G = H // max(Hkv, 1)
-            if max_q == 1 or max_q * G <= 16 or (max_q * G <= 32 and (d == 64 or G & (G - 1))):
-                return None, 0, None
-        need = fa_paged_e4m3_workspace_size(S, max_q, H, Hkv, d)
+        need = _e4m3_workspace_used(S, max_q, H, Hkv, d, max_blocks, causal, window, sinks)
         if not need:
             return None, 0, None
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
@@ -554,7 +567,8 @@ def paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_le
     _check_rows(fn, device, "q", q, torch.bfloat16, (S, H, d))
     o = torch.empty_like(q)
     lse = torch.empty((S, H), dtype=torch.float32, device=q.device)
-    ws, ws_bytes, keep = _e4m3_workspace(fn, workspace, q, S, 1, H, Hkv, d, max_blocks, stream)
+    ws, ws_bytes, keep = _e4m3_workspace(fn, workspace, q, S, 1, H, Hkv, d, max_blocks, 1, window,
+                                         sinks, stream)
     lib = _lib or load()
     _check(lib.fa_paged_decode_e4m3(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
@@ -578,8 +592,8 @@ def paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_l
     _check_rows(fn, device, "cu_seqlens_q", cu_seqlens_q, torch.int32, (S + 1,))
     o = torch.empty_like(q)
     lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
-    ws, ws_bytes, keep = _e4m3_workspace(fn, workspace, q, S, max_seqlen_q, H, Hkv, d,
-                                         max_blocks, stream)
+    ws, ws_bytes, keep = _e4m3_workspace(fn, workspace, q, S, max_seqlen_q, H, Hkv, d, max_blocks,
+                                         1 if causal else 0, window, sinks, stream)
     lib = _lib or load()
     _check(lib.fa_paged_prefill_e4m3(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),

@@ -556,14 +556,25 @@ fa_status check_heads(const char* fn, const void* q, const void* o, const float*
   return FA_OK;
 }
 
-// The workspace of the e4m3 attention entries is optional.
+bool uses_workspace(int num_seqs, int max_q, int H, int Hkv, int d, int max_blocks, int causal,
+                    int window, int sinks) {
+  return fa::rows_e4m3_form(max_q, H, Hkv, d)
+             ? fa::rows_e4m3_uses_workspace(num_seqs, max_q, H, Hkv, d, max_blocks, causal, window, sinks)
+             : fa::cache_parts_taken(num_seqs, max_q, H, Hkv, max_blocks, causal, window, sinks) > 1;
+}
+
+// The workspace of the e4m3 attention entries is optional; where no call of the
+// rows kernels over so many units uses one, it may have any size.
 fa_status check_e4m3_workspace(const char* fn, const void* workspace, size_t bytes, int num_seqs,
                                int max_q, int H, int Hkv, int d) {
   if (workspace == nullptr) return FA_OK;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(FA_ERR_WORKSPACE, "%s: workspace %p is not 256-byte aligned", fn, workspace);
+  if (fa::rows_e4m3_form(max_q, H, Hkv, d) && !fa::rows_e4m3_few_units(num_seqs, Hkv)) return FA_OK;
   const size_t need = fa::rows_e4m3_workspace(num_seqs, max_q, H, Hkv, d);
-  if (bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
-    return fail(FA_ERR_WORKSPACE, "%s: workspace %p of %zu bytes (need %zu, 256-byte aligned)", fn,
-                workspace, bytes, need);
+  if (bytes < need)
+    return fail(FA_ERR_WORKSPACE, "%s: workspace %p of %zu bytes (need %zu)", fn, workspace, bytes,
+                need);
   return FA_OK;
 }
 
@@ -576,6 +587,16 @@ size_t fa_paged_e4m3_workspace_size(int num_seqs, int max_seqlen_q, int H, int H
       (d != 64 && d != 128))
     return 0;
   return fa::rows_e4m3_workspace(num_seqs, max_seqlen_q, H, Hkv, d);
+}
+
+size_t fa_paged_e4m3_workspace_used(int num_seqs, int max_seqlen_q, int H, int Hkv, int d,
+                                    int max_blocks_per_seq, int causal, int window, int sinks) {
+  const size_t need = fa_paged_e4m3_workspace_size(num_seqs, max_seqlen_q, H, Hkv, d);
+  if (need == 0 || max_blocks_per_seq <= 0 || window < 0 || sinks < 0) return 0;
+  return uses_workspace(num_seqs, max_seqlen_q, H, Hkv, d, max_blocks_per_seq, causal,
+                        effective_window(window, max_blocks_per_seq * 16ll), sinks)
+             ? need
+             : 0;
 }
 
 fa_status fa_paged_kv_write_e4m3(const void* k, const void* v, void* k_cache, void* v_cache,

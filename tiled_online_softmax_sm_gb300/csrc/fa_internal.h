@@ -136,6 +136,19 @@ inline size_t cache_parts_bytes(int num_seqs, int max_q, int H, int Hkv, int d) 
   return (size_t)packed_units(num_seqs, max_q, H, Hkv) * parts * 256 * (d + 4) * 4;
 }
 
+// The parts of a launch: no more than one per two K/V tiles (of 128 keys) that a
+// unit can have.
+inline int cache_parts_taken(int num_seqs, int max_q, int H, int Hkv, int max_blocks, int causal,
+                             int window, int sinks) {
+  long long keys = max_blocks * 16ll;
+  if (causal && window > 0) {
+    const long long seen = (long long)window + (256 >> packed_heads_log2(H, Hkv)) + sinks + 256;
+    if (seen < keys) keys = seen;
+  }
+  const long long most = keys / 256, parts = cache_parts(num_seqs, max_q, H, Hkv);
+  return (int)(most < 1 ? 1 : parts < most ? parts : most);
+}
+
 struct DecodeParams {
   const void* q;
   const void* k_cache;
@@ -227,7 +240,12 @@ inline bool rows_e4m3_form(int max_q, int H, int Hkv, int d) {
   if (max_q == 1 || rows <= 16) return true;
   return rows <= kRowsE4m3Max && (d == 64 || (g & (g - 1)) != 0);
 }
+// Bytes for any table width and window of these sizes, and whether the rows
+// kernels use them for the given ones.
 size_t rows_e4m3_workspace(int num_seqs, int max_q, int H, int Hkv, int d);
+bool rows_e4m3_few_units(int num_seqs, int Hkv);   // false: never used, whatever the other sizes
+bool rows_e4m3_uses_workspace(int num_seqs, int max_q, int H, int Hkv, int d, int max_blocks,
+                              int causal, int window, int sinks);
 cudaError_t launch_rows_e4m3(const PagedE4m3Params& p, cudaStream_t stream, const char** why);
 cudaError_t launch_fwd_f32(const FwdParams& p, cudaStream_t stream);
 cudaError_t launch_fwd_bf16(const FwdParams& p, cudaStream_t stream, const char** why);

@@ -1697,12 +1697,8 @@ cudaError_t launch(const FwdParams& p, cudaStream_t stream, const char** why) {
   }
   const int num_pairs = (int)(((long long)p.n + pair_q - 1) / pair_q);
   int parts = 1;
-  if (KV8 && p.workspace != nullptr) {
-    // no more than one part per two K/V tiles that a unit can have
-    long long keys = p.max_blocks * 16ll;
-    if (p.causal && p.window > 0) keys = std::min(keys, (long long)p.window + pair_q + p.sinks + 2 * kBlockN);
-    parts = (int)std::max(1ll, std::min((long long)cache_parts(p.B, p.n, p.H, p.Hkv), keys / (2 * kBlockN)));
-  }
+  if (KV8 && p.workspace != nullptr)
+    parts = cache_parts_taken(p.B, p.n, p.H, p.Hkv, p.max_blocks, p.causal, p.window, p.sinks);
   const long long units = (long long)p.B * (p.H >> gl) * num_pairs * parts;
   float* const part_s = static_cast<float*>(p.workspace);
   float* const part_o = part_s + units * 2 * kBlockM * 4;

@@ -1081,6 +1081,27 @@ rows_merge_kernel(const Args a, int warps) {
   }
 }
 
+// The most pages a unit can have: the table's, or the window's.
+long long unit_pages(int max_blocks, int max_q, int causal, int window, int sinks) {
+  if (!causal || window <= 0) return max_blocks;
+  const long long w = ((long long)window + max_q + 30) / 16 + (sinks + 15ll) / 16;
+  return w < max_blocks ? w : max_blocks;
+}
+
+// The stream form, for few long units that clusters of 8 leave most of the
+// machine idle on: 1 x 131072 tokens 203 (C = 8) against 54 us, 1 x 8192 18
+// against 13.4, 4 x [512, 8192] 16.8 against 15.4; but 1 x 1000 7.5 against 8.5.
+template <int D, int NT>
+bool few_units(long long units) {
+  return 2 * 8 * units <= Geo<D, NT, false>::kCtasPerSm * 152;
+}
+template <int D, int NT>
+bool takes_shares(int num_seqs, int Hkv, int max_blocks, long long pages) {
+  const long long units = (long long)num_seqs * Hkv;
+  return num_seqs <= kMaxSeqs && units * max_blocks <= 0x7fffffffLL && pages >= 128 &&
+         few_units<D, NT>(units);
+}
+
 template <int D, int NT>
 cudaError_t launch(const PagedE4m3Params& p, cudaStream_t stream, const char** why) {
   using GC = Geo<D, NT, false>;
@@ -1096,12 +1117,7 @@ cudaError_t launch(const PagedE4m3Params& p, cudaStream_t stream, const char** w
     return cudaErrorInvalidValue;
   }
   const long long units = (long long)p.num_seqs * p.Hkv;
-  // the most pages a unit can have: the table's, or the window's
-  long long pages = p.max_blocks;
-  if (p.causal && p.window > 0) {
-    const long long w = ((long long)p.window + p.max_q + 30) / 16 + (p.sinks + 15ll) / 16;
-    if (w < pages) pages = w;
-  }
+  const long long pages = unit_pages(p.max_blocks, p.max_q, p.causal, p.window, p.sinks);
   Args a{static_cast<const __nv_bfloat16*>(p.q), static_cast<const uint8_t*>(p.k_scale),
          static_cast<const uint8_t*>(p.v_scale), p.block_table, p.seq_lens, p.cu_q,
          static_cast<__nv_bfloat16*>(p.o), p.lse, p.cu_q ? 1 : p.H, p.cu_q ? p.total_q : 1,
@@ -1128,13 +1144,7 @@ cudaError_t launch(const PagedE4m3Params& p, cudaStream_t stream, const char** w
   const bool alike = p.causal && p.window > 0 && 2 * pages <= p.max_blocks;
   int C = 1;
   while (C < 8 && 4 * units * 2 * C <= (alike ? 4 : 7) * room && pages >= 4ll * C * kWarps) C *= 2;
-  // The stream form, for few long units that clusters of 8 leave most of the
-  // machine idle on: 1 x 131072 tokens 203 (C = 8) against 54 us, 1 x 8192 18
-  // against 13.4, 4 x [512, 8192] 16.8 against 15.4; but 1 x 1000 7.5 against 8.5.
-  const bool stream_form = p.workspace != nullptr && p.num_seqs <= kMaxSeqs &&
-                           units * p.max_blocks <= 0x7fffffffLL && pages >= 128 &&
-                           2 * 8 * units <= room;
-  if (stream_form) {
+  if (p.workspace != nullptr && takes_shares<D, NT>(p.num_seqs, p.Hkv, p.max_blocks, pages)) {
     const size_t slots = (size_t)(W + units) * kRows;
     a.part_s = static_cast<float*>(p.workspace);
     a.part_o = a.part_s + slots * 4;
@@ -1206,6 +1216,27 @@ size_t rows_e4m3_workspace(int num_seqs, int max_q, int H, int Hkv, int d) {
                      : rows <= 16 ? stream_bytes<128, 2>(units) : stream_bytes<128, 4>(units);
   return rows <= 8 ? stream_bytes<64, 1>(units)
                    : rows <= 16 ? stream_bytes<64, 2>(units) : stream_bytes<64, 4>(units);
+}
+
+bool rows_e4m3_few_units(int num_seqs, int Hkv) {   // (the 8-row form's limit is the largest)
+  return few_units<128, 1>((long long)num_seqs * Hkv) || few_units<64, 1>((long long)num_seqs * Hkv);
+}
+
+namespace {
+template <int D>
+bool uses_workspace(int num_seqs, int max_q, int H, int Hkv, int max_blocks, long long pages) {
+  const long long rows = (long long)max_q * (H / Hkv);
+  if (rows <= 8) return takes_shares<D, 1>(num_seqs, Hkv, max_blocks, pages);
+  if (rows <= 16) return takes_shares<D, 2>(num_seqs, Hkv, max_blocks, pages);
+  return rows <= kRowsE4m3Max && takes_shares<D, 4>(num_seqs, Hkv, max_blocks, pages);
+}
+}  // namespace
+
+bool rows_e4m3_uses_workspace(int num_seqs, int max_q, int H, int Hkv, int d, int max_blocks,
+                              int causal, int window, int sinks) {
+  const long long pages = unit_pages(max_blocks, max_q, causal, window, sinks);
+  return d == 128 ? uses_workspace<128>(num_seqs, max_q, H, Hkv, max_blocks, pages)
+                  : uses_workspace<64>(num_seqs, max_q, H, Hkv, max_blocks, pages);
 }
 
 cudaError_t launch_rows_e4m3(const PagedE4m3Params& p, cudaStream_t stream, const char** why) {
