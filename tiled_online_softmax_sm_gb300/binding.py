@@ -581,7 +581,8 @@ def paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_le
 def paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens_q,
                        max_seqlen_q, scale, causal=True, window=0, sinks=0, workspace=None,
                        stream=None):
-    """q [Tq,H,d] packed by cu_seqlens_q over the e4m3 cache -> (o [Tq,H,d], lse [H,Tq])."""
+    """q [Tq,H,d] packed by cu_seqlens_q over the e4m3 cache -> (o [Tq,H,d], lse [H,Tq]).
+    max_seqlen_q may be any upper bound of the sequences' query counts."""
     fn = "paged_prefill_e4m3"
     device = q.get_device()
     _check_cache(fn, device, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
@@ -592,6 +593,8 @@ def paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_l
     _check_rows(fn, device, "cu_seqlens_q", cu_seqlens_q, torch.int32, (S + 1,))
     o = torch.empty_like(q)
     lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
+    if workspace is None:   # (a caller's own is sized for the caller's bound)
+        max_seqlen_q = min(max_seqlen_q, Tq)
     ws, ws_bytes, keep = _e4m3_workspace(fn, workspace, q, S, max_seqlen_q, H, Hkv, d, max_blocks,
                                          1 if causal else 0, window, sinks, stream)
     lib = _lib or load()
