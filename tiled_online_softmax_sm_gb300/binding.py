@@ -10,7 +10,8 @@ library is missing or cannot be loaded, the first call raises.
 The helpers at the end (``forward``, ``forward_f32``, ``forward_varlen``,
 ``paged_decode``, ``paged_decode_fused``, the e4m3 cache's ``paged_..._e4m3``,
 ``split_combine``) allocate outputs with torch and then call the same entry
-points.
+points.  Only they and a call's default stream import torch: the entry points
+themselves, with plain addresses and a given stream, do without it.
 """
 from __future__ import annotations
 
@@ -18,8 +19,6 @@ import ctypes
 import functools
 import os
 import threading
-
-import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # FA_LIBRARY selects another build of the same ABI (the debug build,
@@ -128,11 +127,31 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-# The same for a device that is known to be the current one, and the current
-# device once there are tensors on one.
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda device: torch.cuda.current_stream(device).cuda_stream)
+class _Torch:
+    """Stands for torch until its first use, which imports it."""
+
+    def __getattr__(self, name):
+        global torch
+        import torch
+        return getattr(torch, name)
+
+
+torch = _Torch()
+
+# Set by _bind_torch, before the e4m3 helpers' first check: the current stream of a device that is
+# known to be the current one, the current device once there are tensors on one, and the types of
+# the e4m3 cache's codes and scales.
+_current_raw_stream = _current_device = _CODES = _SCALES = None
+
+
+def _bind_torch():
+    global _current_raw_stream, _current_device, _CODES, _SCALES
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _SCALES = frozenset((torch.uint8, torch.int8) +
+                        ((torch.float8_e8m0fnu,) if hasattr(torch, "float8_e8m0fnu") else ()))
+    _CODES = frozenset((torch.float8_e4m3fn, torch.uint8, torch.int8))
 
 
 def _check(rc: int):
@@ -423,11 +442,6 @@ def paged_decode_fused(q, k_cache, v_cache, block_table, seq_lens, num_splits, s
     return o, lse
 
 
-_CODES = frozenset((torch.float8_e4m3fn, torch.uint8, torch.int8))
-_SCALES = frozenset((torch.uint8, torch.int8) +
-                    ((torch.float8_e8m0fnu,) if hasattr(torch, "float8_e8m0fnu") else ()))
-
-
 def _refuse(fn, device, *named):
     """Raise for the first of (name, tensor, types, shape) that is not a contiguous tensor of one of
     those types and that shape on the current CUDA device: the C entry sees only its address."""
@@ -459,6 +473,8 @@ def _check_tensors(fn, device, *named):
 def _check_cache(fn, device, kc, vc, ks, vs, bt, sl):
     """The paged e4m3 cache's tensors: code and scale caches, block table and lengths.  (Written
     out: it runs on every call of the serving path, where a loop over them takes twice as long.)"""
+    if _CODES is None:
+        _bind_torch()
     shape, table = kc.shape, bt.shape
     if len(shape) != 4 or len(table) != 2:
         raise FaError(FA_ERR_INVALID_ARG, f"{fn}: k_cache has shape {tuple(shape)}, block_table "
