@@ -55,3 +55,46 @@ def test_a_loose_bound_gets_the_workspace_of_the_rows_at_hand(spy, tokens, bound
     ref = E.attend(q.double().numpy(), c.rows["k"][0], c.rows["v"][0], 0.1, vexp=c.vexp[0])
     E.check(o.double().cpu().numpy(), lse.double().cpu().numpy().T, ref, 128, 2.0 ** -7 * 1.01)
     assert fb.fa_get_device_status() == 0
+
+
+def _given(kind):
+    """(what the caller passes, the stream to wait for)"""
+    side = torch.cuda.Stream()
+    if kind == "handle":
+        return side.cuda_stream, side
+    if kind == "current":
+        return torch.cuda.current_stream(), torch.cuda.current_stream()
+    return (0, torch.cuda.default_stream()) if kind == "default" else (side, side)
+
+
+@pytest.mark.parametrize("kind", ["stream", "handle", "default", "current"])
+def test_a_given_stream_has_outputs_and_workspace_of_its_own(spy, kind):
+    """The keys are split on a given stream too, and what the helper allocates comes from that
+    stream's memory, not from a block that work queued on the current one may still read."""
+    rng = np.random.default_rng(61)
+    c = _long(rng)
+    t, cu = c.gpu(), _i32([0, 60])
+    q1, q2 = (E.bf16(rng.standard_normal((n, 8, 128)))[0].cuda() for n in (1, 60))
+    k = E.bf16(rng.standard_normal((1, 60, 2, 128)))[0].cuda()
+    calls = (lambda **s: fb.paged_decode_e4m3(q1, *t, 0.1, **s),
+             lambda **s: fb.paged_prefill_e4m3(q2, *t, cu, 60, 0.1, **s),
+             lambda **s: fb.paged_kv_read_e4m3(*t, _i32([0, 60]), 60, **s),
+             lambda **s: fb.forward_window(q2[None], k, k, 0.1, 20, 2, **s),
+             lambda **s: fb.forward_varlen_window(q2, k[0], k[0], cu, cu, 60, 60, 0.1, 20, 2, **s))
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+    for f, w in zip(calls, want):
+        stream, waited = _given(kind)
+        before = torch.empty_like(w[0])      # the block that the next allocation of this size gets
+        at = before.data_ptr()
+        del before
+        got = f(stream=stream)
+        if kind in ("stream", "handle"):
+            assert got[0].data_ptr() != at
+        waited.synchronize()
+        for a, b in zip(got, w):
+            assert torch.equal(a, b)
+    for entry in ("fa_paged_decode_e4m3", "fa_paged_prefill_e4m3"):
+        with_ws = spy.workspace_bytes(entry)
+        assert len(with_ws) == 2 and with_ws[0] == with_ws[1] > 0
+    assert fb.fa_get_device_status() == 0

@@ -322,6 +322,16 @@ def fa_last_error() -> str:
 
 
 # ------------------------------------------------ torch-allocating helpers
+def _given(stream):
+    """Makes a given stream (a torch stream, or a handle) torch's current one, for the helpers of the
+    windowed forward and of the e4m3 cache: outputs and workspace then belong to it, and a block that
+    torch gets back from another stream's work is not given out to this one's before that is done."""
+    raw = _stream(stream)
+    if isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream())
+
+
 def forward(q, k, v, scale, causal=False, stream=None):
     """q [B,n,H,d], k [B,m,Hkv,d], v [B,m,Hkv,dv] bf16 CUDA tensors -> (o bf16, lse fp32 [B,H,n])."""
     B, n, H, d = q.shape
@@ -368,13 +378,16 @@ def forward_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen
 def forward_window(q, k, v, scale, window, sinks=0, stream=None):
     """q [B,n,H,d], k/v [B,m,Hkv,d] bf16, causal under a sliding window with sinks
     -> (o [B,n,H,d] bf16, lse [B,H,n] fp32)."""
+    if stream is not None:
+        with _given(stream):
+            return forward_window(q, k, v, scale, window, sinks)
     B, n, H, d = q.shape
     m, Hkv = k.shape[1:3]
     _check_tensors("forward_window", q.get_device(), ("q", q, torch.bfloat16, (B, n, H, d)),
              ("k", k, torch.bfloat16, (B, m, Hkv, d)), ("v", v, torch.bfloat16, (B, m, Hkv, d)))
     o = torch.empty_like(q)
     lse = torch.empty((B, H, n), dtype=torch.float32, device=q.device)
-    fa_forward_window(q, k, v, o, lse, B, H, Hkv, n, m, d, d, scale, window, sinks, stream)
+    fa_forward_window(q, k, v, o, lse, B, H, Hkv, n, m, d, d, scale, window, sinks)
     return o, lse
 
 
@@ -382,6 +395,10 @@ def forward_varlen_window(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max
                           window, sinks=0, stream=None):
     """Packed q [Tq,H,d], k/v [Tk,Hkv,d] bf16, causal under a sliding window with sinks
     -> (o [Tq,H,d] bf16, lse [H,Tq] fp32)."""
+    if stream is not None:
+        with _given(stream):
+            return forward_varlen_window(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                                         max_seqlen_k, scale, window, sinks)
     Tq, H, d = q.shape
     Tk, Hkv = k.shape[:2]
     S = cu_seqlens_q.shape[0] - 1
@@ -392,7 +409,7 @@ def forward_varlen_window(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max
     o = torch.empty_like(q)
     lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
     fa_forward_varlen_window(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, S, Tq, Tk, max_seqlen_q,
-                             max_seqlen_k, H, Hkv, d, d, scale, window, sinks, stream)
+                             max_seqlen_k, H, Hkv, d, d, scale, window, sinks)
     return o, lse
 
 
@@ -530,6 +547,10 @@ def paged_kv_write_e4m3(k, v, k_cache, v_cache, k_scale, v_scale, block_table, s
 def paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens,
                        total, stream=None):
     """The last n_s cached rows of every sequence -> (k, v) [total,Hkv,d] bf16."""
+    if stream is not None:
+        with _given(stream):
+            return paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                                      cu_seqlens, total)
     fn = "paged_kv_read_e4m3"
     device = k_cache.get_device()
     _check_cache(fn, device, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
@@ -542,8 +563,7 @@ def paged_kv_read_e4m3(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
     _check(lib.fa_paged_kv_read_e4m3(
         k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(), k.data_ptr(),
-        v.data_ptr(), S, total, Hkv, d, page, P, max_blocks,
-        _current_raw_stream(device) if stream is None else _stream(stream)))
+        v.data_ptr(), S, total, Hkv, d, page, P, max_blocks, _current_raw_stream(device)))
     return k, v
 
 
@@ -554,13 +574,10 @@ def _e4m3_workspace_used(*sizes):
     return int(load().fa_paged_e4m3_workspace_used(*sizes))
 
 
-def _e4m3_workspace(fn, workspace, q, S, max_q, H, Hkv, d, max_blocks, causal, window, sinks, stream):
+def _e4m3_workspace(fn, workspace, q, S, max_q, H, Hkv, d, max_blocks, causal, window, sinks):
     """Address and bytes of the caller's workspace, of a new one where the call uses it, or of none;
-    and the tensor, to be kept until the call is queued.  (None on a stream that is not torch's
-    current one: a new one could be given out again before the call is done.)"""
+    and the tensor, to be kept until the call is queued."""
     if workspace is None:
-        if stream is not None:
-            return None, 0, None
         need = _e4m3_workspace_used(S, max_q, H, Hkv, d, max_blocks, causal, window, sinks)
         if not need:
             return None, 0, None
@@ -574,6 +591,10 @@ def _e4m3_workspace(fn, workspace, q, S, max_q, H, Hkv, d, max_blocks, causal, w
 def paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale,
                       window=0, sinks=0, workspace=None, stream=None):
     """q [S,H,d]; e4m3 cache [P,Hkv,16,d] with scale bytes [P,Hkv,16] -> (o [S,H,d], lse [S,H])."""
+    if stream is not None:
+        with _given(stream):
+            return paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                                     scale, window, sinks, workspace)
     fn = "paged_decode_e4m3"
     device = q.get_device()
     _check_cache(fn, device, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
@@ -584,13 +605,13 @@ def paged_decode_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_le
     o = torch.empty_like(q)
     lse = torch.empty((S, H), dtype=torch.float32, device=q.device)
     ws, ws_bytes, keep = _e4m3_workspace(fn, workspace, q, S, 1, H, Hkv, d, max_blocks, 1, window,
-                                         sinks, stream)
+                                         sinks)
     lib = _lib or load()
     _check(lib.fa_paged_decode_e4m3(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
         v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
         lse.data_ptr(), S, H, Hkv, d, page, P, max_blocks, scale, window, sinks, ws, ws_bytes,
-        _current_raw_stream(device) if stream is None else _stream(stream)))
+        _current_raw_stream(device)))
     return o, lse
 
 
@@ -599,6 +620,11 @@ def paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_l
                        stream=None):
     """q [Tq,H,d] packed by cu_seqlens_q over the e4m3 cache -> (o [Tq,H,d], lse [H,Tq]).
     max_seqlen_q may be any upper bound of the sequences' query counts."""
+    if stream is not None:
+        with _given(stream):
+            return paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                                      cu_seqlens_q, max_seqlen_q, scale, causal, window, sinks,
+                                      workspace)
     fn = "paged_prefill_e4m3"
     device = q.get_device()
     _check_cache(fn, device, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
@@ -612,14 +638,13 @@ def paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_l
     if workspace is None:   # (a caller's own is sized for the caller's bound)
         max_seqlen_q = min(max_seqlen_q, Tq)
     ws, ws_bytes, keep = _e4m3_workspace(fn, workspace, q, S, max_seqlen_q, H, Hkv, d, max_blocks,
-                                         1 if causal else 0, window, sinks, stream)
+                                         1 if causal else 0, window, sinks)
     lib = _lib or load()
     _check(lib.fa_paged_prefill_e4m3(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
         v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens_q.data_ptr(),
         o.data_ptr(), lse.data_ptr(), S, Tq, max_seqlen_q, H, Hkv, d, page, P, max_blocks, scale,
-        1 if causal else 0, window, sinks, ws, ws_bytes,
-        _current_raw_stream(device) if stream is None else _stream(stream)))
+        1 if causal else 0, window, sinks, ws, ws_bytes, _current_raw_stream(device)))
     return o, lse
 
 
