@@ -98,3 +98,39 @@ def test_a_given_stream_has_outputs_and_workspace_of_its_own(spy, kind):
         with_ws = spy.workspace_bytes(entry)
         assert len(with_ws) == 2 and with_ws[0] == with_ws[1] > 0
     assert fb.fa_get_device_status() == 0
+
+
+def test_the_workspace_query_is_kept_by_value():
+    """Counts that come as tensors are not kept alive, nor told apart by identity."""
+    c = _long(np.random.default_rng(63), L=300)
+    t, q = c.gpu(), torch.zeros((60, 8, 128), dtype=torch.bfloat16, device="cuda")
+    fb._e4m3_workspace_used.cache_clear()
+    for _ in range(3):
+        fb.paged_prefill_e4m3(q, *t, _i32([0, 60]), torch.tensor(60), 0.1, window=torch.tensor(50))
+    assert fb._e4m3_workspace_used.cache_info().currsize == 1
+
+
+@pytest.mark.parametrize("scale", [np.float32(0.125), np.float64(0.125), torch.tensor(0.125)])
+@pytest.mark.parametrize("integer", [np.int32, np.int64, torch.tensor])
+def test_numbers_of_other_types(scale, integer):
+    """Scales and counts as numpy and torch give them (a scale of float32(1 / sqrt(d)), a maximum of
+    a length tensor), as the other helpers take them."""
+    rng = np.random.default_rng(62)
+    c = _long(rng, L=300)
+    t, cu = c.gpu(), _i32([0, 60])
+    q1, q2 = (E.bf16(rng.standard_normal((n, 8, 128)))[0].cuda() for n in (1, 60))
+    k = E.bf16(rng.standard_normal((60, 2, 128)))[0].cuda()
+    i = integer
+    for got, want in (
+            (fb.paged_decode_e4m3(q1, *t, scale, window=i(50), sinks=i(2)),
+             fb.paged_decode_e4m3(q1, *t, 0.125, window=50, sinks=2)),
+            (fb.paged_prefill_e4m3(q2, *t, cu, i(60), scale, window=i(50), sinks=i(2)),
+             fb.paged_prefill_e4m3(q2, *t, cu, 60, 0.125, window=50, sinks=2)),
+            (fb.paged_kv_read_e4m3(*t, cu, i(60)), fb.paged_kv_read_e4m3(*t, cu, 60)),
+            (fb.forward_varlen_window(q2, k, k, cu, cu, i(60), i(60), scale, i(20), i(1)),
+             fb.forward_varlen_window(q2, k, k, cu, cu, 60, 60, 0.125, 20, 1)),
+            (fb.forward_window(q2[None], k[None], k[None], scale, i(20), i(1)),
+             fb.forward_window(q2[None], k[None], k[None], 0.125, 20, 1))):
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    assert fb.fa_get_device_status() == 0

@@ -578,7 +578,8 @@ def _e4m3_workspace(fn, workspace, q, S, max_q, H, Hkv, d, max_blocks, causal, w
     """Address and bytes of the caller's workspace, of a new one where the call uses it, or of none;
     and the tensor, to be kept until the call is queued."""
     if workspace is None:
-        need = _e4m3_workspace_used(S, max_q, H, Hkv, d, max_blocks, causal, window, sinks)
+        need = _e4m3_workspace_used(S, int(max_q), H, Hkv, d, max_blocks, causal, int(window),
+                                    int(sinks))
         if not need:
             return None, 0, None
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
