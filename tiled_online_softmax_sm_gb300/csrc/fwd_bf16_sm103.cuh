@@ -1506,7 +1506,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const size_t slot =
             ((((size_t)U.b * Hg + U.h) * num_pairs + U.q_start0 / (2 * kBlockM >> gl)) * parts + U.index % parts) *
                 (2 * kBlockM) + i * kBlockM + r;
-        if (row_valid) {
+        if (row_valid && FA_IN_BOUNDS(slot, (size_t)BH * num_pairs * parts * (2 * kBlockM), status)) {
           *reinterpret_cast<float4*>(part_s + slot * 4) = make_float4(m_ref, l_run, l_p, 0.f);
           if (nkv > 0) {
             uint4* dst = reinterpret_cast<uint4*>(part_o + slot * D);

@@ -110,6 +110,7 @@ struct Args {
   int* pre;
   float* part_s;
   float* part_o;
+  size_t part_rows;
 };
 
 // 16-byte unit u of row t in a tile whose rows are D bytes, as the tensor
@@ -864,7 +865,8 @@ rows_stream_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
   sum_pages(a, s_pre, s_sum, blockIdx.x == 0);
   const int total = s_pre[a.num_seqs];
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= a.num_seqs; i += kWarps * 32) a.pre[i] = s_pre[i];
+    for (int i = threadIdx.x; i <= a.num_seqs; i += kWarps * 32)
+      if (FA_IN_BOUNDS(i, kMaxSeqs + 1, a.status)) a.pre[i] = s_pre[i];
   const int W = sharers(gridDim.x * kWarps, total);
   const int wid = blockIdx.x * kWarps + warp;
   if (wid >= W) return;
@@ -936,7 +938,7 @@ rows_stream_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int row = 8 * t + 2 * c + e;
-        if (row >= Q.n * G) continue;
+        if (row >= Q.n * G || !FA_IN_BOUNDS(slot + row, a.part_rows, a.status)) continue;
         if (r == 0)
           *reinterpret_cast<float4*>(a.part_s + (slot + row) * 4) =
               make_float4(S.m[t][e], S.r[t][e], S.l[t][e], 0.f);
@@ -1123,7 +1125,7 @@ cudaError_t launch(const PagedE4m3Params& p, cudaStream_t stream, const char** w
          static_cast<__nv_bfloat16*>(p.o), p.lse, p.cu_q ? 1 : p.H, p.cu_q ? p.total_q : 1,
          p.num_seqs, p.total_q, p.max_q, p.H, p.Hkv, p.num_pages, p.max_blocks, 1, 0,
          p.scale * kLog2e, p.causal, p.window, p.sinks, skip_first_copy_for_tests(), p.status,
-         nullptr, nullptr, nullptr};
+         nullptr, nullptr, nullptr, 0};
   constexpr int W = kStreamWarps<D, NT>;
   constexpr int kRows = GS::kRows;
   cudaError_t e;
@@ -1146,6 +1148,7 @@ cudaError_t launch(const PagedE4m3Params& p, cudaStream_t stream, const char** w
   while (C < 8 && 4 * units * 2 * C <= (alike ? 4 : 7) * room && pages >= 4ll * C * kWarps) C *= 2;
   if (p.workspace != nullptr && takes_shares<D, NT>(p.num_seqs, p.Hkv, p.max_blocks, pages)) {
     const size_t slots = (size_t)(W + units) * kRows;
+    a.part_rows = slots;
     a.part_s = static_cast<float*>(p.workspace);
     a.part_o = a.part_s + slots * 4;
     a.pre = reinterpret_cast<int*>(a.part_o + slots * D);
