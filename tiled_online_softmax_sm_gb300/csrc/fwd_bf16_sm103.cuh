@@ -800,7 +800,13 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             return true;
           } else {
             const int slot = li % C::kStages;
-            if (!warp_wait(bar_kve + 8 * slot, ((li / C::kStages) & 1) ^ 1)) return false;
+            int id = 0;   // paged: this lane's page, read while the slot is waited for
+            if constexpr (PAGED) {
+              if (lane * 16 < min(kBlockN, U.kv_len - j * kBlockN))
+                id = __ldg(block_table + (size_t)U.b * max_blocks + j * (kBlockN / 16) + lane);
+            }
+            const bool freed =
+                ptx::mbar_wait(bar_kve + 8 * slot, ((li / C::kStages) & 1) ^ 1, status, abort_flag);
             uint8_t* tile = sKV + slot * C::kSlotBytes;
             const uint32_t dst = ptx::smem_u32(tile);
             const CUtensorMap* map = which == 0 ? &tmK : &tmV;
@@ -820,13 +826,12 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             if constexpr (PAGED) {
               const int npages = (rows_valid + 15) / 16;
               // lane 0 posts the byte count (the barrier's one arrival, so the
-              // phase cannot complete before it), then lane pg looks up page
-              // pg and issues its boxes: the page copies go out in parallel
-              if (lane == 0 && !skip) ptx::mbar_arrive_expect_tx(bar, npages * 16 * C::kRowBytes);
-              __syncwarp();
+              // phase cannot complete before it), then lane pg issues the boxes
+              // of page pg: the page copies go out in parallel
+              if (lane == 0 && freed && !skip) ptx::mbar_arrive_expect_tx(bar, npages * 16 * C::kRowBytes);
+              if (__any_sync(0xffffffffu, !freed)) return false;   // (as above)
               if (lane < npages && !skip) {
                 const int pg = lane;
-                int id = __ldg(block_table + (size_t)U.b * max_blocks + j * (kBlockN / 16) + pg);
                 if (id < 0 || id >= num_pages) {
                   atomicExch(status, kDevBadBlockTable);
                   id = 0;
@@ -837,7 +842,7 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                   ptx::tma_load_2d(dst + c * 16384 + pg * 2048, map, C::kChunkElems * c, row, bar);
               }
             } else {
-              if (lane == 0 && !skip) {
+              if (lane == 0 && freed && !skip) {
                 ptx::mbar_arrive_expect_tx(bar, C::kTileBytes);
 #pragma unroll
                 for (int c = 0; c < C::kChunks; ++c) {
@@ -848,6 +853,13 @@ fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     ptx::tma_load_4d_hint(dst + c * 16384, map, C::kChunkElems * c, U.hk,
                                           j * kBlockN, U.b, bar, pol_kv);
                 }
+              }
+              // (voted on behind the copy, which lane 0 has issued if its own wait
+              // succeeded: the drain then waits for it)
+              if (__any_sync(0xffffffffu, !freed)) {
+                if (fix) fix_pending = freed;
+                else li += freed ? 1 : 0;
+                return false;
               }
             }
             if (fix) {
