@@ -231,9 +231,9 @@ constexpr int kRowsE4m3Max = 32;
 // a kv head, and of up to 32 except at d = 128 where the forward packs all heads
 // of a group into one tile (a power of two of them; otherwise it reads K and V
 // once more for each part of the group).  us of the rows kernels and of the
-// forward, d = 128, 8 kv heads of 4, [512, 8192] tokens: 64 x 4 new tokens 158,
-// 252; 64 x 8 322, 252; 16 x 8 104, 83; 1 x 8192 with 8 27, 25; 64 x 8 with
-// groups of 3 320, 870; d = 64, 64 x 8 158, 230.
+// forward, d = 128, 8 kv heads of 4, [512, 8192] tokens: 64 x 4 new tokens 147,
+// 229; 64 x 8 253, 229; 16 x 8 89, 88; 1 x 8192 with 8 26, 27; 64 x 8 with
+// groups of 3 253, 643; d = 64, 64 x 8 131, 209.
 inline bool rows_e4m3_form(int max_q, int H, int Hkv, int d) {
   const int g = H / Hkv;
   const long long rows = (long long)max_q * g;

@@ -101,7 +101,8 @@ constexpr float kRaiseSum = 256.0f;   // 2^kRescaleThreshold
 // one: raises are rare on data with a few long keys, and with them the passes
 // over a tile for its max.  4 x 2048-token chunks over the e4m3 cache, window
 // 4096, key norms spread by 2^(0.3 N(0, 1)): 535-607 us from one draw of the data
-// to the next with 8, 510-512 with 24.
+// to the next with 8, 510-512 with 24 (both without the second row sum, which
+// adds 30).
 constexpr float kRescaleThresholdWin = 24.0f;
 constexpr float kRaiseSumWin = 16777216.0f;
 

@@ -7,13 +7,14 @@
 // MMAs multiply the cached values themselves.  The heads of a group are rows of
 // one tile, so K and V are staged and widened once for all of them.  With few
 // units their tile lists are cut into parts for all SMs, merged by a second
-// launch: 64 tokens of one sequence over 8192 keys 152 -> 26 us.
+// launch: 64 tokens of one sequence over 8192 keys 139 -> 31 us.
 //
 // Bound by the two tiles' chain of MMAs and by issue slots.  16 x 512-token
-// chunks over [512, 8192] tokens (H = 32, Hkv = 8, d = 128): 493 us, 1133
-// TFLOP/s, 0.58 of the bf16 GEMM rate; a copy without softmax and widening takes
-// 376 us, DRAM would need 41.  Below 128 rows a unit has one tile and its time
-// does not depend on the rows (64 sequences, 254 us, 2.0 TB/s).
+// chunks over [512, 8192] tokens (H = 32, Hkv = 8, d = 128): 527 us, 1061
+// TFLOP/s, 0.54 of the bf16 GEMM rate (the bf16 cache's 447 us have no widening
+// warps beside the softmax); a copy without softmax and widening takes 376 us,
+// DRAM would need 41.  Below 128 rows a unit has one tile and its time does not
+// depend on the rows (64 sequences, 229 us, 2.3 TB/s).
 #include "fwd_bf16_sm103.cuh"
 
 namespace fa {

@@ -17,11 +17,12 @@
 //       as a programmatic dependent, merges each unit's partials in a fixed
 //       order.
 //
-// Bound by HBM once there is work for all warps: 64 sequences of [512, 8192]
-// tokens (d = 128, 8 kv heads of 4; 517 MB) take 83 us (6.2 TB/s, 0.91 of a plain
-// copy), and no less in a copy that skips all the arithmetic.  Below that
-// it is bound by the longest sequence's share: 16 sequences of 4 new tokens
-// take 47 us (134 MB, 0.42), of which the copies alone 35.
+// Up to 8 rows it is bound by HBM once there is work for all warps: 64 sequences
+// of [512, 8192] tokens (d = 128, 8 kv heads of 4; 517 MB) take 84 us (6.1 TB/s,
+// 0.90 of a plain copy), and no less in a copy that skips all the arithmetic.
+// With more rows the chain of each page bounds it (loads, MMAs, exponentials,
+// transpose, MMAs) at 12 warps an SM: 4 new tokens of the same sequences take 147
+// us (0.52), of 16 such sequences 47 (134 MB, 0.42; the copies alone 35).
 //
 // Mask.  The n query tokens of a sequence are the last n of its L keys; the
 // one at position p sees key j when j <= p and (window == 0, or j > p - window,
@@ -42,9 +43,9 @@
 // exponent would be off by 2^-4).  Both are raised lazily, when an exponent of p
 // or w passes 15: a vote per page instead of reductions.  m is raised to the
 // largest score, r to 7 below the largest weighted one, so w uses f16's upper
-// range: it is at most 2^15, exact to 11 bits down to 2^-21 of the largest weight times
-// 2^(v exponent), and zero below 2^-32 of it.
-// O = 2^r acc / l, in fp32, rounded once to bf16.
+// range: it is at most 2^15, exact to 11 bits down to 2^-21 of the largest weight
+// times 2^(v exponent), and zero below 2^-32 of it.  O = 2^r acc / l, in fp32,
+// rounded once to bf16.
 //
 // The lanes' shares of a row are chosen so that no shuffle or ldmatrix is
 // needed: lane (r = lane / 4, c = lane % 4) reads tokens r, r + 8 of K at dims
@@ -533,8 +534,8 @@ __device__ __forceinline__ bool run_pages(const Args& a, const Seq& Q, int G,
 // Longest sequences first, since CTAs start in block order: the sequence of rank
 // s when they are counted into classes of length (four an octave, by index within
 // one).  Every CTA counts for itself; skipped when all clusters fit at once.  64
-// x [512, 8192] tokens, 8 kv heads: 101 us in index order, 80 so; 256 x [100,
-// 1000]: 60 and 59, and 83 when every pair of sequences was compared.
+// x [512, 8192] tokens, 8 kv heads: 112 us in index order, 85 so; 256 x [100,
+// 1000]: 62 and 61 (and 84 when every pair of sequences was compared).
 constexpr int kClasses = 128;
 struct Order {
   uint32_t count[kMaxRanked / 32][kClasses / 4];   // bytes: of 32 sequences, then of those before them
@@ -1091,8 +1092,8 @@ long long unit_pages(int max_blocks, int max_q, int causal, int window, int sink
 }
 
 // The stream form, for few long units that clusters of 8 leave most of the
-// machine idle on: 1 x 131072 tokens 203 (C = 8) against 54 us, 1 x 8192 18
-// against 13.4, 4 x [512, 8192] 16.8 against 15.4; but 1 x 1000 7.5 against 8.5.
+// machine idle on: 1 x 131072 tokens 191 (C = 8) against 55 us, 1 x 8192 17.4
+// against 13.4, 4 x [512, 8192] 16.4 against 14.5; but 1 x 1000 7.5 against 8.5.
 template <int D, int NT>
 bool few_units(long long units) {
   return 2 * 8 * units <= Geo<D, NT, false>::kCtasPerSm * 152;
