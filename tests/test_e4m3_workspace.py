@@ -19,7 +19,7 @@ def _decode(lib, S, H, Hkv, d, blocks, ws, bytes_):
 def test_used_is_the_size_or_nothing(lib):
     size, used = fb.fa_paged_e4m3_workspace_size, fb.fa_paged_e4m3_workspace_used
     need = size(1, 1, 32, 8, 128)
-    assert used(1, 1, 32, 8, 128, 128) == used(4, 1, 32, 8, 128, 4096) * 0 + need > 0
+    assert used(1, 1, 32, 8, 128, 128) == need > 0
     assert used(1, 1, 32, 8, 128, 127) == 0              # 2032 keys: a cluster has them at once
     assert used(1, 1, 32, 8, 128, 4096, True, 1000) == 0 # nor under a short window,
     assert used(1, 1, 32, 8, 128, 4096, True, 1000, 1100) == need    # unless there are sinks
