@@ -169,7 +169,9 @@ fa_status fa_forward_varlen(const void* q, const void* k, const void* v, void* o
  * K/V tiles between the sinks and the window are never loaded, so the work is
  * linear in n for a fixed window.
  * A row whose visible scores hold a NaN gets O = LSE = NaN (never the LSE = -inf
- * of a row that sees no key).
+ * of a row that sees no key).  A NaN in K reaches only the rows that see its key;
+ * an inf or NaN in V may reach other rows of its batch element or sequence, as
+ * under fa_forward's causal mask (a hidden key's weight is 0, and 0 * inf is NaN).
  * Supported: d == dv in {64, 128}; pointers 16-byte aligned; dense: B*n, B*m
  * and H*n below 2^31; packed: H*total_q below 2^31; both: fewer than 2^30 work
  * units (a batch element or sequence, empty ones among them; 2^a query heads of
