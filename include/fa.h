@@ -505,6 +505,180 @@ fa_status fa_paged_prefill_e4m3(const void* q, const void* k_cache, const void* 
                                 size_t workspace_bytes, void* stream);
 
 /*
+ * Drafted token trees over a paged cache.
+ *
+ * A serving loop that drafts a tree of tokens for each sequence appends them to
+ * its cache as they are listed (a node behind its parent) and checks them in one
+ * pass: fa_tree_layout turns the parents into ancestor bits and rotary positions,
+ * fa_paged_qkv_write puts the nodes' K and V into the cache, each node attends to
+ * the context and its ancestors (fa_paged_tree_attention), and
+ * fa_paged_kv_accept moves the rows of the accepted path behind the context.
+ * fa_paged_copy_pages gives a forked sequence pages of its own.
+ * The pages of the passage have no counterpart for these calls; the attention is
+ * the recurrence of fa_paged_prefill under another mask.
+ *
+ * Conventions.  seq_lens, cu_seqlens and the block table are as for
+ * fa_paged_prefill: the n_s nodes of sequence s are rows [cu_seqlens[s],
+ * cu_seqlens[s+1]) of the packed tensors and the last n_s of its seq_lens[s]
+ * cached tokens; node t is token seq_lens[s] - n_s + t.  Packed rows that no
+ * sequence owns are left as they are.  A sequence whose offsets leave the packed
+ * rows, or with n_s > seq_lens[s], or seq_lens[s] beyond its table, is skipped
+ * and sets FA_ERR_INVALID_ARG in the device status word.
+ */
+
+/*
+ * fa_tree_layout — ancestor bits and positions of the nodes.
+ *   parents    int32 [total]: the node's parent, an earlier node of its sequence
+ *              (0 <= parent < t), or -1 for a child of the context.  Anything
+ *              else counts as -1 and sets FA_ERR_INVALID_ARG.
+ *   mask       int32 [total][mask_words] written: bit t % 32 of word t / 32 of
+ *              row i says that node i sees node t, itself or an ancestor
+ *   positions  int32 [total] written (may be NULL): seq_lens[s] - n_s + depth,
+ *              depth 0 for a child of the context
+ * A sequence of more than 32*mask_words nodes is skipped and sets
+ * FA_ERR_INVALID_ARG.
+ * Supported: 1 <= mask_words <= 32; total*mask_words below 2^31.
+ */
+fa_status fa_tree_layout(const int* parents, const int* seq_lens, const int* cu_seqlens, int* mask,
+                         int* positions, int num_seqs, int total, int mask_words, void* stream);
+
+/*
+ * fa_qk_norm_rope — q and k of each head normalised and rotated in one pass.
+ *   q, k       bf16 rows [total][H][d] and [total][Hkv][d]; q_stride and k_stride
+ *              are the elements from one token to the next (multiples of 8, at
+ *              least H*d and Hkv*d; the heads of a token are dense), so they may
+ *              be parts of one projection's output
+ *   q_weight, k_weight  bf16 [d], or NULL: that tensor is not normalised.  With
+ *              them y = x / sqrt(mean(x^2) + eps) * weight over the head's d
+ *              values.
+ *   rot_dim    the first rot_dim values of a head are rotated: pair p is values
+ *              (p, p + rot_dim/2), or (2p, 2p + 1) with interleaved = 1, and
+ *              (a, b) becomes (a c - b s, b c + a s) with (c, s) = cos_sin[x][p],
+ *              x the token's position on the pair's axis
+ *   cos_sin    fp32 [max_positions][rot_dim/2][2]; any scaling of the angles or
+ *              of the rotation is the table's (NULL with rot_dim 0)
+ *   positions  int32 [num_axes][total] (NULL with rot_dim 0)
+ *   sections   HOST int [num_axes]: rotary pairs of each axis, in order (time,
+ *              height, width for images and video); their sum is rot_dim/2.
+ *              NULL with one axis.
+ *   q_out, k_out  bf16 [total][H][d], [total][Hkv][d] written; q itself where
+ *              q_stride is H*d, and so for k (no other overlap)
+ * The arithmetic is fp32, rounded once to bf16.  A token with a position outside
+ * [0, max_positions) is skipped (its rows are not written) and sets
+ * FA_ERR_INVALID_ARG in the device status word.
+ * Supported: d in {64, 128}; rot_dim a multiple of 8 up to d; 1 <= num_axes <= 4;
+ * pointers 16-byte aligned; total*(H + 2*Hkv) below 2^31.
+ */
+fa_status fa_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                          const float* cos_sin, const int* positions, void* q_out, void* k_out,
+                          int total, int H, int Hkv, int d, long long q_stride, long long k_stride,
+                          int rot_dim, int interleaved, int num_axes, const int* sections,
+                          int max_positions, float eps, void* stream);
+
+/*
+ * fa_paged_qkv_write — fa_qk_norm_rope with K and V going into the bf16 paged
+ * cache of fa_paged_prefill.
+ *   v, v_stride   bf16 rows [total][Hkv][d], as k; copied as they are
+ *   k_cache, v_cache  bf16 [num_pages][Hkv][page_size][d]: row cu_seqlens[s] + i is
+ *                 written to the slot of token seq_lens[s] - n_s + i, other slots
+ *                 keep their contents.  Two rows of one call that name the same
+ *                 slot leave an unspecified mix there.
+ * The other arguments are as for fa_qk_norm_rope.  A token whose page id is out
+ * of range is skipped and sets FA_ERR_BAD_BLOCK_TABLE.
+ * Supported: as fa_qk_norm_rope; page_size == 16; num_pages*Hkv*16 below 2^31,
+ * max_blocks_per_seq below 2^26.
+ */
+fa_status fa_paged_qkv_write(const void* q, const void* k, const void* v, const void* q_weight,
+                             const void* k_weight, const float* cos_sin, const int* positions,
+                             void* q_out, void* k_cache, void* v_cache, const int* block_table,
+                             const int* seq_lens, const int* cu_seqlens, int num_seqs, int total,
+                             int H, int Hkv, int d, long long q_stride, long long k_stride,
+                             long long v_stride, int rot_dim, int interleaved, int num_axes,
+                             const int* sections, int max_positions, float eps, int page_size,
+                             int num_pages, int max_blocks_per_seq, void* stream);
+
+/*
+ * fa_paged_tree_workspace_size — bytes of workspace fa_paged_tree_attention needs
+ * (0 on invalid sizes): partials of the units whose keys are split.
+ */
+size_t fa_paged_tree_workspace_size(int num_seqs, int max_seqlen_q, int H, int Hkv, int d);
+
+/*
+ * fa_paged_tree_attention — attention of drafted nodes over the bf16 paged cache.
+ * Passage: as fa_paged_prefill.
+ *   q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, o, lse
+ *                 as fa_paged_prefill
+ *   mask          int32 [total_q][mask_words] as fa_tree_layout writes it, or any
+ *                 other bits: node i sees every token of the context (the first
+ *                 seq_lens[s] - n_s) and node t where bit t of its row is set.
+ *                 Bits from n_s on are ignored.  A row that sees no key gets O = 0
+ *                 and LSE = -inf.
+ *   max_seqlen_q  upper bound of the per-sequence node counts
+ *   workspace     device scratch of at least fa_paged_tree_workspace_size() bytes,
+ *                 256-byte aligned; it needs no initialisation, and calls on one
+ *                 workspace must not overlap on the GPU
+ * Cache contents of keys that no node of a sequence sees (past its end, or of
+ * nodes whose bit nobody has) are never used, NaN included; a NaN in a key that
+ * one node sees may reach others of its sequence.  A row whose visible scores
+ * hold a NaN gets O = LSE = NaN.
+ * A sequence of more than max_seqlen_q or 32*mask_words nodes is skipped and sets
+ * FA_ERR_INVALID_ARG.  Page ids outside [0, num_pages) set
+ * FA_ERR_BAD_BLOCK_TABLE; the sequence's output is then unspecified.
+ * Supported: d in {64, 128}, page_size == 16; scale positive and finite;
+ * 1 <= mask_words; num_seqs <= 4096; total_q*H and total_q*mask_words below 2^31;
+ * num_pages*Hkv*16 below 2^31; num_seqs * Hkv * ceil(max_seqlen_q * (H/Hkv) / 256)
+ * * ceil(max_blocks_per_seq / 8) below 2^31.
+ */
+fa_status fa_paged_tree_attention(const void* q, const void* k_cache, const void* v_cache,
+                                  const int* block_table, const int* seq_lens,
+                                  const int* cu_seqlens_q, const int* mask, void* o, float* lse,
+                                  int num_seqs, int total_q, int max_seqlen_q, int mask_words, int H,
+                                  int Hkv, int d, int page_size, int num_pages,
+                                  int max_blocks_per_seq, float scale, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
+ * fa_paged_kv_accept — the accepted path's rows moved behind the context.
+ *   k_cache, v_cache  [num_layers][num_pages][Hkv][page_size][d], bf16, or e4m3
+ *                 with scale bytes k_scale, v_scale [num_layers][num_pages][Hkv]
+ *                 [page_size] (both NULL for bf16); the layers share the table
+ *   path          int32 [num_seqs][max_path]: the accepted nodes of sequence s,
+ *                 in increasing order, path_lens[s] of them (0 <= path_lens[s] <=
+ *                 max_path); the entries behind them may be anything
+ *   new_seq_lens  int32 [num_seqs] written: seq_lens[s] - n_s + path_lens[s] (not
+ *                 seq_lens itself)
+ * The rows of node path[s][a] are copied to the slot of node a, for every a in
+ * turn; the slots behind keep their contents.  A sequence whose path is longer
+ * than max_path or n_s, leaves [0, n_s) or does not increase is skipped, its new
+ * length is seq_lens[s], and FA_ERR_INVALID_ARG is set.  A node with a page id
+ * out of range, its own or its destination's, is skipped and sets
+ * FA_ERR_BAD_BLOCK_TABLE.  The pages that hold a sequence's nodes must be its
+ * own: two sequences that move rows within one page leave an unspecified mix.
+ * Supported: d in {64, 128}, page_size == 16, max_path <= 1024; num_pages*Hkv*16
+ * below 2^31, max_blocks_per_seq below 2^26, num_seqs * num_layers below 2^31.
+ */
+fa_status fa_paged_kv_accept(void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                             const int* block_table, const int* seq_lens, const int* cu_seqlens,
+                             const int* path, const int* path_lens, int* new_seq_lens, int num_seqs,
+                             int total, int max_path, int num_layers, int Hkv, int d, int page_size,
+                             int num_pages, int max_blocks_per_seq, void* stream);
+
+/*
+ * fa_paged_copy_pages — whole pages copied within a cache, in every layer.
+ *   caches, scales, num_layers   as fa_paged_kv_accept
+ *   pairs         int32 [num_pairs][2]: source page, destination page.  A pair
+ *                 with an id out of range is skipped and sets
+ *                 FA_ERR_BAD_BLOCK_TABLE.  A source may appear in several pairs; a
+ *                 page that is the destination of two pairs, or of one and the
+ *                 source of another, is left with an unspecified mix (and the
+ *                 other's destination too).
+ * Supported: as fa_paged_kv_accept; num_pairs * num_layers * Hkv below 2^27.
+ */
+fa_status fa_paged_copy_pages(void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                              const int* pairs, int num_pairs, int num_layers, int Hkv, int d,
+                              int page_size, int num_pages, void* stream);
+
+/*
  * fa_split_combine — merge per-split partial triples with the recurrence's
  * rescale rule ("S12 FlashAttention", 练习 1): for each (s, h)
  *     M = max_x m_x,  w_x = exp(m_x - M)  (w_x = 0 when m_x = -inf),

@@ -9,7 +9,9 @@ library is missing or cannot be loaded, the first call raises.
 
 The helpers at the end (``forward``, ``forward_f32``, ``forward_varlen``,
 ``paged_decode``, ``paged_decode_fused``, the e4m3 cache's ``paged_..._e4m3``,
-``split_combine``) allocate outputs with torch and then call the same entry
+``split_combine``, and those of drafted trees: ``tree_layout``, ``qk_norm_rope``,
+``paged_qkv_write``, ``paged_tree_attention``, ``paged_kv_accept``,
+``paged_copy_pages``) allocate outputs with torch and then call the same entry
 points.  Only they and a call's default stream import torch: the entry points
 themselves, with plain addresses and a given stream, do without it.
 """
@@ -40,6 +42,8 @@ EXPORTED = ("fa_forward", "fa_forward_fp8", "fa_forward_f32", "fa_forward_varlen
             "fa_forward_window", "fa_forward_varlen_window",
             "fa_paged_kv_write_e4m3", "fa_paged_kv_read_e4m3", "fa_paged_e4m3_workspace_size",
             "fa_paged_e4m3_workspace_used", "fa_paged_decode_e4m3", "fa_paged_prefill_e4m3",
+            "fa_tree_layout", "fa_qk_norm_rope", "fa_paged_qkv_write", "fa_paged_tree_workspace_size",
+            "fa_paged_tree_attention", "fa_paged_kv_accept", "fa_paged_copy_pages",
             "fa_last_error",
             "fa_get_device_status")
 FA_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -91,6 +95,14 @@ def load(path: str = LIB_PATH):
         lib.fa_paged_e4m3_workspace_size.restype = Z
         lib.fa_paged_e4m3_workspace_used.argtypes = [I] * 9
         lib.fa_paged_e4m3_workspace_used.restype = Z
+        lib.fa_tree_layout.argtypes = [P] * 5 + [I, I, I, P]
+        lib.fa_qk_norm_rope.argtypes = [P] * 8 + [I, I, I, I, LL, LL, I, I, I, P, I, F, P]
+        lib.fa_paged_qkv_write.argtypes = [P] * 13 + [I] * 5 + [LL, LL, LL, I, I, I, P, I, F, I, I, I, P]
+        lib.fa_paged_tree_workspace_size.argtypes = [I] * 5
+        lib.fa_paged_tree_workspace_size.restype = Z
+        lib.fa_paged_tree_attention.argtypes = [P] * 9 + [I] * 10 + [F, P, Z, P]
+        lib.fa_paged_kv_accept.argtypes = [P] * 10 + [I] * 9 + [P]
+        lib.fa_paged_copy_pages.argtypes = [P] * 5 + [I] * 6 + [P]
         lib.fa_last_error.argtypes = []
         lib.fa_last_error.restype = ctypes.c_char_p
         lib.fa_get_device_status.argtypes = [P, ctypes.POINTER(I)]
@@ -100,7 +112,9 @@ def load(path: str = LIB_PATH):
                      "fa_paged_decode_noalloc", "fa_paged_gather", "fa_split_combine",
                      "fa_forward_window", "fa_forward_varlen_window",
                      "fa_paged_kv_write_e4m3", "fa_paged_kv_read_e4m3", "fa_paged_decode_e4m3",
-                     "fa_paged_prefill_e4m3", "fa_get_device_status"):
+                     "fa_paged_prefill_e4m3", "fa_tree_layout", "fa_qk_norm_rope", "fa_paged_qkv_write",
+                     "fa_paged_tree_attention", "fa_paged_kv_accept", "fa_paged_copy_pages",
+                     "fa_get_device_status"):
             getattr(lib, name).restype = I
         _lib = lib
         return lib
@@ -303,6 +317,80 @@ def fa_paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, se
                                         page_size, num_pages, max_blocks_per_seq, float(scale),
                                         int(causal), int(window), int(sinks), _p(workspace),
                                         int(workspace_bytes), _stream(stream)))
+
+
+def fa_tree_layout(parents, seq_lens, cu_seqlens, mask, positions, num_seqs, total, mask_words, stream=None):
+    _check(load().fa_tree_layout(_p(parents), _p(seq_lens), _p(cu_seqlens), _p(mask), _p(positions),
+                                 num_seqs, total, mask_words, _stream(stream)))
+
+
+@functools.lru_cache(maxsize=256)
+def _ints(values):
+    """The host array of a tuple of ints."""
+    return (ctypes.c_int * len(values))(*values)
+
+
+def fa_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, total, H, Hkv, d,
+                    q_stride, k_stride, rot_dim, interleaved, num_axes, sections, max_positions, eps,
+                    stream=None):
+    """sections: the axes' pairs (a sequence of ints), or None with one axis."""
+    _check(load().fa_qk_norm_rope(_p(q), _p(k), _p(q_weight), _p(k_weight), _p(cos_sin), _p(positions),
+                                  _p(q_out), _p(k_out), total, H, Hkv, d, q_stride, k_stride, rot_dim,
+                                  1 if interleaved else 0, num_axes, _sections(sections, num_axes),
+                                  max_positions, eps, _stream(stream)))
+
+
+def fa_paged_qkv_write(q, k, v, q_weight, k_weight, cos_sin, positions, q_out, k_cache, v_cache,
+                       block_table, seq_lens, cu_seqlens, num_seqs, total, H, Hkv, d, q_stride, k_stride,
+                       v_stride, rot_dim, interleaved, num_axes, sections, max_positions, eps, page_size,
+                       num_pages, max_blocks_per_seq, stream=None):
+    _check(load().fa_paged_qkv_write(_p(q), _p(k), _p(v), _p(q_weight), _p(k_weight), _p(cos_sin),
+                                     _p(positions), _p(q_out), _p(k_cache), _p(v_cache),
+                                     _p(block_table), _p(seq_lens), _p(cu_seqlens), num_seqs, total, H,
+                                     Hkv, d, q_stride, k_stride, v_stride, rot_dim,
+                                     1 if interleaved else 0, num_axes, _sections(sections, num_axes),
+                                     max_positions, eps, page_size, num_pages, max_blocks_per_seq,
+                                     _stream(stream)))
+
+
+def _sections(sections, num_axes):
+    """The host array of the axes' sections, of the length that the entry reads."""
+    if sections is None:
+        return None
+    sections = tuple(sections)
+    if len(sections) != num_axes:
+        raise FaError(FA_ERR_INVALID_ARG, f"{len(sections)} sections for {num_axes} axes")
+    return _ints(sections)
+
+
+def fa_paged_tree_workspace_size(num_seqs, max_seqlen_q, H, Hkv, d) -> int:
+    return int(load().fa_paged_tree_workspace_size(num_seqs, max_seqlen_q, H, Hkv, d))
+
+
+def fa_paged_tree_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, mask, o, lse,
+                            num_seqs, total_q, max_seqlen_q, mask_words, H, Hkv, d, page_size, num_pages,
+                            max_blocks_per_seq, scale, workspace, workspace_bytes, stream=None):
+    _check(load().fa_paged_tree_attention(_p(q), _p(k_cache), _p(v_cache), _p(block_table), _p(seq_lens),
+                                          _p(cu_seqlens_q), _p(mask), _p(o), _p(lse), num_seqs, total_q,
+                                          max_seqlen_q, mask_words, H, Hkv, d, page_size, num_pages,
+                                          max_blocks_per_seq, scale, _p(workspace), workspace_bytes,
+                                          _stream(stream)))
+
+
+def fa_paged_kv_accept(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, path,
+                       path_lens, new_seq_lens, num_seqs, total, max_path, num_layers, Hkv, d, page_size,
+                       num_pages, max_blocks_per_seq, stream=None):
+    _check(load().fa_paged_kv_accept(_p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale), _p(block_table),
+                                     _p(seq_lens), _p(cu_seqlens), _p(path), _p(path_lens),
+                                     _p(new_seq_lens), num_seqs, total, max_path, num_layers, Hkv, d,
+                                     page_size, num_pages, max_blocks_per_seq, _stream(stream)))
+
+
+def fa_paged_copy_pages(k_cache, v_cache, k_scale, v_scale, pairs, num_pairs, num_layers, Hkv, d,
+                        page_size, num_pages, stream=None):
+    _check(load().fa_paged_copy_pages(_p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale), _p(pairs),
+                                      num_pairs, num_layers, Hkv, d, page_size, num_pages,
+                                      _stream(stream)))
 
 
 def fa_split_combine(part_m, part_l, part_o, o, lse, num_seqs, H, num_splits, dv, stream=None):
@@ -647,6 +735,234 @@ def paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_l
         o.data_ptr(), lse.data_ptr(), S, Tq, max_seqlen_q, H, Hkv, d, page, P, max_blocks, scale,
         1 if causal else 0, window, sinks, ws, ws_bytes, _current_raw_stream(device)))
     return o, lse
+
+
+# ------------------------------------------------------ drafted token trees
+def tree_layout(parents, seq_lens, cu_seqlens, mask_words, stream=None):
+    """parents [T] int32 (-1: child of the context) -> (mask [T,mask_words] int32 of ancestor bits,
+    positions [T] int32)."""
+    if stream is not None:
+        with _given(stream):
+            return tree_layout(parents, seq_lens, cu_seqlens, mask_words)
+    device = parents.get_device()
+    T, S = parents.shape[0], seq_lens.shape[0]
+    _check_tensors("tree_layout", device, ("parents", parents, torch.int32, (T,)),
+                   ("seq_lens", seq_lens, torch.int32, (S,)),
+                   ("cu_seqlens", cu_seqlens, torch.int32, (S + 1,)))
+    mask = torch.empty((T, mask_words), dtype=torch.int32, device=parents.device)
+    positions = torch.empty_like(parents)
+    lib = _lib or load()
+    _check(lib.fa_tree_layout(parents.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(),
+                              mask.data_ptr(), positions.data_ptr(), S, T, mask_words,
+                              _raw_stream(device)))
+    return mask, positions
+
+
+def _raw_stream(device):
+    if _CODES is None:
+        _bind_torch()
+    return _current_raw_stream(device)
+
+
+def _heads_stride(fn, name, t, shape, device):
+    """Token stride of bf16 rows [T,heads,d] whose heads are dense."""
+    st = t.stride()
+    if t.shape != shape or st[2] != 1 or (shape[1] > 1 and st[1] != shape[2]) or \
+            t.dtype is not torch.bfloat16 or t.get_device() != device:
+        raise FaError(FA_ERR_INVALID_ARG, f"{fn}: {name} is {t.dtype} on {t.device} of shape "
+                                          f"{tuple(t.shape)} and strides {st}, wanted bf16 "
+                                          f"{tuple(shape)} with dense heads")
+    return st[0] if shape[0] > 1 else shape[1] * shape[2]
+
+
+def _rotary(fn, device, T, d, q_weight, k_weight, cos_sin, positions, sections):
+    """(rot_dim, axes, rows of the table, host sections) of a rotation, its tensors checked."""
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _check_rows(fn, device, name, w, torch.bfloat16, (d,))
+    if cos_sin is None:
+        return 0, 1, 0, None
+    if cos_sin.dim() != 3 or positions is None or positions.dim() != 2:
+        raise FaError(FA_ERR_INVALID_ARG, f"{fn}: a rotation takes cos_sin [positions,rot_dim/2,2] and "
+                                          "positions [axes,T]")
+    rows, half = cos_sin.shape[:2]
+    axes = positions.shape[0]
+    _check_rows(fn, device, "cos_sin", cos_sin, torch.float32, (rows, half, 2))
+    _check_rows(fn, device, "positions", positions, torch.int32, (axes, T))
+    return 2 * half, axes, rows, _sections(sections, axes)
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, sections=None,
+                 interleaved=False, stream=None):
+    """q [T,H,d], k [T,Hkv,d] bf16 (parts of one projection allowed), weights [d] bf16 or None, cos_sin
+    [positions,rot_dim/2,2] fp32 or None, positions [axes,T] int32 -> (q [T,H,d], k [T,Hkv,d])."""
+    if stream is not None:
+        with _given(stream):
+            return qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, sections, interleaved)
+    fn = "qk_norm_rope"
+    device = q.get_device()
+    T, H, d = q.shape
+    Hkv = k.shape[1]
+    if device != torch.cuda.current_device():
+        _refuse(fn, device)
+    qs, ks = (_heads_stride(fn, "q", q, (T, H, d), device), _heads_stride(fn, "k", k, (T, Hkv, d), device))
+    rot, axes, rows, host = _rotary(fn, device, T, d, q_weight, k_weight, cos_sin, positions, sections)
+    q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+    k_out = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=q.device)
+    lib = _lib or load()
+    _check(lib.fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), _p(q_weight), _p(k_weight), _p(cos_sin),
+                               _p(positions), q_out.data_ptr(), k_out.data_ptr(), T, H, Hkv, d, qs, ks,
+                               rot, 1 if interleaved else 0, axes, host, rows, eps, _raw_stream(device)))
+    return q_out, k_out
+
+
+def _check_paged(fn, device, kc, vc, bt, sl, cu):
+    """The bf16 paged cache's tensors.  (Written out: it runs on every call of the serving path.)"""
+    shape, table = kc.shape, bt.shape
+    if len(shape) != 4 or len(table) != 2:
+        raise FaError(FA_ERR_INVALID_ARG, f"{fn}: k_cache has shape {tuple(shape)}, block_table "
+                                          f"{tuple(table)}, wanted 4 and 2 dimensions")
+    kind, i32, S = torch.bfloat16, torch.int32, table[0]
+    if not (kc.dtype is kind and vc.dtype is kind and bt.dtype is i32 and sl.dtype is i32
+            and cu.dtype is i32 and vc.shape == shape and sl.shape == (S,) and cu.shape == (S + 1,)
+            and kc.get_device() == device and vc.get_device() == device and bt.get_device() == device
+            and sl.get_device() == device and cu.get_device() == device and kc.is_contiguous()
+            and vc.is_contiguous() and bt.is_contiguous() and sl.is_contiguous()
+            and cu.is_contiguous() and device >= 0 and device == torch.cuda.current_device()):
+        _refuse(fn, device, ("k_cache", kc, (kind,), shape), ("v_cache", vc, (kind,), shape),
+                ("block_table", bt, (i32,), table), ("seq_lens", sl, (i32,), (S,)),
+                ("cu_seqlens", cu, (i32,), (S + 1,)))
+
+
+def paged_qkv_write(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_cache, block_table,
+                    seq_lens, cu_seqlens, eps=1e-6, sections=None, interleaved=False, stream=None):
+    """As qk_norm_rope, with K and V going into the bf16 paged cache [P,Hkv,16,d] -> q [T,H,d]."""
+    if stream is not None:
+        with _given(stream):
+            return paged_qkv_write(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_cache,
+                                   block_table, seq_lens, cu_seqlens, eps, sections, interleaved)
+    fn = "paged_qkv_write"
+    device = q.get_device()
+    _check_paged(fn, device, k_cache, v_cache, block_table, seq_lens, cu_seqlens)
+    P, Hkv, page, d = k_cache.shape
+    S, max_blocks = block_table.shape
+    T, H = q.shape[:2]
+    qs, ks, vs = (_heads_stride(fn, "q", q, (T, H, d), device),
+                  _heads_stride(fn, "k", k, (T, Hkv, d), device),
+                  _heads_stride(fn, "v", v, (T, Hkv, d), device))
+    rot, axes, rows, host = _rotary(fn, device, T, d, q_weight, k_weight, cos_sin, positions, sections)
+    q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+    lib = _lib or load()
+    _check(lib.fa_paged_qkv_write(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _p(q_weight), _p(k_weight), _p(cos_sin), _p(positions),
+        q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+        seq_lens.data_ptr(), cu_seqlens.data_ptr(), S, T, H, Hkv, d, qs, ks, vs, rot,
+        1 if interleaved else 0, axes, host, rows, eps, page, P, max_blocks, _raw_stream(device)))
+    return q_out
+
+
+@functools.lru_cache(maxsize=4096)
+def _tree_workspace(*sizes):
+    """fa_paged_tree_workspace_size, which depends on the sizes alone."""
+    return fa_paged_tree_workspace_size(*sizes)
+
+
+def paged_tree_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, max_seqlen_q, mask,
+                         scale, workspace=None, stream=None):
+    """Drafted nodes q [T,H,d] packed by cu_seqlens_q over the bf16 cache, mask [T,words] int32 of the
+    nodes that each node sees beside the context -> (o [T,H,d] bf16, lse [H,T] fp32)."""
+    if stream is not None:
+        with _given(stream):
+            return paged_tree_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q,
+                                        max_seqlen_q, mask, scale, workspace)
+    fn = "paged_tree_attention"
+    device = q.get_device()
+    _check_paged(fn, device, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q)
+    P, Hkv, page, d = k_cache.shape
+    S, max_blocks = block_table.shape
+    T, H = q.shape[:2]
+    words = mask.shape[-1]
+    _check_rows(fn, device, "q", q, torch.bfloat16, (T, H, d))
+    _check_rows(fn, device, "mask", mask, torch.int32, (T, words))
+    if workspace is None:   # (a caller's own is sized for the caller's bound)
+        max_seqlen_q = min(max_seqlen_q, T)
+        workspace = torch.empty(_tree_workspace(S, max_seqlen_q, H, Hkv, d), dtype=torch.uint8,
+                                device=q.device)
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise FaError(FA_ERR_WORKSPACE, f"{fn}: the workspace is on {workspace.device} with strides "
+                                        f"{workspace.stride()}")
+    o = torch.empty_like(q)
+    lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+    lib = _lib or load()
+    _check(lib.fa_paged_tree_attention(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        cu_seqlens_q.data_ptr(), mask.data_ptr(), o.data_ptr(), lse.data_ptr(), S, T, max_seqlen_q, words,
+        H, Hkv, d, page, P, max_blocks, scale, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_stream(device)))
+    return o, lse
+
+
+def _check_layers(fn, device, kc, vc, ks, vs):
+    """Caches [P,Hkv,16,d], or [layers,P,Hkv,16,d], bf16 or (with scales) e4m3; their layers."""
+    if _CODES is None:
+        _bind_torch()
+    shape = kc.shape
+    if len(shape) not in (4, 5) or (ks is None) != (vs is None):
+        raise FaError(FA_ERR_INVALID_ARG, f"{fn}: k_cache has shape {tuple(shape)}, wanted 4 dimensions, or "
+                                          "5 with layers first, and both scales or none")
+    kinds = (torch.bfloat16,) if ks is None else _CODES
+    named = [("k_cache", kc, kinds, shape), ("v_cache", vc, kinds, shape)]
+    if ks is not None:
+        named += [("k_scale", ks, _SCALES, shape[:-1]), ("v_scale", vs, _SCALES, shape[:-1])]
+    for _, t, kind, want in named:
+        if t.dtype not in kind or t.shape != want or t.get_device() != device or not t.is_contiguous():
+            _refuse(fn, device, *named)
+    if device != _current_device():
+        _refuse(fn, device)
+    return shape[0] if len(shape) == 5 else 1
+
+
+def paged_kv_accept(k_cache, v_cache, block_table, seq_lens, cu_seqlens, path, path_lens, k_scale=None,
+                    v_scale=None, stream=None):
+    """The rows of the accepted nodes path [S,max_path] int32 (path_lens [S] of them) moved behind the
+    context, in caches [P,Hkv,16,d] or [layers,P,Hkv,16,d] -> the new lengths [S] int32."""
+    if stream is not None:
+        with _given(stream):
+            return paged_kv_accept(k_cache, v_cache, block_table, seq_lens, cu_seqlens, path, path_lens,
+                                   k_scale, v_scale)
+    fn = "paged_kv_accept"
+    device = k_cache.get_device()
+    layers = _check_layers(fn, device, k_cache, v_cache, k_scale, v_scale)
+    P, Hkv, page, d = k_cache.shape[-4:]
+    S, max_blocks = block_table.shape
+    max_path = path.shape[-1]
+    for name, t, shape in (("block_table", block_table, (S, max_blocks)), ("seq_lens", seq_lens, (S,)),
+                           ("cu_seqlens", cu_seqlens, (S + 1,)), ("path", path, (S, max_path)),
+                           ("path_lens", path_lens, (S,))):
+        _check_rows(fn, device, name, t, torch.int32, shape)
+    new_lens = torch.empty_like(seq_lens)
+    lib = _lib or load()
+    _check(lib.fa_paged_kv_accept(
+        k_cache.data_ptr(), v_cache.data_ptr(), _p(k_scale), _p(v_scale), block_table.data_ptr(),
+        seq_lens.data_ptr(), cu_seqlens.data_ptr(), path.data_ptr(), path_lens.data_ptr(),
+        new_lens.data_ptr(), S, 0x7fffffff, max_path, layers, Hkv, d, page, P, max_blocks,
+        _raw_stream(device)))
+    return new_lens
+
+
+def paged_copy_pages(k_cache, v_cache, pairs, k_scale=None, v_scale=None, stream=None):
+    """Pages pairs[:, 0] copied to pages pairs[:, 1] ([N,2] int32) of caches [P,Hkv,16,d] or
+    [layers,P,Hkv,16,d], and of their scales."""
+    fn = "paged_copy_pages"
+    device = k_cache.get_device()
+    layers = _check_layers(fn, device, k_cache, v_cache, k_scale, v_scale)
+    P, Hkv, page, d = k_cache.shape[-4:]
+    N = pairs.shape[0]
+    _check_rows(fn, device, "pairs", pairs, torch.int32, (N, 2))
+    lib = _lib or load()
+    _check(lib.fa_paged_copy_pages(k_cache.data_ptr(), v_cache.data_ptr(), _p(k_scale), _p(v_scale),
+                                   pairs.data_ptr(), N, layers, Hkv, d, page, P,
+                                   _raw_stream(device) if stream is None else _stream(stream)))
 
 
 def split_combine(part_m, part_l, part_o, stream=None):

@@ -260,4 +260,87 @@ cudaError_t launch_split_combine(const CombineParams& p, cudaStream_t stream,
                                  bool behind_partials = false);
 cudaError_t launch_decode_gather(const GatherParams& p, cudaStream_t stream);
 
+// q, k and v rows of new tokens: norms, rotation, and K, V into the bf16 paged
+// cache (k_cache != nullptr) or k to k_out.
+constexpr int kMaxAxes = 4;
+struct QkvRowsParams {
+  const void* q;             // bf16 [total][H][d], [total][Hkv][d] by token strides
+  const void* k;
+  const void* v;
+  long long q_stride, k_stride, v_stride;
+  const void* q_weight;      // bf16 [d] or null
+  const void* k_weight;
+  const float* cos_sin;      // [max_positions][rot_dim / 2][2]
+  const int* positions;      // [num_axes][total]
+  void* q_out;
+  void* k_out;               // dense form
+  void* k_cache;             // paged form
+  void* v_cache;
+  const int* block_table;
+  const int* seq_lens;
+  const int* cu;
+  int num_seqs, total, H, Hkv, d, rot_dim, interleaved, num_axes;
+  int section_end[kMaxAxes]; // pair p belongs to the first axis with p < section_end
+  int max_positions, num_pages, max_blocks;
+  float eps;
+  int* status;
+};
+cudaError_t launch_qkv_rows(const QkvRowsParams& p, cudaStream_t stream);
+
+struct TreeLayoutParams {
+  const int* parents;
+  const int* seq_lens;
+  const int* cu;
+  int* mask;
+  int* positions;            // may be null
+  int num_seqs, total, words;
+  int* status;
+};
+cudaError_t launch_tree_layout(const TreeLayoutParams& p, cudaStream_t stream);
+
+// Caches of all layers, [layers][pages][Hkv][16] rows of row_bytes (and a scale
+// byte a row where k_scale is not null).
+struct KvMoveParams {
+  void* k_cache;
+  void* v_cache;
+  void* k_scale;
+  void* v_scale;
+  int num_layers, Hkv, row_bytes, num_pages;
+  int* status;
+};
+struct KvAcceptParams {
+  KvMoveParams c;
+  const int* block_table;
+  const int* seq_lens;
+  const int* cu;
+  const int* path;
+  const int* path_lens;
+  int* new_seq_lens;
+  int num_seqs, total, max_path, max_blocks;
+};
+constexpr int kMaxPath = 1024;
+cudaError_t launch_kv_accept(const KvAcceptParams& p, cudaStream_t stream);
+cudaError_t launch_copy_pages(const KvMoveParams& c, const int* pairs, int num_pairs,
+                              cudaStream_t stream);
+
+// Attention of drafted nodes over the bf16 paged cache.
+constexpr int kMaxTreeSeqs = 4096;
+struct TreeAttnParams {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int* block_table;
+  const int* seq_lens;
+  const int* cu_q;
+  const int* mask;
+  void* o;
+  float* lse;                // [H][total_q], may be null
+  int num_seqs, total_q, max_q, words, H, Hkv, d, num_pages, max_blocks;
+  float scale;
+  void* workspace;
+  int* status;
+};
+size_t tree_attn_workspace(int max_q, int H, int Hkv, int d);
+cudaError_t launch_tree_attn(const TreeAttnParams& p, cudaStream_t stream, const char** why);
+
 }  // namespace fa
