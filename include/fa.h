@@ -624,10 +624,11 @@ size_t fa_paged_tree_workspace_size(int num_seqs, int max_seqlen_q, int H, int H
  * A sequence of more than max_seqlen_q or 32*mask_words nodes is skipped and sets
  * FA_ERR_INVALID_ARG.  Page ids outside [0, num_pages) set
  * FA_ERR_BAD_BLOCK_TABLE; the sequence's output is then unspecified.
- * Supported: d in {64, 128}, page_size == 16; scale positive and finite;
- * 1 <= mask_words; num_seqs <= 4096; total_q*H and total_q*mask_words below 2^31;
- * num_pages*Hkv*16 below 2^31; num_seqs * Hkv * ceil(max_seqlen_q * (H/Hkv) / 256)
- * * ceil(max_blocks_per_seq / 8) below 2^31.
+ * Supported: d in {64, 128}, page_size == 16, H / Hkv <= 128; scale positive and
+ * finite; 1 <= mask_words; num_seqs <= 4096; total_q*H and total_q*mask_words below
+ * 2^31; num_pages*Hkv*16 below 2^31; units * (3*ceil(max_blocks_per_seq / 8) + 4)
+ * below 2^31, where units = num_seqs * Hkv * ceil(max_seqlen_q / (2*floor(128 /
+ * (H / Hkv)))).
  */
 fa_status fa_paged_tree_attention(const void* q, const void* k_cache, const void* v_cache,
                                   const int* block_table, const int* seq_lens,

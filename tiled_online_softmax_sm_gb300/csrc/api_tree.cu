@@ -220,7 +220,8 @@ fa_status fa_paged_qkv_write(const void* q, const void* k, const void* v, const 
 }
 
 size_t fa_paged_tree_workspace_size(int num_seqs, int max_seqlen_q, int H, int Hkv, int d) {
-  if (num_seqs <= 0 || max_seqlen_q <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || (d != 64 && d != 128))
+  if (num_seqs <= 0 || max_seqlen_q <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || H / Hkv > 128 ||
+      (d != 64 && d != 128))
     return 0;
   return fa::tree_attn_workspace(max_seqlen_q, H, Hkv, d);
 }
@@ -242,6 +243,7 @@ fa_status fa_paged_tree_attention(const void* q, const void* k_cache, const void
     return fail(FA_ERR_INVALID_ARG, "%s: scale must be positive and finite", fn);
   fa_status st = check_dims(fn, d, page_size);
   if (st != FA_OK) return st;
+  if (H / Hkv > 128) return fail(FA_ERR_UNSUPPORTED, "%s: H/Hkv=%d > 128", fn, H / Hkv);
   if (num_seqs > fa::kMaxTreeSeqs)
     return fail(FA_ERR_UNSUPPORTED, "%s: num_seqs=%d > %d", fn, num_seqs, fa::kMaxTreeSeqs);
   if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return FA_OK;
@@ -255,12 +257,12 @@ fa_status fa_paged_tree_attention(const void* q, const void* k_cache, const void
     return fail(FA_ERR_WORKSPACE, "%s: workspace %p of %zu bytes (need %zu, 256-byte aligned)", fn, workspace,
                 workspace_bytes, need);
   if (max_seqlen_q > total_q) max_seqlen_q = total_q;   // no sequence has more
-  // rows, mask words and the list of K/V tiles are numbered in 32 bits
-  const long long row_units = ((long long)max_seqlen_q * (H / Hkv) + 255) / 256;
-  const long long tiles = ((long long)max_blocks_per_seq + 7) / 8;
+  // rows, mask words and positions in the list of K/V tiles (at most 3 a tile and 4 a
+  // unit of two query tiles) are numbered in 32 bits
+  const long long nodes = 2 * (128 / (H / Hkv));
+  const double units = (double)num_seqs * Hkv * (double)((max_seqlen_q + nodes - 1) / nodes);
   if ((long long)total_q * H > kInt || (long long)total_q * mask_words > kInt ||
-      (long long)max_seqlen_q * (H / Hkv) > kInt - 256 ||
-      (double)num_seqs * Hkv * (double)row_units * (double)tiles > (double)kInt)
+      units * (3.0 * ((max_blocks_per_seq + 7) / 8) + 4.0) > (double)kInt)
     return fail(FA_ERR_UNSUPPORTED, "%s: total_q*H, total_q*mask_words or the K/V tiles of all units exceed 2^31", fn);
   fa::TreeAttnParams p{q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, mask, o, lse, num_seqs, total_q,
                        max_seqlen_q, mask_words, H, Hkv, d, num_pages, max_blocks_per_seq, scale, workspace,

@@ -3,20 +3,23 @@
 // tokens) and the nodes whose bit is set in its row of the mask.
 //
 // The query rows of a kv head, n nodes times G = H / Hkv heads, are packed into
-// 128-row tiles (row r = node r / G, head r % G).  A unit is one or two such tiles
-// of one (sequence, kv head), so K and V are read once for 256 rows.  A few dozen
-// nodes are far too few rows to keep the tensor cores busy (4 d flops per key and
-// row against 4 d bytes per key): the pass is bound by HBM, and what matters is
-// that every SM reads all the time.  So the units' K/V tiles (128 keys) form one
-// long list, of which every CTA of a one-wave grid takes an equal piece, whatever
-// the lengths.  A unit that lies within one piece is finished there; of a unit cut
-// between pieces each CTA leaves its rows' (m, l, O) in the workspace, and
-// tree_merge_kernel, launched behind as a programmatic dependent, merges them in
-// order (the triples' merge of "S12 FlashAttention", 练习 1).
+// tiles of as many whole nodes as 128 rows hold (row r = node r / G, head r % G).
+// A unit is one or two such tiles of one (sequence, kv head), so K and V are read
+// once for up to 256 rows.  A few dozen nodes are far too few rows to keep the
+// tensor cores busy (4 d flops per key and row against 4 d bytes per key): the pass
+// is bound by HBM, and what matters is that every SM reads all the time.  So the
+// units' K/V tiles (128 keys) form one long list, of which every CTA of a one-wave
+// grid takes an equal piece by cost, whatever the lengths.  A unit that lies within
+// one piece is finished there; of a unit cut between pieces each CTA leaves its
+// rows' (m, l, O) in the workspace, and tree_merge_kernel, launched behind as a
+// programmatic dependent, merges them in order (the triples' merge of "S12
+// FlashAttention", 练习 1).
 //
-//   warp 0       K and V tiles, a page at a time (TMA, 128-byte swizzle)
-//   warp 1       tensor memory; its lane 0 issues every tcgen05.mma
-//   warp 2       query rows into shared memory
+//   warp 0       copies: query tiles, then K and V tiles a page at a time (TMA,
+//                128-byte swizzle)
+//   warps 1, 2   tensor memory; lane 0 of warp 1 + w issues the tcgen05.mma of
+//                softmax warpgroup w (one thread for both left the tensor pipe idle
+//                behind its waits and commits: 4800 clocks a K/V tile for 256 rows)
 //   warp 3       V rows that no node sees are zeroed before the MMA reads them
 //   warps 4-11   softmax, thread = query row = tensor-memory lane
 //
@@ -27,11 +30,8 @@
 // of the unit inside the CTA.
 //
 // Softmax as in the forward: p = 2^(s scale log2 e - ref), the reference raised
-// only when a tile's maximum passes it by more than 8; two sums are kept, of p for
-// the LSE and of the bf16-rounded p that the P V MMA multiplies for O.  A row's 128
-// scores are read from tensor memory twice, for the maximum (reduced by the load
-// itself) and for p, 32 columns at a time: that keeps a thread within the 168
-// registers that 384 threads leave it.
+// only when a tile's maximum passes it by far; two sums are kept, of p for the LSE
+// and of the bf16-rounded p that the P V MMA multiplies for O.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -51,25 +51,29 @@ constexpr int kThreads = 384;
 constexpr int kCtas = 152;        // one per SM
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRaise = 8.f;     // log2 units
+// The reference is raised when a row's maximum passes it by more than this (log2
+// units): p, and bf16's exponent, reach that far, and each raise multiplies O in
+// tensor memory.
+constexpr float kRaise = 24.f;
 
 template <int D>
 struct Cfg {
   static constexpr int kChunks = D / 64;             // 128-byte pieces of a row
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kStages = D == 128 ? 4 : 8;   // K/V ring slots
+  // K/V tiles are laid out in groups of eight keys, a group's 1 KB pieces (64
+  // values of each key) side by side, so that one copy brings a whole page
+  static constexpr int kGroup = 1024 * kChunks;
   static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;   // + alignment slack
   static constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(128, kTile, false, false);
   static constexpr uint32_t kIdescO = ptx::idesc_bf16_f32(128, D, false, true);
 };
 
-// The unit that begins in a CTA's piece and ends in a later one's.
+// The unit whose first tile lies in a CTA's piece and whose last one in a later one's.
 struct Cut {
-  int seq, row0, rows;   // sequence, first of its rows n * G, rows of the unit
-  int head;              // kv head
-  int last;              // CTA of the last piece; -1: no such unit
-  int late;              // the unit is not the first of this CTA's piece
-  int pad[2];
+  int q0, rows, head0, nt;   // first row of the packed q; rows (0: no such unit); first head; tiles
+  int first, weight;         // position of tile 0 in the list, cost of a tile
+  int total, sharers;        // the list
 };
 
 struct Args {
@@ -80,7 +84,7 @@ struct Args {
   const int* mask;
   __nv_bfloat16* o;
   float* lse;
-  int num_seqs, total_q, max_q, words, H, Hkv, G, num_pages, max_blocks;
+  int num_seqs, total_q, max_q, words, H, Hkv, G, tile_nodes, num_pages, max_blocks;
   float scale_log2;
   int skip_first_copy;
   int* status;
@@ -109,50 +113,86 @@ __device__ __forceinline__ Seq load_seq(const Args& a, int s) {
   return Q;
 }
 
-// Units of a sequence along its rows, and K/V tiles of each.
-__device__ __forceinline__ int row_units(const Args& a, const Seq& Q) {
-  return (Q.n * a.G + 2 * kTile - 1) / (2 * kTile);
+// Units of a sequence along its nodes, K/V tiles of each, and the cost of one: with
+// two query tiles it takes about half as long again.
+__device__ __forceinline__ int node_units(const Args& a, const Seq& Q) {
+  return (Q.n + 2 * a.tile_nodes - 1) / (2 * a.tile_nodes);
 }
 __device__ __forceinline__ int key_tiles(const Seq& Q) { return (Q.L + kTile - 1) / kTile; }
+__device__ __forceinline__ int tile_cost(const Args& a, const Seq& Q, bool weighed) {
+  return !weighed ? 1 : Q.n > a.tile_nodes ? 3 : 2;
+}
+// Cost of beginning and ending a unit.
+constexpr int kUnitCost = 4;
+// Tiles a CTA from which on costs are weighed.  (Below, a tile costs 1 and a unit
+// nothing, so that every piece has a tile; above, a piece is longer than any cost, so
+// that of a cut unit every piece between its first and its last tile has one, too.)
+constexpr int kWeighedTiles = 8;
 
 struct Shared {
-  int pre[kMaxTreeSeqs + 1];   // list tiles of sequences 0 .. s - 1
-  int warp_sum[kThreads / 32];
+  int pre[kMaxTreeSeqs + 1];   // cost of sequences 0 .. s - 1
+  int warp_sum[2][kThreads / 32];
   uint64_t q_full[2], q_empty[2];   // Q tile i
   uint64_t kv_full[8], kv_empty[8]; // ring slots
   uint64_t fix_full[8];             // ring slots: a V tile landed that is to be cleaned
   uint64_t s_full[2], p_full[2], o_done[2], o_empty[2];
   uint64_t stat_full, stat_empty;   // warpgroup 1's row states are in stat / were read
-  uint64_t drain;
+  uint64_t drain[2];
+  uint64_t turn[2];                 // two query tiles: issuer w may go on
   float stat[kTile][3];
   uint32_t tmem_base;
   int abort;
 };
 
-// The part of a unit that lies in this CTA's piece: tiles [j0, j1) of nt.
-struct Seg {
-  int s, g, row0, rows;   // rows: of the unit, at most 256
-  Seq Q;
-  int j0, j1, nt;
-  bool pair;              // two query tiles
+// The list: sequence s begins at pre[s]; each of its units takes `begin` and then
+// its tiles' cost.  The CTA of [xb, xe) has the tiles whose position lies in it.
+struct List {
+  const int* pre;
+  bool weighed;
+  int begin, xb, xe;
 };
 
-// The segment at list position x, and the position behind it.
-__device__ __forceinline__ int segment(const Args& a, const int* pre, int x, int xe, int& s, Seg& S) {
-  while (pre[s + 1] <= x) ++s;
-  S.s = s;
-  S.Q = load_seq(a, s);
-  S.nt = key_tiles(S.Q);
-  const int ru = row_units(a, S.Q);
-  const int u = (x - pre[s]) / S.nt;
-  const int u0 = pre[s] + u * S.nt;
-  S.g = u / ru;
-  S.row0 = (u - S.g * ru) * 2 * kTile;
-  S.rows = min(2 * kTile, S.Q.n * a.G - S.row0);
-  S.pair = S.rows > kTile;
-  S.j0 = x - u0;
-  S.j1 = min(xe - u0, S.nt);
-  return u0 + S.j1;
+// The part of a unit that lies in this CTA's piece: tiles [j0, j1) of nt.
+struct Seg {
+  int s, g, node0, nodes;   // nodes of the unit, of one or two query tiles
+  Seq Q;
+  int first, cost;          // position of tile 0, cost of a tile
+  int j0, j1, nt;
+  bool pair;                // two query tiles
+};
+
+// The copies of a segment go out in the order in which the MMAs use them, so that the
+// ring's slots are freed in order: K 0, V 0, K 1, V 1, ... for two query tiles
+// (S(j + 1) follows P V(j)); K 0, K 1, V 0, K 2, V 1, K 3, ... for one, whose scores
+// are formed two tiles ahead.  Number of the copy of V(j) of nt tiles; behind it comes
+// K(j + 1) or K(j + 2), if there is one.
+__device__ __forceinline__ int copy_v(bool pair, int j, int nt) {
+  return pair ? 2 * j + 1 : min(2, nt) + j + min(j, max(nt - 2, 0));
+}
+
+// Steps through the segments of a piece: x is a position in the unit to look at (it
+// begins at list.xb) and s its sequence.  False when there are no more.
+__device__ __forceinline__ bool next_segment(const Args& a, const List& list, int& x, int& s, Seg& S) {
+  while (x < list.xe) {
+    while (list.pre[s + 1] <= x) ++s;
+    S.s = s;
+    S.Q = load_seq(a, s);
+    S.nt = key_tiles(S.Q);
+    S.cost = tile_cost(a, S.Q, list.weighed);
+    const int along = node_units(a, S.Q);
+    const int unit = list.begin + S.nt * S.cost;
+    const int u = (x - list.pre[s]) / unit;
+    S.first = list.pre[s] + u * unit + list.begin;
+    x = S.first + S.nt * S.cost;
+    S.g = u / along;
+    S.node0 = (u - S.g * along) * 2 * a.tile_nodes;
+    S.nodes = min(2 * a.tile_nodes, S.Q.n - S.node0);
+    S.pair = S.nodes > a.tile_nodes;
+    S.j0 = max(0, list.xb - S.first + S.cost - 1) / S.cost;
+    S.j1 = min(S.nt, max(0, list.xe - S.first + S.cost - 1) / S.cost);
+    if (S.j0 < S.j1) return true;
+  }
+  return false;
 }
 
 // Which of the keys k0 + 32 c .. + 31 node i sees, as bits.
@@ -185,8 +225,8 @@ __device__ __forceinline__ float sum_packed(const uint32_t (&p)[16]) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                 const Args a) {
+tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, const Args a) {
   using C = Cfg<D>;
   constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -203,28 +243,29 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   const uint32_t bar_s = ptx::smem_u32(sh.s_full), bar_p = ptx::smem_u32(sh.p_full);
   const uint32_t bar_o = ptx::smem_u32(sh.o_done), bar_oe = ptx::smem_u32(sh.o_empty);
   const uint32_t bar_sf = ptx::smem_u32(&sh.stat_full), bar_se = ptx::smem_u32(&sh.stat_empty);
-  const uint32_t bar_drain = ptx::smem_u32(&sh.drain);
+  const uint32_t bar_drain = ptx::smem_u32(sh.drain), bar_turn = ptx::smem_u32(sh.turn);
 
   // the merge behind this kernel may start its own set-up (it waits for this
   // kernel's completion before it reads the partials)
   asm volatile("griddepcontrol.launch_dependents;");
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(bar_q + 8 * i, 32);
-      ptx::mbar_init(bar_qe + 8 * i, 1);
+      ptx::mbar_init(bar_q + 8 * i, 1);
+      ptx::mbar_init(bar_qe + 8 * i, 2);    // an arrival of each issuer, here and below
       ptx::mbar_init(bar_s + 8 * i, 1);
       ptx::mbar_init(bar_p + 8 * i, kTile);
       ptx::mbar_init(bar_o + 8 * i, 1);
       ptx::mbar_init(bar_oe + 8 * i, kTile);
+      ptx::mbar_init(bar_drain + 8 * i, 1);
+      ptx::mbar_init(bar_turn + 8 * i, 1);
     }
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(bar_kvf + 8 * i, 1);
-      ptx::mbar_init(bar_kve + 8 * i, 1);
+      ptx::mbar_init(bar_kve + 8 * i, 2);
       ptx::mbar_init(bar_fix + 8 * i, 1);
     }
     ptx::mbar_init(bar_sf, kTile);
     ptx::mbar_init(bar_se, kTile);
-    ptx::mbar_init(bar_drain, 1);
     sh.abort = 0;
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
@@ -233,26 +274,40 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     ptx::tmem_alloc(ptx::smem_u32(&sh.tmem_base), 512);
     ptx::tmem_relinquish();
   }
-  {  // the list's offsets
-    const int per = (a.num_seqs + kThreads - 1) / kThreads;
-    const int s0 = min(a.num_seqs, (int)threadIdx.x * per), s1 = min(a.num_seqs, s0 + per);
+  // the list: how many tiles there are, whether beginning a unit counts, the offsets
+  const int per = (a.num_seqs + kThreads - 1) / kThreads;
+  const int s0 = min(a.num_seqs, (int)threadIdx.x * per), s1 = min(a.num_seqs, s0 + per);
+  int tiles = 0;
+  List list{sh.pre, false, 0, 0, 0};
+  {
     int mine = 0;
     for (int s = s0; s < s1; ++s) {
       const Seq Q = load_seq(a, s);
       if (Q.bad && blockIdx.x == 0) atomicExch(status, kDevInvalidArg);
-      if (Q.n > 0) mine += row_units(a, Q) * a.Hkv * key_tiles(Q);
-      sh.pre[s + 1] = mine;
+      if (Q.n > 0) mine += node_units(a, Q) * a.Hkv * key_tiles(Q);
     }
-    int run = mine;
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (lane == 0) sh.warp_sum[0][warp] = mine;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) tiles += sh.warp_sum[0][w];
+    list.weighed = tiles >= kWeighedTiles * (int)gridDim.x;
+    list.begin = list.weighed ? kUnitCost : 0;
+    int run = 0;
+    for (int s = s0; s < s1; ++s) {
+      const Seq Q = load_seq(a, s);
+      if (Q.n > 0) run += node_units(a, Q) * a.Hkv * (list.begin + key_tiles(Q) * tile_cost(a, Q, list.weighed));
+      sh.pre[s + 1] = run;
+    }
+    const int own = run;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, run, o);
       if (lane >= o) run += v;
     }
-    if (lane == 31) sh.warp_sum[warp] = run;
+    if (lane == 31) sh.warp_sum[1][warp] = run;
     __syncthreads();
-    int base = run - mine;
-    for (int w = 0; w < warp; ++w) base += sh.warp_sum[w];
+    int base = run - own;
+    for (int w = 0; w < warp; ++w) base += sh.warp_sum[1][w];
     for (int s = s0; s < s1; ++s) sh.pre[s + 1] += base;
     if (threadIdx.x == 0) sh.pre[0] = 0;
   }
@@ -261,251 +316,219 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   ptx::tc_fence_after();
   const uint32_t tbase = sh.tmem_base;
   const int total = sh.pre[a.num_seqs];
-  const int W = min((int)gridDim.x, total);
+  const int W = min((int)gridDim.x, tiles);
   const int cta = blockIdx.x;
-  const int xb = cta < W ? (int)((long long)cta * total / W) : 0;
-  const int xe = cta < W ? (int)((long long)(cta + 1) * total / W) : 0;
   int s_first = 0;   // the sequence that holds position xb
-  if (xb < xe) {
+  if (cta < W) {
+    list.xb = (int)((long long)cta * total / W);
+    list.xe = (int)((long long)(cta + 1) * total / W);
     int hi = a.num_seqs;   // pre[s_first] <= xb < pre[hi]
     while (hi - s_first > 1) {
       const int mid = (s_first + hi) >> 1;
-      if (sh.pre[mid] <= xb) s_first = mid;
+      if (sh.pre[mid] <= list.xb) s_first = mid;
       else hi = mid;
     }
   }
 
+  int x = list.xb, s = s_first;
+  Seg S;
   if (warp == 0) {
-    // ------------------------------------------------------ K and V tiles
+    // -------------------------------------------------------------- copies
     int li = 0;                 // tiles issued
+    int nq[2] = {0, 0}, half = 0;
     uint32_t to_fix = 0u;       // slots whose last copy went to the fix barrier,
     uint32_t fixes = 0u;        // and the parity of the slots' copies that did
     bool ok = true, skip = a.skip_first_copy != 0;
-    int s = s_first;
-    for (int x = xb; x < xe && ok;) {
-      Seg S;
-      x = segment(a, sh.pre, x, xe, s, S);
+    while (ok && next_segment(a, list, x, s, S)) {
+      for (int i = 0; i < (S.pair ? 2 : 1) && ok; ++i) {
+        // (rows past the sequence's last node are its neighbour's, or zeros behind the
+        // last row of all: they only reach their own rows of S and O, which nobody reads)
+        const int qb = S.pair ? i : half;
+        const int phase = qb == 0 ? nq[0] : nq[1];
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_qe + 8 * qb, (phase & 1) ^ 1, status, abort_flag));
+        if (!ok) break;
+        if (qb == 0) ++nq[0];
+        else ++nq[1];
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(bar_q + 8 * qb, a.tile_nodes * a.G * D * 2);
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+            ptx::tma_load_3d(ptx::smem_u32(sQ) + qb * C::kTileBytes + c * 16384, &tmQ, 64 * c, S.g * a.G,
+                             S.Q.q0 + S.node0 + i * a.tile_nodes, bar_q + 8 * qb);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (!S.pair) half ^= 1;
       const int* ids = a.block_table + (size_t)S.s * a.max_blocks;
-      // (lane pg: page pg of the tile, looked up a tile ahead)
-      auto look_up = [&](int j) { return lane < 8 && j * kTile + lane * kPage < S.Q.L ? __ldg(ids + j * 8 + lane) : 0; };
-      int id_next = look_up(S.j0);
-      for (int j = S.j0; j < S.j1 && ok; ++j) {
-        int id = id_next;
-        if (j + 1 < S.j1) id_next = look_up(j + 1);
+      // (lane pg: page pg of tile j)
+      auto look_up = [&](int j) {
+        return lane < 8 && j < S.j1 && j * kTile + lane * kPage < S.Q.L ? __ldg(ids + j * 8 + lane) : 0;
+      };
+      auto copy = [&](int which, int j, int id) {
         const int npages = (min(kTile, S.Q.L - j * kTile) + kPage - 1) / kPage;
         if (lane < npages && (id < 0 || id >= a.num_pages)) {
           atomicExch(status, kDevBadBlockTable);
           id = 0;
         }
-        const bool fix = (j + 1) * kTile > S.Q.L - S.Q.n;   // the tile holds nodes
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-          const int slot = li % kStages;
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_kve + 8 * slot, ((li / kStages) & 1) ^ 1, status,
-                                                      abort_flag));
-          if (!ok) break;
-          const bool cleaned = fix && which == 1;
-          const uint32_t bar = (cleaned ? bar_fix : bar_kvf) + 8 * slot;
-          const uint32_t dst = ptx::smem_u32(sKV) + slot * C::kTileBytes;
-          if (lane == 0 && !skip) ptx::mbar_arrive_expect_tx(bar, npages * kPage * D * 2);
-          __syncwarp();
-          if (lane < npages && !skip) {
-            const int row = (id * a.Hkv + S.g) * kPage;
-#pragma unroll
-            for (int c = 0; c < C::kChunks; ++c)
-              ptx::tma_load_2d(dst + c * 16384 + lane * 2048, which ? &tmV : &tmK, 64 * c, row, bar);
-          }
-          skip = false;
-          to_fix = (to_fix & ~(1u << slot)) | ((cleaned ? 1u : 0u) << slot);
-          if (cleaned) fixes ^= 1u << slot;
-          ++li;
-        }
+        const int slot = li % kStages;
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_kve + 8 * slot, ((li / kStages) & 1) ^ 1, status,
+                                                    abort_flag));
+        if (!ok) return;
+        // (tiles that hold nodes: warp 3 cleans their V rows first)
+        const bool cleaned = which == 1 && (j + 1) * kTile > S.Q.L - S.Q.n;
+        const uint32_t bar = (cleaned ? bar_fix : bar_kvf) + 8 * slot;
+        const uint32_t dst = ptx::smem_u32(sKV) + slot * C::kTileBytes;
+        if (lane == 0 && !skip) ptx::mbar_arrive_expect_tx(bar, npages * kPage * D * 2);
+        __syncwarp();
+        if (lane < npages && !skip)
+          ptx::tma_load_4d(dst + lane * 2 * C::kGroup, which ? &tmV : &tmK, 0, 0, 0, (id * a.Hkv + S.g) * 2, bar);
+        skip = false;
+        to_fix = (to_fix & ~(1u << slot)) | ((cleaned ? 1u : 0u) << slot);
+        if (cleaned) fixes ^= 1u << slot;
+        ++li;
+      };
+      // page ids of tiles j to j + 3, the last looked up long before its copy
+      int i0 = look_up(S.j0), i1 = look_up(S.j0 + 1), i2 = look_up(S.j0 + 2), i3;
+      copy(0, S.j0, i0);
+      if (!S.pair && ok && S.j0 + 1 < S.j1) copy(0, S.j0 + 1, i1);
+      for (int j = S.j0; j < S.j1 && ok; ++j) {
+        i3 = look_up(j + 3);
+        copy(1, j, i0);
+        const int jk = j + (S.pair ? 1 : 2);
+        if (ok && jk < S.j1) copy(0, jk, S.pair ? i1 : i2);
+        i0 = i1;
+        i1 = i2;
+        i2 = i3;
       }
     }
-    if (!ok && lane == 0)   // let the copies in flight land before shared memory is released
+    if (!ok && lane == 0) {   // let the copies in flight land before shared memory is released
       for (int l = max(0, li - kStages); l < li; ++l) {
         const int slot = l % kStages;
         if (to_fix >> slot & 1u) ptx::mbar_wait(bar_fix + 8 * slot, (fixes >> slot & 1u) ^ 1u, nullptr);
         else ptx::mbar_wait(bar_kvf + 8 * slot, (l / kStages) & 1, nullptr);
       }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (nq[i] > 0) ptx::mbar_wait(bar_q + 8 * i, (nq[i] - 1) & 1, nullptr);
+    }
     __syncwarp();
-  } else if (warp == 1 && lane == 0) {
-    // -------------------------------------------------------- MMA issuer
-    const uint64_t qdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sQ), 16, 1024);
-    const uint64_t kdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 16, 1024);
-    const uint64_t vdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 16384, 1024);
-    int lc = 0;                    // tiles consumed
-    int nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};
-    int half = 0;                  // Q buffer of the next one-tile unit
-    bool ok = true;
-    auto issue_s = [&](int w, int qb, int l) {   // S_w = Q K(l)^T
-      const int slot = l % kStages;
-      const uint64_t qd = qdesc0 + (uint64_t)(qb * (C::kTileBytes >> 4));
-      const uint64_t kd = kdesc0 + (uint64_t)(slot * (C::kTileBytes >> 4));
+  } else if (warp <= 2) {
+    if (lane == 0) {
+      // ------------------------------------------------------ MMA issuers
+      const int w = warp - 1;
+      const uint64_t qdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sQ), 16, 1024);
+      const uint64_t kdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 16, C::kGroup);
+      const uint64_t vdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 1024, C::kGroup);
+      const uint32_t s_tm = tbase + w * kTile, o_tm = tbase + 256 + w * 128;
+      int lc = 0;                    // copies of the segments so far
+      int nq[2] = {0, 0}, half = 0;  // query tiles used, the buffer of the next single one
+      int np = 0, no = 0, nturn = 0; // P tiles, units, turns taken
+      bool ok = true;
+      // Every copy is waited for, and its slot released, by both issuers, so that a
+      // barrier's phase is never ahead of a wait by two; one that the other issuer
+      // alone uses is passed.
+      auto landed = [&](int l) {
+        return ptx::mbar_wait(bar_kvf + 8 * (l % kStages), (l / kStages) & 1, status, abort_flag);
+      };
+      auto pass = [&](int l) {
+        if (!landed(l)) return false;
+        ptx::mbar_arrive(bar_kve + 8 * (l % kStages));
+        return true;
+      };
+      // With two query tiles the issuers take turns, a turn being P V(j) and S(j + 1):
+      // one warpgroup's exponentials then run beside the other's MMAs.  (Left alone, the
+      // two fall into step, as both wait for the same K/V tiles.)
+      auto take_turn = [&]() {
+        if (w == 0 && nturn == 0) {
+          ++nturn;
+          return true;
+        }
+        return ptx::mbar_wait(bar_turn + 8 * w, (nturn++ - (w == 0 ? 1 : 0)) & 1, status, abort_flag);
+      };
+      auto score = [&](int l, int qb, bool last) {   // S = Q K^T, K being copy l
+        if (!landed(l)) return false;
+        ptx::tc_fence_after();
+        const int slot = l % kStages;
+        const uint64_t qd = qdesc0 + (uint64_t)(qb * (C::kTileBytes >> 4));
+        const uint64_t kd = kdesc0 + (uint64_t)(slot * (C::kTileBytes >> 4));
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-        ptx::mma_ss(tbase + w * kTile, qd + off, kd + off, C::kIdescS, k > 0);
-      }
-      ptx::tc_commit(bar_s + 8 * w);
-    };
-    auto wait_kv = [&](int l) {
-      return ptx::mbar_wait(bar_kvf + 8 * (l % kStages), (l / kStages) & 1, status, abort_flag);
-    };
-    auto free_kv = [&](int l) { ptx::tc_commit(bar_kve + 8 * (l % kStages)); };
-    auto issue_pv = [&](int w, int l, bool first) {   // O_w (+)= P_w V(l)
-      if (first && !ptx::mbar_wait(bar_oe + 8 * w, (no[w] & 1) ^ 1, status, abort_flag)) return false;
-      if (!ptx::mbar_wait(bar_p + 8 * w, np[w] & 1, status, abort_flag)) return false;
-      ++np[w];
-      ptx::tc_fence_after();
-      const uint64_t vd = vdesc0 + (uint64_t)((l % kStages) * (C::kTileBytes >> 4));
+        for (int k = 0; k < D / 16; ++k)
+          ptx::mma_ss(s_tm, qd + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
+                      kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), C::kIdescS, k > 0);
+        ptx::tc_commit(bar_s + 8 * w);
+        if (S.pair) ptx::mbar_arrive(bar_turn + 8 * (w ^ 1));
+        ptx::tc_commit(bar_kve + 8 * slot);
+        if (last) ptx::tc_commit(bar_qe + 8 * qb);
+        return true;
+      };
+      auto values = [&](int l, bool first) {         // O (+)= P V, V being copy l
+        if (!landed(l) || !ptx::mbar_wait(bar_p + 8 * w, np & 1, status, abort_flag)) return false;
+        ++np;
+        if (S.pair && !take_turn()) return false;
+        ptx::tc_fence_after();
+        const int slot = l % kStages;
+        const uint64_t vd = vdesc0 + (uint64_t)(slot * (C::kTileBytes >> 4));
 #pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        ptx::mma_ts(tbase + 256 + w * 128, tbase + w * kTile + k * 8, vd + (uint64_t)(k * 128), C::kIdescO,
-                    (!first || k > 0) ? 1u : 0u);
-      return true;
-    };
-    int s = s_first;
-    for (int x = xb; x < xe && ok;) {
-      Seg S;
-      x = segment(a, sh.pre, x, xe, s, S);
-      const int nt = S.j1 - S.j0;
-      if (S.pair) {
+        for (int k = 0; k < kTile / 16; ++k)
+          ptx::mma_ts(o_tm, s_tm + k * 8, vd + (uint64_t)(k * (C::kGroup >> 3)), C::kIdescO,
+                      (!first || k > 0) ? 1u : 0u);
+        ptx::tc_commit(bar_kve + 8 * slot);
+        return true;
+      };
+      while (ok && next_segment(a, list, x, s, S)) {
+        const int nt = S.j1 - S.j0;
+        const int step = S.pair ? 1 : 2, j0 = S.pair ? 0 : w;   // this issuer's tiles
+        const int qb = S.pair ? w : half;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 2; ++i) {                           // the query tiles
+          if (!S.pair && i != half) continue;
           ok = ok && ptx::mbar_wait(bar_q + 8 * i, nq[i] & 1, status, abort_flag);
           ++nq[i];
+          if (ok && (i != qb || j0 >= nt)) ptx::mbar_arrive(bar_qe + 8 * i);
         }
-        ok = ok && wait_kv(lc);
-        if (!ok) break;
-        ptx::tc_fence_after();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          issue_s(i, i, lc);
-          if (nt == 1) ptx::tc_commit(bar_qe + 8 * i);
+        if (!S.pair) half ^= 1;
+        if (S.pair) {
+          ok = ok && landed(lc) && take_turn() && score(lc, qb, nt == 1);
+        } else {
+          for (int j = 0; j < min(2, nt) && ok; ++j) ok = j == w ? score(lc + j, qb, j + 2 >= nt) : pass(lc + j);
         }
-        free_kv(lc);
-        for (int j = 0; j < nt; ++j) {
-          const bool next = j + 1 < nt;
-          ok = wait_kv(lc + 2 * j + 1) && (!next || wait_kv(lc + 2 * j + 2));
-          if (!ok) break;
-          ptx::tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            ok = ok && issue_pv(i, lc + 2 * j + 1, j == 0);
-            if (!ok) break;
-            if (!next) ptx::tc_commit(bar_o + 8 * i);
-            if (next) {
-              issue_s(i, i, lc + 2 * j + 2);
-              if (j + 2 == nt) ptx::tc_commit(bar_qe + 8 * i);
-            }
+        for (int j = 0; j < nt && ok; ++j) {
+          const bool mine = S.pair || (j & 1) == w, next = j + step < nt;
+          const int lv = lc + copy_v(S.pair, j, nt);            // K(j + step) is the copy behind it
+          if (mine) {
+            // (the previous unit's O is read out of tensor memory)
+            if (j == j0 && !(ok = ptx::mbar_wait(bar_oe + 8 * w, (no++ & 1) ^ 1, status, abort_flag))) break;
+            ok = values(lv, j == j0) && (!next || score(lv + 1, qb, j + 2 * step >= nt));
+            if (ok && !next) ptx::tc_commit(bar_o + 8 * w);
+            if (S.pair && !next) ptx::mbar_arrive(bar_turn + 8 * (w ^ 1));
+          } else {
+            ok = pass(lv) && (!next || pass(lv + 1));
           }
-          if (!ok) break;
-          free_kv(lc + 2 * j + 1);
-          if (next) free_kv(lc + 2 * j + 2);
         }
-        ++no[0];
-        ++no[1];
-      } else {
-        const int qb = half;
-        half ^= 1;
-        ok = qb == 0 ? ptx::mbar_wait(bar_q, nq[0] & 1, status, abort_flag)
-                     : ptx::mbar_wait(bar_q + 8, nq[1] & 1, status, abort_flag);
-        if (qb == 0) ++nq[0];
-        else ++nq[1];
-        // S of tile j goes to warpgroup j mod 2
-        auto score = [&](int w, int j) {
-          issue_s(w, qb, lc + 2 * j);
-          if (j == nt - 1) ptx::tc_commit(bar_qe + 8 * qb);
-          free_kv(lc + 2 * j);
-        };
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-          if (ok && w < nt) {
-            ok = wait_kv(lc + 2 * w);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            score(w, w);
-          }
-        for (int j0 = 0; j0 < nt && ok; j0 += 2)
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const int j = j0 + w;
-            if (j >= nt || !ok) break;
-            const bool next = j + 2 < nt;
-            ok = wait_kv(lc + 2 * j + 1) && (!next || wait_kv(lc + 2 * j + 4));
-            if (!ok) break;
-            ptx::tc_fence_after();
-            ok = issue_pv(w, lc + 2 * j + 1, j == w);
-            if (!ok) break;
-            if (!next) ptx::tc_commit(bar_o + 8 * w);
-            free_kv(lc + 2 * j + 1);
-            if (next) score(w, j + 2);
-          }
-        ++no[0];
-        if (nt > 1) ++no[1];
+        lc += 2 * nt;
       }
-      lc += 2 * nt;
+      // no tcgen05.mma may still run when the tensor memory is released
+      ptx::tc_commit(bar_drain + 8 * w);
+      ptx::mbar_wait(bar_drain + 8 * w, 0, nullptr);
     }
-    // no tcgen05.mma may still run when the tensor memory is released
-    ptx::tc_commit(bar_drain);
-    ptx::mbar_wait(bar_drain, 0, nullptr);
-  } else if (warp == 2) {
-    // --------------------------------------------------------- query rows
-    int nq[2] = {0, 0}, half = 0;
-    bool ok = true;
-    int s = s_first;
-    for (int x = xb; x < xe && ok;) {
-      Seg S;
-      x = segment(a, sh.pre, x, xe, s, S);
-      const int tiles = S.pair ? 2 : 1;
-      for (int i = 0; i < tiles; ++i) {
-        const int qb = S.pair ? i : half;
-        const int phase = qb == 0 ? nq[0] : nq[1];
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_qe + 8 * qb, (phase & 1) ^ 1, status, abort_flag));
-        if (!ok) break;
-        const int r0 = S.row0 + i * kTile;
-        const int rows = min(kTile, S.rows - i * kTile);
-        const uint32_t dst = ptx::smem_u32(sQ) + qb * C::kTileBytes;
-        // (rows past the last one keep what was there: they only reach their own
-        // rows of S and O, which nobody reads)
-        for (int e = lane; e < rows * (D / 8); e += 32) {
-          const int r = e / (D / 8), u = e % (D / 8);
-          const int node = (r0 + r) / a.G, h = (r0 + r) - node * a.G;
-          const __nv_bfloat16* src =
-              a.q + ((size_t)(S.Q.q0 + node) * a.H + S.g * a.G + h) * D + u * 8;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                           dst + (u >> 3) * 16384 + r * 128 + (((u & 7) ^ (r & 7)) << 4)),
-                       "l"(src)
-                       : "memory");
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(bar_q + 8 * qb);
-        if (qb == 0) ++nq[0];
-        else ++nq[1];
-      }
-      if (!S.pair) half ^= 1;
-    }
+    __syncwarp();
   } else if (warp == 3) {
     // ------------------------------------------------- V rows nobody sees
     // Their weights are exactly 0, but they may hold anything and 0 * NaN is NaN.
     int lc = 0;
     uint32_t fixes = 0u;   // parity of each slot's copies to the fix barrier
     bool ok = true;
-    int s = s_first;
-    for (int x = xb; x < xe && ok;) {
-      Seg S;
-      x = segment(a, sh.pre, x, xe, s, S);
-      const int i0 = S.row0 / a.G, i1 = (S.row0 + S.rows - 1) / a.G + 1;   // the unit's nodes
-      const int fix0 = (S.Q.L - S.Q.n) / kTile;                            // first tile with nodes
+    while (ok && next_segment(a, list, x, s, S)) {
+      const int i0 = S.node0, i1 = S.node0 + S.nodes;
+      const int fix0 = (S.Q.L - S.Q.n) / kTile;   // first tile with nodes
       for (int j = max(S.j0, fix0); j < S.j1; ++j) {
         // lane: the union over every eighth node of 32 keys' bits
         uint32_t seen = 0u;
         for (int i = i0 + (lane >> 2); i < i1; i += 8) seen |= sees(a, S.Q, i, j * kTile + 32 * (lane & 3));
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) seen |= __shfl_xor_sync(0xffffffffu, seen, o);
-        const int slot = (lc + 2 * (j - S.j0) + 1) % kStages;
+        const int slot = (lc + copy_v(S.pair, j - S.j0, S.j1 - S.j0)) % kStages;
         ok = __all_sync(0xffffffffu,
                         ptx::mbar_wait(bar_fix + 8 * slot, fixes >> slot & 1u, status, abort_flag));
         if (!ok) break;
@@ -525,8 +548,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             if (row >= 0)
 #pragma unroll
               for (int h = 0; h < C::kChunks; ++h)
-                *reinterpret_cast<uint4*>(tile + h * 16384 + (32 * c + row) * 128 + (lane & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(tile + (4 * c + (row >> 3)) * C::kGroup + h * 1024 + (row & 7) * 128 +
+                                          (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         ptx::fence_proxy_async_smem();
@@ -546,31 +569,20 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     const uint64_t sc2 = ptx::f2_bits(a.scale_log2, a.scale_log2);
     int ns = 0, nod[2] = {0, 0}, nstat = 0;
     bool ok = true;
-    int s = s_first;
-    if (threadIdx.x == 128 && cta < (int)gridDim.x) {
-      // what the merge finds of this CTA: the unit that begins here and is cut
-      Cut cut{0, 0, 0, 0, -1, 0, {0, 0}};
-      if (xb < xe) {
-        int se = s_first;
-        Seg S;
-        while (sh.pre[se + 1] <= xe - 1) ++se;
-        segment(a, sh.pre, xe - 1, xe, se, S);
-        const int u0 = xe - 1 - S.j0, u1 = u0 + S.nt;   // the unit of the piece's last tile
-        if (u0 >= xb && u1 > xe)
-          cut = Cut{S.s, S.row0, S.rows, S.g, (int)(((long long)u1 * W - 1) / total), u0 > xb, {0, 0}};
-      }
-      a.cuts[cta] = cut;
+    if (threadIdx.x == 128) {   // for the merge: no unit cut behind this piece, until one is met
+      a.cuts[cta] = Cut{0, 0, 0, 0, 0, 0, 0, 0};
     }
-    for (int x = xb; x < xe && ok;) {
-      Seg S;
-      const int seg_x = x;
-      x = segment(a, sh.pre, x, xe, s, S);
+    while (ok && next_segment(a, list, x, s, S)) {
       const int nt = S.j1 - S.j0;
-      const int row = S.pair ? w * kTile + r : r;          // of the unit
-      const bool valid = row < S.rows;
-      const int node = (S.row0 + row) / a.G;
+      const int tile_rows = a.tile_nodes * a.G;
+      const int rows = min(tile_rows, S.nodes * a.G - (S.pair && w == 1 ? tile_rows : 0));   // of this tile
+      const bool valid = r < rows;
+      const int node = S.node0 + (S.pair && w == 1 ? a.tile_nodes : 0) + r / a.G;
+      const int row = (S.pair && w == 1 ? tile_rows : 0) + r;                // of the unit
       // a warp without a valid row leaves P as it is: it reaches only its own rows
-      const bool any = (S.pair ? w * kTile : 0) + quarter * 32 < S.rows;
+      const bool any = quarter * 32 < rows;
+      if (threadIdx.x == 128 && S.j0 == 0 && S.j1 < S.nt)
+        a.cuts[cta] = Cut{S.Q.q0 + S.node0, S.nodes * a.G, S.g * a.G, S.nt, S.first, S.cost, total, W};
       float m_ref = -INFINITY, l_run = 0.f, l_p = 0.f;
       const int step = S.pair ? 1 : 2, jw = S.pair ? 0 : w;
       for (int jl = jw; jl < nt; jl += step) {
@@ -587,10 +599,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         ptx::tc_fence_after();
         if (any) {
           float mx = -INFINITY;
-          if (!masked) {
-#pragma unroll
-            for (int c = 0; c < 4; c += 2) {
-              uint32_t x0[32], x1[32];
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            uint32_t x0[32], x1[32];
+            if (!masked) {   // the loads reduce the maximum themselves
               float m0, m1;
               ptx::tmem_ld32_max(s_col + c * 32, x0, m0);
               ptx::tmem_ld32_max(s_col + c * 32 + 32, x1, m1);
@@ -599,22 +611,20 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
               for (int e = 0; e < 32; ++e)   // (the registers stay theirs until the loads are done)
                 asm volatile("" ::"r"(x0[e]), "r"(x1[e]));
               mx = ptx::fmax3(mx, m0, m1);
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t x32[32];
-              ptx::tmem_ld32(s_col + c * 32, x32);
+            } else {
+              const uint32_t v0 = c == 0 ? vis[0] : vis[2], v1 = c == 0 ? vis[1] : vis[3];
+              ptx::tmem_ld32(s_col + c * 32, x0);
+              ptx::tmem_ld32(s_col + c * 32 + 32, x1);
               ptx::tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                mx = fmaxf(mx, vis[c] >> e & 1u ? __uint_as_float(x32[e]) : -INFINITY);
+                mx = ptx::fmax3(mx, v0 >> e & 1u ? __uint_as_float(x0[e]) : -INFINITY,
+                                v1 >> e & 1u ? __uint_as_float(x1[e]) : -INFINITY);
             }
           }
           const float m_tile = mx * a.scale_log2;   // scale > 0: the maximum commutes with it
-          const bool raise = valid && (m_tile > m_ref + kRaise || (m_ref == -INFINITY && m_tile > -INFINITY));
           float alpha = 1.f;
-          if (raise) {
+          if (valid && (m_tile > m_ref + kRaise || (m_ref == -INFINITY && m_tile > -INFINITY))) {
             alpha = m_ref == -INFINITY ? 1.f : ptx::ex2(m_ref - m_tile);
             m_ref = m_tile;
             l_run *= alpha;
@@ -622,7 +632,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           }
           // (S of this tile is complete, so every earlier P V is: they were issued
           // before it)
-          if (__any_sync(0xffffffffu, raise && jl > jw && alpha != 1.f)) {
+          if (__any_sync(0xffffffffu, jl > jw && alpha != 1.f)) {
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t ov[32];
@@ -635,35 +645,43 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           }
           const float ref = m_ref == -INFINITY ? 0.f : m_ref;
           const uint64_t nref2 = ptx::f2_bits(-ref, -ref);
-          // P (bf16 pairs) overwrites S from its first column on: chunk c goes to
-          // columns 16 c .. 16 c + 15, which belong to scores read before
-          uint32_t sr[2][32];
-          ptx::tmem_ld32(s_col, sr[0]);
-          uint64_t sum2 = ptx::f2_bits(0.f, 0.f), sum2b = sum2;
+          uint64_t sum2[2] = {ptx::f2_bits(0.f, 0.f), ptx::f2_bits(0.f, 0.f)};
+          // P (bf16 pairs) overwrites S from its first column on: 32 keys' go to 16
+          // columns whose scores were read before
+          auto form = [&](uint32_t (&x)[32], int c) __attribute__((always_inline)) {
+            if (masked) {
+              const uint32_t v = c == 0 ? vis[0] : c == 1 ? vis[1] : c == 2 ? vis[2] : vis[3];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            ptx::tmem_wait_ld();
-            if (c < 3) ptx::tmem_ld32(s_col + (c + 1) * 32, sr[(c + 1) & 1]);
-            uint32_t pr[16];
+              for (int e = 0; e < 32; ++e) x[e] = v >> e & 1u ? x[e] : 0xff800000u;
+            }
+            uint32_t pp[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              float s0 = __uint_as_float(sr[c & 1][e]), s1 = __uint_as_float(sr[c & 1][e + 1]);
-              if (masked) {
-                s0 = vis[c] >> e & 1u ? s0 : -INFINITY;
-                s1 = vis[c] >> (e + 1) & 1u ? s1 : -INFINITY;
-              }
               float x0, x1;
-              ptx::f2_split(ptx::ffma2(ptx::f2_bits(s0, s1), sc2, nref2), x0, x1);
+              ptx::f2_split(ptx::ffma2(ptx::f2_bits(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), sc2, nref2),
+                            x0, x1);
               const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
-              if (e & 2) sum2b = ptx::fadd2(sum2b, ptx::f2_bits(p0, p1));
-              else sum2 = ptx::fadd2(sum2, ptx::f2_bits(p0, p1));
-              pr[e / 2] = ptx::pack_bf16x2(p0, p1);
+              sum2[(e / 2) & 1] = ptx::fadd2(sum2[(e / 2) & 1], ptx::f2_bits(p0, p1));
+              pp[e / 2] = ptx::pack_bf16x2(p0, p1);
             }
-            ptx::tmem_st16(s_col + c * 16, pr);
-            l_p += sum_packed(pr);
+            ptx::tmem_st16(s_col + c * 16, pp);
+            l_p += sum_packed(pp);
+          };
+          // (a rolled loop: unrolled, the code of the softmax warps pushes that of the
+          // issuers out of the instruction cache)
+          uint32_t xa[32], xb[32];
+          ptx::tmem_ld32(s_col, xa);
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            ptx::tmem_wait_ld();
+            ptx::tmem_ld32(s_col + c * 32 + 32, xb);
+            form(xa, c);
+            ptx::tmem_wait_ld();
+            if (c == 0) ptx::tmem_ld32(s_col + 64, xa);
+            form(xb, c + 1);
           }
           float a0, a1;
-          ptx::f2_split(ptx::fadd2(sum2, sum2b), a0, a1);
+          ptx::f2_split(ptx::fadd2(sum2[0], sum2[1]), a0, a1);
           l_run += a0 + a1;
           ptx::tmem_wait_st();
         }
@@ -692,9 +710,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       }
       bool there = w == 0 ? ptx::mbar_wait(bar_o, ph0, status, abort_flag)
                           : ptx::mbar_wait(bar_o + 8, ph1, status, abort_flag);
-      if (two)
-        there = there && ptx::mbar_wait(bar_o + 8, ph1, status, abort_flag) &&
-                ptx::mbar_wait(bar_sf, phs, status, abort_flag);
+      if (two)   // (warpgroup 1's states first: behind them its accumulator's phase is this unit's)
+        there = there && ptx::mbar_wait(bar_sf, phs, status, abort_flag) &&
+                ptx::mbar_wait(bar_o + 8, ph1, status, abort_flag);
       ok = __all_sync(0xffffffffu, there);
       if (!ok) break;
       ptx::tc_fence_after();
@@ -709,9 +727,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       }
       const bool whole = S.j0 == 0 && S.j1 == S.nt;
       const size_t tok = (size_t)(S.Q.q0 + node);
-      const int head = S.g * a.G + (S.row0 + row) - node * a.G;
+      const int head = S.g * a.G + r % a.G;
       const size_t orow = tok * a.H + head;
-      const size_t slot = 2 * (size_t)cta + (seg_x > xb ? 1 : 0);
+      const size_t slot = 2 * (size_t)cta + (S.j0 == 0 ? 1 : 0);
       if (whole) {
         // (a NaN sum makes the row NaN; without a visible key it is 0)
         const float inv = l_p > 0.f ? 1.f / l_p : (l_p == 0.f ? 0.f : l_p);
@@ -787,56 +805,67 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 }
 
 // Merge of the cut units: with M = max m_x, O = sum 2^(m_x - M) O_x / sum 2^(m_x -
-// M) l_p_x, the LSE from the exact sums.  Block (cta, 32 rows): the unit that
-// begins in CTA `cta`'s piece; lane = row, warp = every eighth float4 of O.
+// M) l_p_x, the LSE from the exact sums.  Block (cta, 32 rows, 8 float4s of O): the
+// unit whose first tile lies in CTA `cta`'s piece; lane = row, warp = float4.  Latency
+// counts: eight partials are on their way at a time, in one pass with a running
+// maximum.
 constexpr int kMergeWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32)
 tree_merge_kernel(const Args a) {
-  constexpr int kEach = D / 4 / kMergeWarps;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = blockIdx.z * kMergeWarps + (threadIdx.x >> 5);
   const int row = blockIdx.y * 32 + lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 c0 = __ldcg(reinterpret_cast<const int4*>(a.cuts + blockIdx.x));
-  const int2 c1 = __ldcg(reinterpret_cast<const int2*>(a.cuts + blockIdx.x) + 2);
-  const int seq = c0.x, row0 = c0.y, rows = c0.z, g = c0.w, last = c1.x, late = c1.y;
-  if (last < 0 || row >= rows) return;
+  const int4 c1 = __ldcg(reinterpret_cast<const int4*>(a.cuts + blockIdx.x) + 1);
+  const int q0 = c0.x, rows = c0.y, head0 = c0.z, nt = c0.w, at0 = c1.x, cost = c1.y, total = c1.z, W = c1.w;
+  if (row >= rows) return;
   const int first = blockIdx.x;
-  const int q0 = __ldg(a.cu_q + seq);
-  auto slot_of = [&](int x) { return (size_t)(2 * x + (x == first ? late : 0)); };
-  float M = -INFINITY;
-#pragma unroll 4
-  for (int x = first; x <= last; ++x) M = fmaxf(M, __ldcg(a.part_s + slot_of(x) * a.row_cap + row).x);
-  float l = 0.f, lp = 0.f;
-  float4 y[kEach];
+  // the last tile's CTA: the one whose piece holds its position
+  const int last = (int)(((long long)(at0 + (nt - 1) * cost + 1) * W - 1) / total);
+  float M = -INFINITY, l = 0.f, lp = 0.f;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int x0 = first; x0 <= last; x0 += 8) {
+    float4 st[8], v[8];
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int x = first; x <= last; ++x) {
-    const float4 st = __ldcg(a.part_s + slot_of(x) * a.row_cap + row);
-    const float f = st.x == -INFINITY ? 0.f : ptx::ex2(st.x - M);
-    l += f * st.y;
-    lp += f * st.z;
-    const float4* po = a.part_o + (slot_of(x) * (D / 4) + warp * kEach) * a.row_cap + row;
+    for (int u = 0; u < 8; ++u) {
+      const int x = x0 + u;
+      st[u] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (x <= last) {
+        const size_t slot = 2 * (size_t)x + (x == first ? 1 : 0);
+        st[u] = __ldcg(a.part_s + slot * a.row_cap + row);
+        v[u] = __ldcg(a.part_o + (slot * (D / 4) + warp) * a.row_cap + row);
+      }
+    }
+    float top = M;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const float4 v = __ldcg(po + (size_t)i * a.row_cap);
-      y[i].x = fmaf(f, v.x, y[i].x);
-      y[i].y = fmaf(f, v.y, y[i].y);
-      y[i].z = fmaf(f, v.z, y[i].z);
-      y[i].w = fmaf(f, v.w, y[i].w);
+    for (int u = 0; u < 8; ++u) top = fmaxf(top, st[u].x);
+    const float f = M == -INFINITY ? 1.f : ptx::ex2(M - top);   // (what came before is 0 or NaN, or has an M)
+    M = top;
+    l *= f;
+    lp *= f;
+    y.x *= f;
+    y.y *= f;
+    y.z *= f;
+    y.w *= f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float g = st[u].x == -INFINITY ? 0.f : ptx::ex2(st[u].x - top);
+      l += g * st[u].y;
+      lp += g * st[u].z;
+      y.x = fmaf(g, v[u].x, y.x);
+      y.y = fmaf(g, v[u].y, y.y);
+      y.z = fmaf(g, v[u].z, y.z);
+      y.w = fmaf(g, v[u].w, y.w);
     }
   }
   const float inv = lp > 0.f ? 1.f / lp : (lp == 0.f ? 0.f : lp);
-  const int node = (row0 + row) / a.G;
-  const int head = g * a.G + row0 + row - node * a.G;
-  const size_t tok = (size_t)(q0 + node), orow = tok * a.H + head;
+  const int head = head0 + row % a.G;
+  const size_t tok = (size_t)(q0 + row / a.G), orow = tok * a.H + head;
   if (!FA_IN_BOUNDS(orow, (size_t)a.total_q * a.H, a.status)) return;
-  uint2* dst = reinterpret_cast<uint2*>(a.o + orow * D) + warp * kEach;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i)
-    dst[i] = make_uint2(ptx::pack_bf16x2(y[i].x * inv, y[i].y * inv),
-                        ptx::pack_bf16x2(y[i].z * inv, y[i].w * inv));
+  reinterpret_cast<uint2*>(a.o + orow * D)[warp] =
+      make_uint2(ptx::pack_bf16x2(y.x * inv, y.y * inv), ptx::pack_bf16x2(y.z * inv, y.w * inv));
   if (warp == 0 && a.lse != nullptr)
     a.lse[(size_t)head * a.total_q + tok] =
         l > 0.f ? (M + __log2f(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
@@ -852,20 +881,26 @@ constexpr size_t kCutBytes = (kCtas * sizeof(Cut) + 255) / 256 * 256;
 template <int D>
 cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream, const char** why) {
   using C = Cfg<D>;
-  CUtensorMap tmK, tmV;
-  // (dim, cache row); one box = 64 values of one page of one kv head
-  const uint64_t dims[2] = {(uint64_t)D, (uint64_t)p.num_pages * p.Hkv * kPage};
-  const uint64_t strides[1] = {(uint64_t)D * 2};
-  const uint32_t box[2] = {64, (uint32_t)kPage};
-  if (!make_tmap_bf16(&tmK, p.k_cache, 2, dims, strides, box) ||
-      !make_tmap_bf16(&tmV, p.v_cache, 2, dims, strides, box)) {
-    *why = "tensor map for the caches";
+  CUtensorMap tmQ, tmK, tmV;
+  // (value of 64, key of 8, piece of 64 values, group of 8 keys): one box = a page of
+  // one kv head, in the order of the tile
+  const uint64_t dims[4] = {64, 8, (uint64_t)C::kChunks, (uint64_t)p.num_pages * p.Hkv * 2};
+  const uint64_t strides[3] = {(uint64_t)D * 2, 128, (uint64_t)D * 16};
+  const uint32_t box[4] = {64, 8, (uint32_t)C::kChunks, 2};
+  const int G = p.H / p.Hkv, tile_nodes = kTile / G;
+  // (value of 64, head, node): one box = 64 values of a query tile
+  const uint64_t q_dims[3] = {(uint64_t)D, (uint64_t)p.H, (uint64_t)p.total_q};
+  const uint64_t q_strides[2] = {(uint64_t)D * 2, (uint64_t)p.H * D * 2};
+  const uint32_t q_box[3] = {64, (uint32_t)G, (uint32_t)tile_nodes};
+  if (!make_tmap_bf16(&tmQ, p.q, 3, q_dims, q_strides, q_box) ||
+      !make_tmap_bf16(&tmK, p.k_cache, 4, dims, strides, box) ||
+      !make_tmap_bf16(&tmV, p.v_cache, 4, dims, strides, box)) {
+    *why = "tensor map for the queries and caches";
     return cudaErrorInvalidValue;
   }
-  const int G = p.H / p.Hkv;
   Args a{static_cast<const __nv_bfloat16*>(p.q), p.block_table, p.seq_lens, p.cu_q, p.mask,
          static_cast<__nv_bfloat16*>(p.o), p.lse, p.num_seqs, p.total_q, p.max_q, p.words, p.H, p.Hkv, G,
-         p.num_pages, p.max_blocks, p.scale * kLog2e, skip_first_copy_for_tests(), p.status,
+         tile_nodes, p.num_pages, p.max_blocks, p.scale * kLog2e, skip_first_copy_for_tests(), p.status,
          nullptr, nullptr, nullptr, row_cap(p.max_q, G)};
   char* ws = static_cast<char*>(p.workspace);
   a.cuts = reinterpret_cast<Cut*>(ws);
@@ -874,7 +909,7 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream, const char** wh
   auto kernel = tree_attn_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e == cudaSuccess) {
-    kernel<<<kCtas, kThreads, C::kSmem, stream>>>(tmK, tmV, a);
+    kernel<<<kCtas, kThreads, C::kSmem, stream>>>(tmQ, tmK, tmV, a);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) {
@@ -883,7 +918,7 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream, const char** wh
   }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3(kCtas, (unsigned)(a.row_cap / 32));
+  cfg.gridDim = dim3(kCtas, (unsigned)(a.row_cap / 32), D / 4 / kMergeWarps);
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
