@@ -152,14 +152,15 @@ class _Torch:
 
 torch = _Torch()
 
-# Set by _bind_torch, before the e4m3 helpers' first check: the current stream of a device that is
-# known to be the current one, the current device once there are tensors on one, and the types of
-# the e4m3 cache's codes and scales.
-_current_raw_stream = _current_device = _CODES = _SCALES = None
+# Set by _bind_torch, before the e4m3 and tree helpers' first check: the current stream of a device
+# that is known to be the current one, the current device once there are tensors on one, the types of
+# the e4m3 cache's codes and scales, and torch's own under names that cost one look-up.
+_current_raw_stream = _current_device = _CODES = _SCALES = _I32 = _BF16 = _F32 = _empty = None
 
 
 def _bind_torch():
-    global _current_raw_stream, _current_device, _CODES, _SCALES
+    global _current_raw_stream, _current_device, _CODES, _SCALES, _I32, _BF16, _F32, _empty
+    _I32, _BF16, _F32, _empty = torch.int32, torch.bfloat16, torch.float32, torch.empty
     _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -738,37 +739,44 @@ def paged_prefill_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_l
 
 
 # ------------------------------------------------------ drafted token trees
+# (The checks are written out: these helpers run on every step of a serving loop, whose kernels take a
+# few us, where a loop over the tensors or a call for each of them would take twice as long.)
+def _refuse_ints(fn, device, *named):
+    _refuse(fn, device, *((name, t, (_I32,), shape) for name, t, shape in named))
+
+
 def tree_layout(parents, seq_lens, cu_seqlens, mask_words, stream=None):
     """parents [T] int32 (-1: child of the context) -> (mask [T,mask_words] int32 of ancestor bits,
     positions [T] int32)."""
     if stream is not None:
         with _given(stream):
             return tree_layout(parents, seq_lens, cu_seqlens, mask_words)
-    device = parents.get_device()
-    T, S = parents.shape[0], seq_lens.shape[0]
-    _check_tensors("tree_layout", device, ("parents", parents, torch.int32, (T,)),
-                   ("seq_lens", seq_lens, torch.int32, (S,)),
-                   ("cu_seqlens", cu_seqlens, torch.int32, (S + 1,)))
-    mask = torch.empty((T, mask_words), dtype=torch.int32, device=parents.device)
-    positions = torch.empty_like(parents)
-    lib = _lib or load()
-    _check(lib.fa_tree_layout(parents.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(),
-                              mask.data_ptr(), positions.data_ptr(), S, T, mask_words,
-                              _raw_stream(device)))
-    return mask, positions
-
-
-def _raw_stream(device):
     if _CODES is None:
         _bind_torch()
-    return _current_raw_stream(device)
+    i32, device = _I32, parents.get_device()
+    T, S = parents.shape[0], seq_lens.shape[0]
+    if not (parents.dtype is i32 and seq_lens.dtype is i32 and cu_seqlens.dtype is i32
+            and parents.dim() == 1 and seq_lens.dim() == 1 and cu_seqlens.shape == (S + 1,)
+            and seq_lens.get_device() == device and cu_seqlens.get_device() == device
+            and parents.is_contiguous() and seq_lens.is_contiguous() and cu_seqlens.is_contiguous()
+            and device >= 0 and device == _current_device()):
+        _refuse_ints("tree_layout", device, ("parents", parents, (T,)), ("seq_lens", seq_lens, (S,)),
+                     ("cu_seqlens", cu_seqlens, (S + 1,)))
+    mask = _empty((T, mask_words), dtype=i32, device=parents.device)
+    positions = torch.empty_like(parents)
+    lib = _lib or load()
+    rc = lib.fa_tree_layout(parents.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(), mask.data_ptr(),
+                            positions.data_ptr(), S, T, mask_words, _current_raw_stream(device))
+    if rc:
+        _check(rc)
+    return mask, positions
 
 
 def _heads_stride(fn, name, t, shape, device):
     """Token stride of bf16 rows [T,heads,d] whose heads are dense."""
     st = t.stride()
-    if t.shape != shape or st[2] != 1 or (shape[1] > 1 and st[1] != shape[2]) or \
-            t.dtype is not torch.bfloat16 or t.get_device() != device:
+    if t.shape != shape or st[2] != 1 or (st[1] != shape[2] and shape[1] > 1) or t.dtype is not _BF16 or \
+            t.get_device() != device:
         raise FaError(FA_ERR_INVALID_ARG, f"{fn}: {name} is {t.dtype} on {t.device} of shape "
                                           f"{tuple(t.shape)} and strides {st}, wanted bf16 "
                                           f"{tuple(shape)} with dense heads")
@@ -776,20 +784,33 @@ def _heads_stride(fn, name, t, shape, device):
 
 
 def _rotary(fn, device, T, d, q_weight, k_weight, cos_sin, positions, sections):
-    """(rot_dim, axes, rows of the table, host sections) of a rotation, its tensors checked."""
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _check_rows(fn, device, name, w, torch.bfloat16, (d,))
+    """Addresses of the weights, the table and the positions, and (rot_dim, axes, rows of the table, host
+    sections) of the rotation; its tensors checked."""
+    qw = kw = cs = at = None
+    if q_weight is not None:
+        if not (q_weight.dtype is _BF16 and q_weight.shape == (d,) and q_weight.get_device() == device
+                and q_weight.is_contiguous()):
+            _refuse(fn, device, ("q_weight", q_weight, (_BF16,), (d,)))
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        if not (k_weight.dtype is _BF16 and k_weight.shape == (d,) and k_weight.get_device() == device
+                and k_weight.is_contiguous()):
+            _refuse(fn, device, ("k_weight", k_weight, (_BF16,), (d,)))
+        kw = k_weight.data_ptr()
     if cos_sin is None:
-        return 0, 1, 0, None
-    if cos_sin.dim() != 3 or positions is None or positions.dim() != 2:
+        return qw, kw, None, None, 0, 1, 0, None
+    if positions is None or cos_sin.dim() != 3 or positions.dim() != 2:
         raise FaError(FA_ERR_INVALID_ARG, f"{fn}: a rotation takes cos_sin [positions,rot_dim/2,2] and "
                                           "positions [axes,T]")
-    rows, half = cos_sin.shape[:2]
-    axes = positions.shape[0]
-    _check_rows(fn, device, "cos_sin", cos_sin, torch.float32, (rows, half, 2))
-    _check_rows(fn, device, "positions", positions, torch.int32, (axes, T))
-    return 2 * half, axes, rows, _sections(sections, axes)
+    rows, half, two = cos_sin.shape
+    axes, tokens = positions.shape
+    if not (cos_sin.dtype is _F32 and positions.dtype is _I32 and two == 2 and tokens == T
+            and cos_sin.get_device() == device and positions.get_device() == device
+            and cos_sin.is_contiguous() and positions.is_contiguous()):
+        _refuse(fn, device, ("cos_sin", cos_sin, (_F32,), (rows, half, 2)),
+                ("positions", positions, (_I32,), (axes, T)))
+    return qw, kw, cos_sin.data_ptr(), positions.data_ptr(), 2 * half, axes, rows, \
+        None if sections is None else _sections(sections, axes)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, sections=None,
@@ -799,39 +820,47 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, section
     if stream is not None:
         with _given(stream):
             return qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, sections, interleaved)
+    if _CODES is None:
+        _bind_torch()
     fn = "qk_norm_rope"
     device = q.get_device()
-    T, H, d = q.shape
-    Hkv = k.shape[1]
-    if device != torch.cuda.current_device():
+    T, H, d = shape = q.shape
+    k_shape = (T, k.shape[1], d)
+    if device < 0 or device != _current_device():
         _refuse(fn, device)
-    qs, ks = (_heads_stride(fn, "q", q, (T, H, d), device), _heads_stride(fn, "k", k, (T, Hkv, d), device))
-    rot, axes, rows, host = _rotary(fn, device, T, d, q_weight, k_weight, cos_sin, positions, sections)
-    q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
-    k_out = torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=q.device)
+    qs, ks = _heads_stride(fn, "q", q, shape, device), _heads_stride(fn, "k", k, k_shape, device)
+    qw, kw, cs, at, rot, axes, rows, host = _rotary(fn, device, T, d, q_weight, k_weight, cos_sin, positions,
+                                                    sections)
+    q_out = _empty(shape, dtype=_BF16, device=q.device)
+    k_out = _empty(k_shape, dtype=_BF16, device=q.device)
     lib = _lib or load()
-    _check(lib.fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), _p(q_weight), _p(k_weight), _p(cos_sin),
-                               _p(positions), q_out.data_ptr(), k_out.data_ptr(), T, H, Hkv, d, qs, ks,
-                               rot, 1 if interleaved else 0, axes, host, rows, eps, _raw_stream(device)))
+    rc = lib.fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), qw, kw, cs, at, q_out.data_ptr(), k_out.data_ptr(), T,
+                             H, k_shape[1], d, qs, ks, rot, 1 if interleaved else 0, axes, host, rows, eps,
+                             _current_raw_stream(device))
+    if rc:
+        _check(rc)
     return q_out, k_out
 
 
 def _check_paged(fn, device, kc, vc, bt, sl, cu):
-    """The bf16 paged cache's tensors.  (Written out: it runs on every call of the serving path.)"""
-    shape, table = kc.shape, bt.shape
+    """The bf16 paged cache's tensors; the shapes of the cache and of the block table."""
+    if _CODES is None:
+        _bind_torch()
+    shape, table, kind, i32 = kc.shape, bt.shape, _BF16, _I32
     if len(shape) != 4 or len(table) != 2:
         raise FaError(FA_ERR_INVALID_ARG, f"{fn}: k_cache has shape {tuple(shape)}, block_table "
                                           f"{tuple(table)}, wanted 4 and 2 dimensions")
-    kind, i32, S = torch.bfloat16, torch.int32, table[0]
+    S = table[0]
     if not (kc.dtype is kind and vc.dtype is kind and bt.dtype is i32 and sl.dtype is i32
             and cu.dtype is i32 and vc.shape == shape and sl.shape == (S,) and cu.shape == (S + 1,)
             and kc.get_device() == device and vc.get_device() == device and bt.get_device() == device
             and sl.get_device() == device and cu.get_device() == device and kc.is_contiguous()
             and vc.is_contiguous() and bt.is_contiguous() and sl.is_contiguous()
-            and cu.is_contiguous() and device >= 0 and device == torch.cuda.current_device()):
+            and cu.is_contiguous() and device >= 0 and device == _current_device()):
         _refuse(fn, device, ("k_cache", kc, (kind,), shape), ("v_cache", vc, (kind,), shape),
                 ("block_table", bt, (i32,), table), ("seq_lens", sl, (i32,), (S,)),
                 ("cu_seqlens", cu, (i32,), (S + 1,)))
+    return shape, table
 
 
 def paged_qkv_write(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_cache, block_table,
@@ -843,21 +872,23 @@ def paged_qkv_write(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_
                                    block_table, seq_lens, cu_seqlens, eps, sections, interleaved)
     fn = "paged_qkv_write"
     device = q.get_device()
-    _check_paged(fn, device, k_cache, v_cache, block_table, seq_lens, cu_seqlens)
-    P, Hkv, page, d = k_cache.shape
-    S, max_blocks = block_table.shape
-    T, H = q.shape[:2]
-    qs, ks, vs = (_heads_stride(fn, "q", q, (T, H, d), device),
-                  _heads_stride(fn, "k", k, (T, Hkv, d), device),
-                  _heads_stride(fn, "v", v, (T, Hkv, d), device))
-    rot, axes, rows, host = _rotary(fn, device, T, d, q_weight, k_weight, cos_sin, positions, sections)
-    q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+    (P, Hkv, page, d), (S, max_blocks) = _check_paged(fn, device, k_cache, v_cache, block_table, seq_lens,
+                                                      cu_seqlens)
+    T, H, _ = q.shape
+    shape, kv_shape = (T, H, d), (T, Hkv, d)
+    qs, ks, vs = (_heads_stride(fn, "q", q, shape, device), _heads_stride(fn, "k", k, kv_shape, device),
+                  _heads_stride(fn, "v", v, kv_shape, device))
+    qw, kw, cs, at, rot, axes, rows, host = _rotary(fn, device, T, d, q_weight, k_weight, cos_sin, positions,
+                                                    sections)
+    q_out = _empty(shape, dtype=_BF16, device=q.device)
     lib = _lib or load()
-    _check(lib.fa_paged_qkv_write(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), _p(q_weight), _p(k_weight), _p(cos_sin), _p(positions),
-        q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-        seq_lens.data_ptr(), cu_seqlens.data_ptr(), S, T, H, Hkv, d, qs, ks, vs, rot,
-        1 if interleaved else 0, axes, host, rows, eps, page, P, max_blocks, _raw_stream(device)))
+    rc = lib.fa_paged_qkv_write(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), qw, kw, cs, at, q_out.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(), S, T, H, Hkv, d,
+        qs, ks, vs, rot, 1 if interleaved else 0, axes, host, rows, eps, page, P, max_blocks,
+        _current_raw_stream(device))
+    if rc:
+        _check(rc)
     return q_out
 
 
@@ -877,49 +908,54 @@ def paged_tree_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_
                                         max_seqlen_q, mask, scale, workspace)
     fn = "paged_tree_attention"
     device = q.get_device()
-    _check_paged(fn, device, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q)
-    P, Hkv, page, d = k_cache.shape
-    S, max_blocks = block_table.shape
-    T, H = q.shape[:2]
+    (P, Hkv, page, d), (S, max_blocks) = _check_paged(fn, device, k_cache, v_cache, block_table, seq_lens,
+                                                      cu_seqlens_q)
+    T, H, width = q.shape
     words = mask.shape[-1]
-    _check_rows(fn, device, "q", q, torch.bfloat16, (T, H, d))
-    _check_rows(fn, device, "mask", mask, torch.int32, (T, words))
+    if not (q.dtype is _BF16 and mask.dtype is _I32 and width == d and mask.shape == (T, words)
+            and mask.get_device() == device and q.is_contiguous() and mask.is_contiguous()):
+        _refuse(fn, device, ("q", q, (_BF16,), (T, H, d)), ("mask", mask, (_I32,), (T, words)))
     if workspace is None:   # (a caller's own is sized for the caller's bound)
         max_seqlen_q = min(max_seqlen_q, T)
-        workspace = torch.empty(_tree_workspace(S, max_seqlen_q, H, Hkv, d), dtype=torch.uint8,
-                                device=q.device)
+        size = _tree_workspace(S, max_seqlen_q, H, Hkv, d)
+        workspace = _empty(size, dtype=torch.uint8, device=q.device)
     elif workspace.get_device() != device or not workspace.is_contiguous():
         raise FaError(FA_ERR_WORKSPACE, f"{fn}: the workspace is on {workspace.device} with strides "
                                         f"{workspace.stride()}")
+    else:
+        size = workspace.nbytes
     o = torch.empty_like(q)
-    lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+    lse = _empty((H, T), dtype=_F32, device=q.device)
     lib = _lib or load()
-    _check(lib.fa_paged_tree_attention(
+    rc = lib.fa_paged_tree_attention(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
         cu_seqlens_q.data_ptr(), mask.data_ptr(), o.data_ptr(), lse.data_ptr(), S, T, max_seqlen_q, words,
-        H, Hkv, d, page, P, max_blocks, scale, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _raw_stream(device)))
+        H, Hkv, d, page, P, max_blocks, scale, workspace.data_ptr(), size, _current_raw_stream(device))
+    if rc:
+        _check(rc)
     return o, lse
 
 
 def _check_layers(fn, device, kc, vc, ks, vs):
-    """Caches [P,Hkv,16,d], or [layers,P,Hkv,16,d], bf16 or (with scales) e4m3; their layers."""
+    """Caches [P,Hkv,16,d], or [layers,P,Hkv,16,d], bf16 or (with scales) e4m3; their layers and a layer's
+    shape."""
     if _CODES is None:
         _bind_torch()
     shape = kc.shape
     if len(shape) not in (4, 5) or (ks is None) != (vs is None):
         raise FaError(FA_ERR_INVALID_ARG, f"{fn}: k_cache has shape {tuple(shape)}, wanted 4 dimensions, or "
                                           "5 with layers first, and both scales or none")
-    kinds = (torch.bfloat16,) if ks is None else _CODES
-    named = [("k_cache", kc, kinds, shape), ("v_cache", vc, kinds, shape)]
-    if ks is not None:
-        named += [("k_scale", ks, _SCALES, shape[:-1]), ("v_scale", vs, _SCALES, shape[:-1])]
-    for _, t, kind, want in named:
-        if t.dtype not in kind or t.shape != want or t.get_device() != device or not t.is_contiguous():
-            _refuse(fn, device, *named)
-    if device != _current_device():
-        _refuse(fn, device)
-    return shape[0] if len(shape) == 5 else 1
+    ok = vc.shape == shape and kc.is_contiguous() and vc.is_contiguous() and vc.get_device() == device and \
+        device >= 0 and device == _current_device()
+    if ks is None:
+        if not (ok and kc.dtype is _BF16 and vc.dtype is _BF16):
+            _refuse(fn, device, ("k_cache", kc, (_BF16,), shape), ("v_cache", vc, (_BF16,), shape))
+    elif not (ok and kc.dtype in _CODES and vc.dtype in _CODES and ks.dtype in _SCALES and vs.dtype in _SCALES
+              and ks.shape == shape[:-1] and vs.shape == shape[:-1] and ks.is_contiguous()
+              and vs.is_contiguous() and ks.get_device() == device and vs.get_device() == device):
+        _refuse(fn, device, ("k_cache", kc, _CODES, shape), ("v_cache", vc, _CODES, shape),
+                ("k_scale", ks, _SCALES, shape[:-1]), ("v_scale", vs, _SCALES, shape[:-1]))
+    return (1, *shape) if len(shape) == 4 else shape
 
 
 def paged_kv_accept(k_cache, v_cache, block_table, seq_lens, cu_seqlens, path, path_lens, k_scale=None,
@@ -932,21 +968,29 @@ def paged_kv_accept(k_cache, v_cache, block_table, seq_lens, cu_seqlens, path, p
                                    k_scale, v_scale)
     fn = "paged_kv_accept"
     device = k_cache.get_device()
-    layers = _check_layers(fn, device, k_cache, v_cache, k_scale, v_scale)
-    P, Hkv, page, d = k_cache.shape[-4:]
+    layers, P, Hkv, page, d = _check_layers(fn, device, k_cache, v_cache, k_scale, v_scale)
     S, max_blocks = block_table.shape
-    max_path = path.shape[-1]
-    for name, t, shape in (("block_table", block_table, (S, max_blocks)), ("seq_lens", seq_lens, (S,)),
-                           ("cu_seqlens", cu_seqlens, (S + 1,)), ("path", path, (S, max_path)),
-                           ("path_lens", path_lens, (S,))):
-        _check_rows(fn, device, name, t, torch.int32, shape)
+    max_path, i32 = path.shape[-1], _I32
+    if not (block_table.dtype is i32 and seq_lens.dtype is i32 and cu_seqlens.dtype is i32
+            and path.dtype is i32 and path_lens.dtype is i32 and seq_lens.shape == (S,)
+            and cu_seqlens.shape == (S + 1,) and path.shape == (S, max_path) and path_lens.shape == (S,)
+            and block_table.get_device() == device and seq_lens.get_device() == device
+            and cu_seqlens.get_device() == device and path.get_device() == device
+            and path_lens.get_device() == device and block_table.is_contiguous()
+            and seq_lens.is_contiguous() and cu_seqlens.is_contiguous() and path.is_contiguous()
+            and path_lens.is_contiguous()):
+        _refuse_ints(fn, device, ("block_table", block_table, (S, max_blocks)), ("seq_lens", seq_lens, (S,)),
+                     ("cu_seqlens", cu_seqlens, (S + 1,)), ("path", path, (S, max_path)),
+                     ("path_lens", path_lens, (S,)))
     new_lens = torch.empty_like(seq_lens)
     lib = _lib or load()
-    _check(lib.fa_paged_kv_accept(
-        k_cache.data_ptr(), v_cache.data_ptr(), _p(k_scale), _p(v_scale), block_table.data_ptr(),
-        seq_lens.data_ptr(), cu_seqlens.data_ptr(), path.data_ptr(), path_lens.data_ptr(),
-        new_lens.data_ptr(), S, 0x7fffffff, max_path, layers, Hkv, d, page, P, max_blocks,
-        _raw_stream(device)))
+    rc = lib.fa_paged_kv_accept(
+        k_cache.data_ptr(), v_cache.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
+        None if v_scale is None else v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        cu_seqlens.data_ptr(), path.data_ptr(), path_lens.data_ptr(), new_lens.data_ptr(), S, 0x7fffffff,
+        max_path, layers, Hkv, d, page, P, max_blocks, _current_raw_stream(device))
+    if rc:
+        _check(rc)
     return new_lens
 
 
@@ -955,14 +999,19 @@ def paged_copy_pages(k_cache, v_cache, pairs, k_scale=None, v_scale=None, stream
     [layers,P,Hkv,16,d], and of their scales."""
     fn = "paged_copy_pages"
     device = k_cache.get_device()
-    layers = _check_layers(fn, device, k_cache, v_cache, k_scale, v_scale)
-    P, Hkv, page, d = k_cache.shape[-4:]
+    layers, P, Hkv, page, d = _check_layers(fn, device, k_cache, v_cache, k_scale, v_scale)
     N = pairs.shape[0]
-    _check_rows(fn, device, "pairs", pairs, torch.int32, (N, 2))
+    if not (pairs.dtype is _I32 and pairs.shape == (N, 2) and pairs.get_device() == device
+            and pairs.is_contiguous()):
+        _refuse_ints(fn, device, ("pairs", pairs, (N, 2)))
     lib = _lib or load()
-    _check(lib.fa_paged_copy_pages(k_cache.data_ptr(), v_cache.data_ptr(), _p(k_scale), _p(v_scale),
-                                   pairs.data_ptr(), N, layers, Hkv, d, page, P,
-                                   _raw_stream(device) if stream is None else _stream(stream)))
+    rc = lib.fa_paged_copy_pages(k_cache.data_ptr(), v_cache.data_ptr(),
+                                 None if k_scale is None else k_scale.data_ptr(),
+                                 None if v_scale is None else v_scale.data_ptr(), pairs.data_ptr(), N, layers,
+                                 Hkv, d, page, P,
+                                 _current_raw_stream(device) if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def split_combine(part_m, part_l, part_o, stream=None):
