@@ -4,13 +4,18 @@
 //   y = x / sqrt(mean(x^2) + eps) * w    over the d values of a head
 //   (a, b) -> (a c - b s, b c + a s)     for the pairs of the first rot_dim values
 //
-// A row is 2 d bytes read and 2 d written, and the d values need two reductions'
-// worth of nothing else, so the pass is bound by memory traffic.  D / 8 lanes
-// share a row; a lane holds four rotary pairs of it as two pieces of four values:
-// the halves' pairs (p, p + rot_dim/2) for p = 4 l .. 4 l + 3, or eight values in
-// a row when pairs are neighbours, so both values of a pair are in one lane and
-// only the sum of squares crosses lanes.  The table's entries of a lane's pairs
-// serve every row of the token that the warp handles.
+// A row is 2 d bytes read and 2 d written.  D / 8 lanes share a row; a lane holds
+// four rotary pairs of it: values 4 l .. 4 l + 3 and as many rot_dim / 2 further on,
+// or eight values in a row when pairs are neighbours, so both values of a pair are
+// in one lane and only the sum of squares crosses lanes.  Norm weight, cos and sin
+// of a value are the same in every row of the token: their products are formed once
+// (y_i = (x_i C_i + x_partner S_i) / rms), which leaves 3 packed fp32 instructions for
+// two values.  That matters: with the weights, cos and sin applied one after the
+// other, row by row, the pass was bound by instructions (126 us for 21 300 tokens of
+// 32 + 8 + 8 heads, d = 128).
+//
+// Where a token's rows go (a search of cu_seqlens, then the block table: four
+// dependent loads) is looked up behind its first rows' loads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -23,6 +28,10 @@ namespace fa {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kSteps = 4;     // rows that a lane works on
+// Blocks an SM: at 5 nothing is spilled.  us for 21 300 tokens (see above): 4 96, 5 88,
+// 6 99; 2 steps at 8 blocks 115, 3 steps at 6 97.
+constexpr int kBlocks = 5;
 
 __device__ __forceinline__ uint2 ld_row(const void* p) {
   uint2 v;   // (not .nc: q may be its own output)
@@ -30,49 +39,64 @@ __device__ __forceinline__ uint2 ld_row(const void* p) {
   return v;
 }
 
-__device__ __forceinline__ void widen(const uint2& w, float (&x)[4]) {
-  x[0] = __uint_as_float(w.x << 16);
-  x[1] = __uint_as_float(w.x & 0xffff0000u);
-  x[2] = __uint_as_float(w.y << 16);
-  x[3] = __uint_as_float(w.y & 0xffff0000u);
+// The two bf16 values of a word as packed fp32.
+__device__ __forceinline__ uint64_t widen(uint32_t w) {
+  return ptx::f2_bits(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// A warp's share: kSteps times 32 / (D / 8) rows of one token, of its q heads,
-// then its k heads, then (paged) its v heads.
-template <int D, bool PAGED, int kSteps>
-__global__ void __launch_bounds__(kWarps * 32)
-qkv_rows_kernel(const QkvRowsParams p) {
+__device__ __forceinline__ uint64_t swapped(uint64_t v) {
+  float lo, hi;
+  ptx::f2_split(v, lo, hi);
+  return ptx::f2_bits(hi, lo);
+}
+
+__device__ __forceinline__ uint32_t narrow(uint64_t v) {
+  float lo, hi;
+  ptx::f2_split(v, lo, hi);
+  return ptx::pack_bf16x2(lo, hi);
+}
+
+// A group is up to kSteps * 32 / (D / 8) heads of q, of k or of v of one token; a
+// token's groups are shared out over `parts` warps.  A warp's next group is on its
+// way while it works on one.
+template <int D, bool PAGED, bool INTER>
+__global__ void __launch_bounds__(kWarps * 32, kBlocks)
+qkv_rows_kernel(const QkvRowsParams p, int parts) {
   constexpr int kLanes = D / 8;
   constexpr int kRows = 32 / kLanes;
+  constexpr int kEach = kSteps * kRows;
   const int lane = threadIdx.x & 31;
   const int sub = lane / kLanes, l = lane % kLanes;
-  const int heads = p.H + (PAGED ? 2 : 1) * p.Hkv;
-  const int shares = (heads + kSteps * kRows - 1) / (kSteps * kRows);
-  const uint32_t item = blockIdx.x * (uint32_t)kWarps + (threadIdx.x >> 5);   // below 2^32
-  const uint32_t tok = item / (uint32_t)shares;
+  const uint32_t wid = blockIdx.x * (uint32_t)kWarps + (threadIdx.x >> 5);   // below 2^32
+  const uint32_t tok = wid / (uint32_t)parts;
   if (tok >= (uint32_t)p.total) return;
-  const int t = (int)tok;
-  const int r0 = (int)(item - tok * (uint32_t)shares) * (kSteps * kRows) + sub;
-  // this lane's two pieces of a row
+  const int t = (int)tok, part = (int)(wid - tok * (uint32_t)parts);
+  const int q_groups = (p.H + kEach - 1) / kEach, k_groups = (p.Hkv + kEach - 1) / kEach;
+  const int groups = q_groups + (PAGED ? 2 : 1) * k_groups;
+  const int g0 = (int)((long long)part * groups / parts), g1 = (int)((long long)(part + 1) * groups / parts);
   const int rl = p.rot_dim / 8;                    // lanes whose values are rotated
-  const int off_a = l < rl && !p.interleaved ? 4 * l : 8 * l;
-  const int off_b = l < rl && !p.interleaved ? 4 * l + p.rot_dim / 2 : 8 * l + 4;
-
-  uint2 a[kSteps], b[kSteps];
+  const int off_a = l < rl && !INTER ? 4 * l : 8 * l;
+  const int off_b = l < rl && !INTER ? 4 * l + p.rot_dim / 2 : 8 * l + 4;
+  const bool all = rl == kLanes;                   // every lane's are
+  auto kind_of = [&](int g) { return g < q_groups ? 0 : g < q_groups + k_groups ? 1 : 2; };   // q, k, v
+  auto head_of = [&](int g) { return (g - (g < q_groups ? 0 : g < q_groups + k_groups ? q_groups : q_groups + k_groups)) * kEach + sub; };
+  uint2 a[kSteps], b[kSteps], na[kSteps], nb[kSteps];
+  auto fetch = [&](int g) __attribute__((always_inline)) {
+    const int kind = kind_of(g), heads = kind == 0 ? p.H : p.Hkv, h0 = head_of(g);
+    const __nv_bfloat16* src = (kind == 0 ? static_cast<const __nv_bfloat16*>(p.q) + t * p.q_stride
+                                : kind == 1 ? static_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride
+                                            : static_cast<const __nv_bfloat16*>(p.v) + t * p.v_stride) + h0 * D;
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int row = r0 + i * kRows;
-    const __nv_bfloat16* src;
-    if (row < p.H) src = static_cast<const __nv_bfloat16*>(p.q) + t * p.q_stride + row * D;
-    else if (row < p.H + p.Hkv) src = static_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride + (row - p.H) * D;
-    else src = static_cast<const __nv_bfloat16*>(p.v) + t * p.v_stride + (row - p.H - p.Hkv) * D;
-    a[i] = b[i] = make_uint2(0u, 0u);
-    if (row < heads) {
-      a[i] = ld_row(src + off_a);
-      b[i] = ld_row(src + off_b);
+    for (int e = 0; e < kSteps; ++e) {
+      na[e] = nb[e] = make_uint2(0u, 0u);
+      if (h0 + e * kRows < heads) {
+        na[e] = ld_row(src + e * kRows * D + off_a);
+        nb[e] = ld_row(src + e * kRows * D + off_b);
+      }
     }
-  }
-  // cos and sin of the lane's pairs 4 l .. 4 l + 3
+  };
+  fetch(g0);
+  // positions, cos and sin of the lane's pairs, the token's slot
   float c[4], s[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -101,109 +125,120 @@ qkv_rows_kernel(const QkvRowsParams p) {
       }
     }
   }
-  if (bad) {   // (the same in every lane)
-    if (lane == 0) atomicExch(p.status, kDevInvalidArg);
-    return;
-  }
   long long slot = 0;
-  if constexpr (PAGED) {
+  if constexpr (PAGED)
     slot = token_slot(t, p.cu, p.seq_lens, p.block_table, p.num_seqs, p.total, p.max_blocks, p.num_pages,
                       p.status, lane);
-    if (slot < 0) return;
+  if (bad || slot < 0) {   // (the same in every lane)
+    if (slot >= 0 && lane == 0) atomicExch(p.status, kDevInvalidArg);
+    return;
   }
-  uint2 wqa = make_uint2(0u, 0u), wqb = wqa, wka = wqa, wkb = wqa;
-  if (p.q_weight != nullptr) {
-    wqa = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q_weight) + off_a));
-    wqb = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q_weight) + off_b));
-  }
-  if (p.k_weight != nullptr) {
-    wka = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.k_weight) + off_a));
-    wkb = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.k_weight) + off_b));
-  }
+  uint64_t C[4], S[4];
+  int made = -1;           // the kind that C and S are of
+  bool norm = false;
+  for (int g = g0; g < g1; ++g) {
+    const int kind = kind_of(g), heads = kind == 0 ? p.H : p.Hkv, h0 = head_of(g);
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int row = r0 + i * kRows;
-    const bool is_q = row < p.H, is_v = row >= p.H + p.Hkv;
-    float xa[4], xb[4];
-    widen(a[i], xa);
-    widen(b[i], xb);
-    float sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sum = fmaf(xa[e], xa[e], fmaf(xb[e], xb[e], sum));
-#pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    const bool norm = is_q ? p.q_weight != nullptr : p.k_weight != nullptr;
-    if (norm) {
-      const float r = rsqrtf(sum * (1.f / D) + p.eps);
-      float wa[4], wb[4];
-      widen(is_q ? wqa : wka, wa);
-      widen(is_q ? wqb : wkb, wb);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        xa[e] = xa[e] * r * wa[e];
-        xb[e] = xb[e] * r * wb[e];
-      }
+    for (int e = 0; e < kSteps; ++e) {
+      a[e] = na[e];
+      b[e] = nb[e];
     }
-    float ya[4], yb[4];
-    if (l >= rl) {   // not rotated (times 0 would turn an inf into a NaN)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        ya[e] = xa[e];
-        yb[e] = xb[e];
-      }
-    } else if (p.interleaved) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        ya[2 * e] = xa[2 * e] * c[e] - xa[2 * e + 1] * s[e];
-        ya[2 * e + 1] = xa[2 * e + 1] * c[e] + xa[2 * e] * s[e];
-        yb[2 * e] = xb[2 * e] * c[e + 2] - xb[2 * e + 1] * s[e + 2];
-        yb[2 * e + 1] = xb[2 * e + 1] * c[e + 2] + xb[2 * e] * s[e + 2];
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        ya[e] = xa[e] * c[e] - xb[e] * s[e];
-        yb[e] = xb[e] * c[e] + xa[e] * s[e];
-      }
-    }
-    uint2 oa = make_uint2(ptx::pack_bf16x2(ya[0], ya[1]), ptx::pack_bf16x2(ya[2], ya[3]));
-    uint2 ob = make_uint2(ptx::pack_bf16x2(yb[0], yb[1]), ptx::pack_bf16x2(yb[2], yb[3]));
-    if ((PAGED && is_v) || (!norm && l >= rl)) {   // as they are
-      oa = a[i];
-      ob = b[i];
-    }
-    if (row >= heads) continue;
+    if (g + 1 < g1) fetch(g + 1);
+    // output row of head h: first + h * step
     __nv_bfloat16* dst;
-    bool in = true;
-    if (is_q) {
-      const size_t at = (size_t)t * p.H + row;
-      in = FA_IN_BOUNDS(at, (size_t)p.total * p.H, p.status);
-      dst = static_cast<__nv_bfloat16*>(p.q_out) + at * D;
-    } else if constexpr (PAGED) {
-      const int h = row - p.H - (is_v ? p.Hkv : 0);
-      const size_t at = (size_t)((slot / kPage * p.Hkv + h) * kPage + slot % kPage);
-      in = FA_IN_BOUNDS(at, (size_t)p.num_pages * p.Hkv * kPage, p.status);
-      dst = static_cast<__nv_bfloat16*>(is_v ? p.v_cache : p.k_cache) + at * D;
+    size_t first, limit;
+    int step = 1;
+    if (kind == 0 || !PAGED) {
+      dst = static_cast<__nv_bfloat16*>(kind == 0 ? p.q_out : p.k_out);
+      first = (size_t)t * heads;
+      limit = (size_t)p.total * heads;
     } else {
-      const size_t at = (size_t)t * p.Hkv + (row - p.H);
-      in = FA_IN_BOUNDS(at, (size_t)p.total * p.Hkv, p.status);
-      dst = static_cast<__nv_bfloat16*>(p.k_out) + at * D;
+      dst = static_cast<__nv_bfloat16*>(kind == 1 ? p.k_cache : p.v_cache);
+      first = (size_t)(slot / kPage * p.Hkv * kPage + slot % kPage);
+      limit = (size_t)p.num_pages * p.Hkv * kPage;
+      step = kPage;
     }
-    if (in) {
-      *reinterpret_cast<uint2*>(dst + off_a) = oa;
-      *reinterpret_cast<uint2*>(dst + off_b) = ob;
+    if (kind < 2 && kind != made) {
+      made = kind;
+      const __nv_bfloat16* weight = static_cast<const __nv_bfloat16*>(kind == 0 ? p.q_weight : p.k_weight);
+      norm = weight != nullptr;
+      float w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = 1.f;
+      if (norm) {
+        const uint2 wa = __ldg(reinterpret_cast<const uint2*>(weight + off_a));
+        const uint2 wb = __ldg(reinterpret_cast<const uint2*>(weight + off_b));
+        ptx::f2_split(widen(wa.x), w[0], w[1]);
+        ptx::f2_split(widen(wa.y), w[2], w[3]);
+        ptx::f2_split(widen(wb.x), w[4], w[5]);
+        ptx::f2_split(widen(wb.y), w[6], w[7]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (INTER) {   // values 2 e and 2 e + 1 are a pair
+          C[e] = ptx::f2_bits(w[2 * e] * c[e], w[2 * e + 1] * c[e]);
+          S[e] = ptx::f2_bits(-w[2 * e + 1] * s[e], w[2 * e] * s[e]);
+        } else {                 // values e and 4 + e are
+          const int x = 2 * (e & 1);
+          C[e] = ptx::f2_bits(w[2 * e] * c[x], w[2 * e + 1] * c[x + 1]);
+          S[e] = e < 2 ? ptx::f2_bits(-w[4 + x] * s[x], -w[5 + x] * s[x + 1])
+                       : ptx::f2_bits(w[x] * s[x], w[x + 1] * s[x + 1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kSteps; ++e) {
+      const int h = h0 + e * kRows;
+      uint32_t y[4] = {a[e].x, a[e].y, b[e].x, b[e].y};
+      if (!PAGED || kind < 2) {
+        const uint64_t x[4] = {widen(y[0]), widen(y[1]), widen(y[2]), widen(y[3])};
+        float r = 1.f;
+        if (norm) {
+          float lo, hi;
+          ptx::f2_split(
+              ptx::ffma2(x[0], x[0], ptx::ffma2(x[1], x[1], ptx::ffma2(x[2], x[2], ptx::fmul2(x[3], x[3])))), lo, hi);
+          float sum = lo + hi;
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          r = rsqrtf(sum * (1.f / D) + p.eps);
+        }
+        const uint64_t r2 = ptx::f2_bits(r, r);
+        uint64_t z[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[k] = ptx::fmul2(x[k], r2);
+        if (norm || l < rl) {          // (the rest as they are)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint64_t v = ptx::fmul2(z[k], C[k]);
+            if (all || l < rl)         // (elsewhere an inf times S = 0 would be a NaN)
+              v = ptx::ffma2(INTER ? swapped(z[k]) : z[k ^ 2], S[k], v);
+            y[k] = narrow(v);
+          }
+        }
+      }
+      const size_t row = first + (size_t)h * step;
+      if (h < heads && FA_IN_BOUNDS(row, limit, p.status)) {
+        *reinterpret_cast<uint2*>(dst + row * D + off_a) = make_uint2(y[0], y[1]);
+        *reinterpret_cast<uint2*>(dst + row * D + off_b) = make_uint2(y[2], y[3]);
+      }
     }
   }
 }
 
 template <int D, bool PAGED>
 void launch(const QkvRowsParams& p, cudaStream_t stream) {
-  constexpr int kSteps = 4;
-  const int heads = p.H + (PAGED ? 2 : 1) * p.Hkv;
   constexpr int kEach = kSteps * 256 / D;
-  const long long items = (long long)p.total * ((heads + kEach - 1) / kEach);
-  qkv_rows_kernel<D, PAGED, kSteps>
-      <<<(unsigned)((items + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(p);
+  const int groups = (p.H + kEach - 1) / kEach + (PAGED ? 2 : 1) * ((p.Hkv + kEach - 1) / kEach);
+  // As many warps a token as one wave has room for, up to one a group: latency counts
+  // there; beyond, a warp that keeps a token's C, S and slot is the cheapest.  us with
+  // one, two and six warps a token (32 + 8 + 8 heads, d = 128): 64 tokens 7.7, 5.5, 3.7;
+  // 1024 8.7, 7.1, 8.9; 4096 19, 20, 27; 16384 69, 74, 113.
+  const int wave = 152 * kWarps * kBlocks / (p.total < 1 ? 1 : p.total);
+  const int parts = wave < 1 ? 1 : wave < groups ? wave : groups;
+  const long long warps = (long long)p.total * parts;
+  const unsigned blocks = (unsigned)((warps + kWarps - 1) / kWarps);
+  if (p.interleaved) qkv_rows_kernel<D, PAGED, true><<<blocks, kWarps * 32, 0, stream>>>(p, parts);
+  else qkv_rows_kernel<D, PAGED, false><<<blocks, kWarps * 32, 0, stream>>>(p, parts);
 }
 
 }  // namespace
