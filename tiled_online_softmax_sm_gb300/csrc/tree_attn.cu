@@ -19,19 +19,30 @@
 //                128-byte swizzle)
 //   warps 1, 2   tensor memory; lane 0 of warp 1 + w issues the tcgen05.mma of
 //                softmax warpgroup w (one thread for both left the tensor pipe idle
-//                behind its waits and commits: 4800 clocks a K/V tile for 256 rows)
+//                behind its waits and commits)
 //   warp 3       V rows that no node sees are zeroed before the MMA reads them
 //   warps 4-11   softmax, thread = query row = tensor-memory lane
 //
 // The two softmax warpgroups w have a score tile S_w and an accumulator O_w each.
-// A unit of two row tiles gives one to each (every K/V tile is used by both); a
-// unit of one row tile gives warpgroup w the K/V tiles j = w mod 2, so that one's
+// A unit of two query tiles gives one to each (every K/V tile is used by both); a
+// unit of one query tile gives warpgroup w the K/V tiles j = w mod 2, so that one's
 // exponentials run beside the other's MMAs, and the two states merge at the end
-// of the unit inside the CTA.
+// of the segment inside the CTA.
 //
 // Softmax as in the forward: p = 2^(s scale log2 e - ref), the reference raised
 // only when a tile's maximum passes it by far; two sums are kept, of p for the LSE
 // and of the bf16-rounded p that the P V MMA multiplies for O.
+//
+// Measured (d = 128, 32 heads of 8, contexts uniform on the range): 64 x 16 nodes over
+// [512, 8192] tokens, one query tile a unit, 177 us for 1.04 GB (5.9 TB/s, 0.88 of a
+// plain copy; a unit's beginning and end cost as much as three K/V tiles of 350). 4 x
+// [48, 64] nodes over [16384, 65536], two query tiles, 128 us for 0.56 GB (4.4 TB/s):
+// a K/V tile's MMAs for 256 rows take 2050 clocks at d = 128 (3070 in halves) and its
+// exponentials 2050, of the 2500 that HBM takes to bring it.  An MMA of 64 rows or 64
+// columns takes as long as one of 128 x 128.  Two CTAs, one query tile each and K and V
+// shared through L2, took longer (157 us): L2 delivers every K/V tile twice.  What the
+// roles' loops have in common is the instruction cache: with the softmax loops
+// unrolled over a whole tile the issuers' code was pushed out of it (64 x 16 198 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -65,7 +76,6 @@ struct Cfg {
   // values of each key) side by side, so that one copy brings a whole page
   static constexpr int kGroup = 1024 * kChunks;
   static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;   // + alignment slack
-  static constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(128, kTile, false, false);
   static constexpr uint32_t kIdescO = ptx::idesc_bf16_f32(128, D, false, true);
 };
 
@@ -120,10 +130,10 @@ __device__ __forceinline__ int node_units(const Args& a, const Seq& Q) {
 }
 __device__ __forceinline__ int key_tiles(const Seq& Q) { return (Q.L + kTile - 1) / kTile; }
 __device__ __forceinline__ int tile_cost(const Args& a, const Seq& Q, bool weighed) {
-  return !weighed ? 1 : Q.n > a.tile_nodes ? 3 : 2;
+  return !weighed ? 1 : Q.n > a.tile_nodes ? 4 : 2;
 }
 // Cost of beginning and ending a unit.
-constexpr int kUnitCost = 4;
+constexpr int kUnitCost = 6;
 // Tiles a CTA from which on costs are weighed.  (Below, a tile costs 1 and a unit
 // nothing, so that every piece has a tile; above, a piece is longer than any cost, so
 // that of a cut unit every piece between its first and its last tile has one, too.)
@@ -135,10 +145,10 @@ struct Shared {
   uint64_t q_full[2], q_empty[2];   // Q tile i
   uint64_t kv_full[8], kv_empty[8]; // ring slots
   uint64_t fix_full[8];             // ring slots: a V tile landed that is to be cleaned
-  uint64_t s_full[2], p_full[2], o_done[2], o_empty[2];
+  uint64_t s_full[2][2], p_full[2][2];      // warpgroup, part of the K/V tile
+  uint64_t pv_done[2], o_done[2], o_empty[2];
   uint64_t stat_full, stat_empty;   // warpgroup 1's row states are in stat / were read
   uint64_t drain[2];
-  uint64_t turn[2];                 // two query tiles: issuer w may go on
   float stat[kTile][3];
   uint32_t tmem_base;
   int abort;
@@ -172,6 +182,7 @@ __device__ __forceinline__ int copy_v(bool pair, int j, int nt) {
 
 // Steps through the segments of a piece: x is a position in the unit to look at (it
 // begins at list.xb) and s its sequence.  False when there are no more.
+template <bool PAIRS>
 __device__ __forceinline__ bool next_segment(const Args& a, const List& list, int& x, int& s, Seg& S) {
   while (x < list.xe) {
     while (list.pre[s + 1] <= x) ++s;
@@ -187,7 +198,7 @@ __device__ __forceinline__ bool next_segment(const Args& a, const List& list, in
     S.g = u / along;
     S.node0 = (u - S.g * along) * 2 * a.tile_nodes;
     S.nodes = min(2 * a.tile_nodes, S.Q.n - S.node0);
-    S.pair = S.nodes > a.tile_nodes;
+    S.pair = PAIRS && S.nodes > a.tile_nodes;
     S.j0 = max(0, list.xb - S.first + S.cost - 1) / S.cost;
     S.j1 = min(S.nt, max(0, list.xe - S.first + S.cost - 1) / S.cost);
     if (S.j0 < S.j1) return true;
@@ -223,12 +234,19 @@ __device__ __forceinline__ float sum_packed(const uint32_t (&p)[16]) {
   return (x0 + x1) + (x2 + x3);
 }
 
-template <int D>
+template <int D, bool PAIRS>
 __global__ void __launch_bounds__(kThreads, 1)
 tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const Args a) {
   using C = Cfg<D>;
   constexpr int kStages = C::kStages;
+  // Scores are formed and used in parts of a K/V tile: halves where units have two query
+  // tiles, so that a softmax warpgroup works on one half while the other is multiplied (an
+  // MMA of 64 columns takes as long as one of 128, but waiting costs more: 4 x 64 nodes
+  // over [16384, 65536] tokens 138 us whole, 129 in halves); whole tiles otherwise, where
+  // HBM is the bound (64 x 16 nodes 175 us whole, 182 in halves).
+  constexpr int kParts = PAIRS ? 2 : 1, kCols = kTile / kParts;
+  constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(128, kCols, false, false);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sQ = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
@@ -241,9 +259,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const uint32_t bar_kvf = ptx::smem_u32(sh.kv_full), bar_kve = ptx::smem_u32(sh.kv_empty);
   const uint32_t bar_fix = ptx::smem_u32(sh.fix_full);
   const uint32_t bar_s = ptx::smem_u32(sh.s_full), bar_p = ptx::smem_u32(sh.p_full);
-  const uint32_t bar_o = ptx::smem_u32(sh.o_done), bar_oe = ptx::smem_u32(sh.o_empty);
+  const uint32_t bar_pv = ptx::smem_u32(sh.pv_done), bar_o = ptx::smem_u32(sh.o_done), bar_oe = ptx::smem_u32(sh.o_empty);
   const uint32_t bar_sf = ptx::smem_u32(&sh.stat_full), bar_se = ptx::smem_u32(&sh.stat_empty);
-  const uint32_t bar_drain = ptx::smem_u32(sh.drain), bar_turn = ptx::smem_u32(sh.turn);
+  const uint32_t bar_drain = ptx::smem_u32(sh.drain);
 
   // the merge behind this kernel may start its own set-up (it waits for this
   // kernel's completion before it reads the partials)
@@ -252,12 +270,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bar_q + 8 * i, 1);
       ptx::mbar_init(bar_qe + 8 * i, 2);    // an arrival of each issuer, here and below
-      ptx::mbar_init(bar_s + 8 * i, 1);
-      ptx::mbar_init(bar_p + 8 * i, kTile);
+      for (int b = 0; b < 2; ++b) {
+        ptx::mbar_init(bar_s + 16 * i + 8 * b, 1);
+        ptx::mbar_init(bar_p + 16 * i + 8 * b, kTile);
+      }
+      ptx::mbar_init(bar_pv + 8 * i, 1);
       ptx::mbar_init(bar_o + 8 * i, 1);
       ptx::mbar_init(bar_oe + 8 * i, kTile);
       ptx::mbar_init(bar_drain + 8 * i, 1);
-      ptx::mbar_init(bar_turn + 8 * i, 1);
     }
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(bar_kvf + 8 * i, 1);
@@ -339,7 +359,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     uint32_t to_fix = 0u;       // slots whose last copy went to the fix barrier,
     uint32_t fixes = 0u;        // and the parity of the slots' copies that did
     bool ok = true, skip = a.skip_first_copy != 0;
-    while (ok && next_segment(a, list, x, s, S)) {
+    while (ok && next_segment<PAIRS>(a, list, x, s, S)) {
       for (int i = 0; i < (S.pair ? 2 : 1) && ok; ++i) {
         // (rows past the sequence's last node are its neighbour's, or zeros behind the
         // last row of all: they only reach their own rows of S and O, which nobody reads)
@@ -423,7 +443,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const uint32_t s_tm = tbase + w * kTile, o_tm = tbase + 256 + w * 128;
       int lc = 0;                    // copies of the segments so far
       int nq[2] = {0, 0}, half = 0;  // query tiles used, the buffer of the next single one
-      int np = 0, no = 0, nturn = 0; // P tiles, units, turns taken
+      int np = 0, no = 0;            // P tiles, units
       bool ok = true;
       // Every copy is waited for, and its slot released, by both issuers, so that a
       // barrier's phase is never ahead of a wait by two; one that the other issuer
@@ -436,47 +456,30 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         ptx::mbar_arrive(bar_kve + 8 * (l % kStages));
         return true;
       };
-      // With two query tiles the issuers take turns, a turn being P V(j) and S(j + 1):
-      // one warpgroup's exponentials then run beside the other's MMAs.  (Left alone, the
-      // two fall into step, as both wait for the same K/V tiles.)
-      auto take_turn = [&]() {
-        if (w == 0 && nturn == 0) {
-          ++nturn;
-          return true;
-        }
-        return ptx::mbar_wait(bar_turn + 8 * w, (nturn++ - (w == 0 ? 1 : 0)) & 1, status, abort_flag);
-      };
-      auto score = [&](int l, int qb, bool last) {   // S = Q K^T, K being copy l
-        if (!landed(l)) return false;
-        ptx::tc_fence_after();
+      // S = Q K^T over a part of copy l.
+      auto score = [&](int l, int part, int qb) {
         const int slot = l % kStages;
         const uint64_t qd = qdesc0 + (uint64_t)(qb * (C::kTileBytes >> 4));
-        const uint64_t kd = kdesc0 + (uint64_t)(slot * (C::kTileBytes >> 4));
+        const uint64_t kd = kdesc0 + (uint64_t)(slot * (C::kTileBytes >> 4) + part * (C::kGroup >> 1));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          ptx::mma_ss(s_tm, qd + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
-                      kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), C::kIdescS, k > 0);
-        ptx::tc_commit(bar_s + 8 * w);
-        if (S.pair) ptx::mbar_arrive(bar_turn + 8 * (w ^ 1));
-        ptx::tc_commit(bar_kve + 8 * slot);
-        if (last) ptx::tc_commit(bar_qe + 8 * qb);
-        return true;
+          ptx::mma_ss(s_tm + kCols * part, qd + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
+                      kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), kIdescS, k > 0);
+        ptx::tc_commit(bar_s + 16 * w + 8 * part);
       };
-      auto values = [&](int l, bool first) {         // O (+)= P V, V being copy l
-        if (!landed(l) || !ptx::mbar_wait(bar_p + 8 * w, np & 1, status, abort_flag)) return false;
-        ++np;
-        if (S.pair && !take_turn()) return false;
+      // O (+)= P V over a part of copy l; false when the wait for P ran out.
+      auto values = [&](int l, int part, bool first) {
+        if (!ptx::mbar_wait(bar_p + 16 * w + 8 * part, np & 1, status, abort_flag)) return false;
         ptx::tc_fence_after();
-        const int slot = l % kStages;
-        const uint64_t vd = vdesc0 + (uint64_t)(slot * (C::kTileBytes >> 4));
+        const uint64_t vd = vdesc0 + (uint64_t)((l % kStages) * (C::kTileBytes >> 4) + part * (C::kGroup >> 1));
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          ptx::mma_ts(o_tm, s_tm + k * 8, vd + (uint64_t)(k * (C::kGroup >> 3)), C::kIdescO,
-                      (!first || k > 0) ? 1u : 0u);
-        ptx::tc_commit(bar_kve + 8 * slot);
+        for (int k = 0; k < kCols / 16; ++k)
+          ptx::mma_ts(o_tm, s_tm + kCols * part + k * 8, vd + (uint64_t)(k * (C::kGroup >> 3)), C::kIdescO,
+                      (!first || part > 0 || k > 0) ? 1u : 0u);
+        ptx::tc_commit(bar_pv + 8 * w);
         return true;
       };
-      while (ok && next_segment(a, list, x, s, S)) {
+      while (ok && next_segment<PAIRS>(a, list, x, s, S)) {
         const int nt = S.j1 - S.j0;
         const int step = S.pair ? 1 : 2, j0 = S.pair ? 0 : w;   // this issuer's tiles
         const int qb = S.pair ? w : half;
@@ -488,10 +491,20 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           if (ok && (i != qb || j0 >= nt)) ptx::mbar_arrive(bar_qe + 8 * i);
         }
         if (!S.pair) half ^= 1;
-        if (S.pair) {
-          ok = ok && landed(lc) && take_turn() && score(lc, qb, nt == 1);
-        } else {
-          for (int j = 0; j < min(2, nt) && ok; ++j) ok = j == w ? score(lc + j, qb, j + 2 >= nt) : pass(lc + j);
+        auto k_done = [&](int l, bool last) {      // all of K's scores are on their way
+          ptx::tc_commit(bar_kve + 8 * (l % kStages));
+          if (last) ptx::tc_commit(bar_qe + 8 * qb);
+        };
+        for (int j = 0; j < min(step, nt) && ok; ++j) {
+          if (!S.pair && j != w) {
+            ok = pass(lc + j);
+            continue;
+          }
+          if (!(ok = landed(lc + j))) break;
+          ptx::tc_fence_after();
+          score(lc + j, 0, qb);
+          if constexpr (kParts == 2) score(lc + j, 1, qb);
+          k_done(lc + j, j + step >= nt);
         }
         for (int j = 0; j < nt && ok; ++j) {
           const bool mine = S.pair || (j & 1) == w, next = j + step < nt;
@@ -499,9 +512,20 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           if (mine) {
             // (the previous unit's O is read out of tensor memory)
             if (j == j0 && !(ok = ptx::mbar_wait(bar_oe + 8 * w, (no++ & 1) ^ 1, status, abort_flag))) break;
-            ok = values(lv, j == j0) && (!next || score(lv + 1, qb, j + 2 * step >= nt));
-            if (ok && !next) ptx::tc_commit(bar_o + 8 * w);
-            if (S.pair && !next) ptx::mbar_arrive(bar_turn + 8 * (w ^ 1));
+            ok = landed(lv) && values(lv, 0, j == j0) && (!next || landed(lv + 1));
+            if (!ok) break;
+            if constexpr (kParts == 2) {
+              if (next) score(lv + 1, 0, qb);
+              if (!(ok = values(lv, 1, j == j0))) break;
+            }
+            ++np;
+            ptx::tc_commit(bar_kve + 8 * (lv % kStages));
+            if (next) {
+              score(lv + 1, kParts - 1, qb);
+              k_done(lv + 1, j + 2 * step >= nt);
+            } else {
+              ptx::tc_commit(bar_o + 8 * w);
+            }
           } else {
             ok = pass(lv) && (!next || pass(lv + 1));
           }
@@ -519,7 +543,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     int lc = 0;
     uint32_t fixes = 0u;   // parity of each slot's copies to the fix barrier
     bool ok = true;
-    while (ok && next_segment(a, list, x, s, S)) {
+    while (ok && next_segment<PAIRS>(a, list, x, s, S)) {
       const int i0 = S.node0, i1 = S.node0 + S.nodes;
       const int fix0 = (S.Q.L - S.Q.n) / kTile;   // first tile with nodes
       for (int j = max(S.j0, fix0); j < S.j1; ++j) {
@@ -572,7 +596,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     if (threadIdx.x == 128) {   // for the merge: no unit cut behind this piece, until one is met
       a.cuts[cta] = Cut{0, 0, 0, 0, 0, 0, 0, 0};
     }
-    while (ok && next_segment(a, list, x, s, S)) {
+    while (ok && next_segment<PAIRS>(a, list, x, s, S)) {
       const int nt = S.j1 - S.j0;
       const int tile_rows = a.tile_nodes * a.G;
       const int rows = min(tile_rows, S.nodes * a.G - (S.pair && w == 1 ? tile_rows : 0));   // of this tile
@@ -593,100 +617,116 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
           for (int c = 0; c < 4; ++c) vis[c] = valid ? sees(a, S.Q, node, k0 + 32 * c) : 0u;
         }
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_s + 8 * w, ns & 1, status, abort_flag));
-        if (!ok) break;
-        ++ns;
-        ptx::tc_fence_after();
-        if (any) {
-          float mx = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < 4; c += 2) {
+        for (int part = 0; part < kParts; ++part) {
+          ok = __all_sync(0xffffffffu,
+                          ptx::mbar_wait(bar_s + 16 * w + 8 * part, ns & 1, status, abort_flag));
+          if (!ok) break;
+          ptx::tc_fence_after();
+          if (any) {
+            const uint32_t col = s_col + kCols * part;
             uint32_t x0[32], x1[32];
-            if (!masked) {   // the loads reduce the maximum themselves
+            // 64 scores, those of hidden keys -inf; returns the maximum.  (The loads of a
+            // tile without nodes reduce it themselves.)
+            auto load = [&](int g) __attribute__((always_inline)) -> float {
               float m0, m1;
-              ptx::tmem_ld32_max(s_col + c * 32, x0, m0);
-              ptx::tmem_ld32_max(s_col + c * 32 + 32, x1, m1);
+              ptx::tmem_ld32_max(col + 64 * g, x0, m0);
+              ptx::tmem_ld32_max(col + 64 * g + 32, x1, m1);
               ptx::tmem_wait_ld();
+              float top = fmaxf(m0, m1);
+              if (masked) {
+                const bool low = kParts == 2 ? part == 0 : g == 0;
+                const uint32_t v0 = low ? vis[0] : vis[2], v1 = low ? vis[1] : vis[3];
+                top = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  x0[e] = v0 >> e & 1u ? x0[e] : 0xff800000u;
+                  x1[e] = v1 >> e & 1u ? x1[e] : 0xff800000u;
+                  top = ptx::fmax3(top, __uint_as_float(x0[e]), __uint_as_float(x1[e]));
+                }
+              }
+              return top;
+            };
+            float mx = load(0);
+            if constexpr (kParts == 1) {
 #pragma unroll
               for (int e = 0; e < 32; ++e)   // (the registers stay theirs until the loads are done)
                 asm volatile("" ::"r"(x0[e]), "r"(x1[e]));
-              mx = ptx::fmax3(mx, m0, m1);
+              mx = fmaxf(mx, load(1));
+            }
+            const float m_tile = mx * a.scale_log2;   // scale > 0: the maximum commutes with it
+            float alpha = 1.f;
+            if (valid && (m_tile > m_ref + kRaise || (m_ref == -INFINITY && m_tile > -INFINITY))) {
+              alpha = m_ref == -INFINITY ? 1.f : ptx::ex2(m_ref - m_tile);
+              m_ref = m_tile;
+              l_run *= alpha;
+              l_p *= alpha;
+            }
+            // O is rescaled behind the P V of the part before this one
+            if (__any_sync(0xffffffffu, (jl > jw || part > 0) && alpha != 1.f)) {
+              const uint32_t done = kParts == 2 ? part ^ 1 : (ns & 1) ^ 1;   // (the phase before this part's)
+              ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_pv + 8 * w, done, status, abort_flag));
+              if (!ok) break;
+              ptx::tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t ov[32];
+                ptx::tmem_ld32(o_col + c * 32, ov);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                ptx::tmem_st32(o_col + c * 32, ov);
+              }
+            }
+            const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+            const uint64_t nref2 = ptx::f2_bits(-ref, -ref);
+            uint64_t sum2[2] = {ptx::f2_bits(0.f, 0.f), ptx::f2_bits(0.f, 0.f)};
+            // P (bf16 pairs) overwrites the first half of its scores, which are in
+            // registers
+            auto form = [&](const uint32_t (&x)[32], int c) __attribute__((always_inline)) {
+              uint32_t pp[16];
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float y0, y1;
+                ptx::f2_split(
+                    ptx::ffma2(ptx::f2_bits(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), sc2, nref2), y0, y1);
+                const float p0 = ptx::ex2(y0), p1 = ptx::ex2(y1);
+                sum2[(e / 2) & 1] = ptx::fadd2(sum2[(e / 2) & 1], ptx::f2_bits(p0, p1));
+                pp[e / 2] = ptx::pack_bf16x2(p0, p1);
+              }
+              ptx::tmem_st16(col + c * 16, pp);
+              l_p += sum_packed(pp);
+            };
+            if constexpr (kParts == 1) {   // (x holds the upper 64: they go last)
+              uint32_t y0[32], y1[32];
+              ptx::tmem_ld32(col, y0);
+              ptx::tmem_ld32(col + 32, y1);
+              ptx::tmem_wait_ld();
+              if (masked) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  y0[e] = vis[0] >> e & 1u ? y0[e] : 0xff800000u;
+                  y1[e] = vis[1] >> e & 1u ? y1[e] : 0xff800000u;
+                }
+              }
+              form(y0, 0);
+              form(y1, 1);
+              form(x0, 2);
+              form(x1, 3);
             } else {
-              const uint32_t v0 = c == 0 ? vis[0] : vis[2], v1 = c == 0 ? vis[1] : vis[3];
-              ptx::tmem_ld32(s_col + c * 32, x0);
-              ptx::tmem_ld32(s_col + c * 32 + 32, x1);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                mx = ptx::fmax3(mx, v0 >> e & 1u ? __uint_as_float(x0[e]) : -INFINITY,
-                                v1 >> e & 1u ? __uint_as_float(x1[e]) : -INFINITY);
+              form(x0, 0);
+              form(x1, 1);
             }
+            float a0, a1;
+            ptx::f2_split(ptx::fadd2(sum2[0], sum2[1]), a0, a1);
+            l_run += a0 + a1;
+            ptx::tmem_wait_st();
           }
-          const float m_tile = mx * a.scale_log2;   // scale > 0: the maximum commutes with it
-          float alpha = 1.f;
-          if (valid && (m_tile > m_ref + kRaise || (m_ref == -INFINITY && m_tile > -INFINITY))) {
-            alpha = m_ref == -INFINITY ? 1.f : ptx::ex2(m_ref - m_tile);
-            m_ref = m_tile;
-            l_run *= alpha;
-            l_p *= alpha;
-          }
-          // (S of this tile is complete, so every earlier P V is: they were issued
-          // before it)
-          if (__any_sync(0xffffffffu, jl > jw && alpha != 1.f)) {
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t ov[32];
-              ptx::tmem_ld32(o_col + c * 32, ov);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-              ptx::tmem_st32(o_col + c * 32, ov);
-            }
-          }
-          const float ref = m_ref == -INFINITY ? 0.f : m_ref;
-          const uint64_t nref2 = ptx::f2_bits(-ref, -ref);
-          uint64_t sum2[2] = {ptx::f2_bits(0.f, 0.f), ptx::f2_bits(0.f, 0.f)};
-          // P (bf16 pairs) overwrites S from its first column on: 32 keys' go to 16
-          // columns whose scores were read before
-          auto form = [&](uint32_t (&x)[32], int c) __attribute__((always_inline)) {
-            if (masked) {
-              const uint32_t v = c == 0 ? vis[0] : c == 1 ? vis[1] : c == 2 ? vis[2] : vis[3];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = v >> e & 1u ? x[e] : 0xff800000u;
-            }
-            uint32_t pp[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float x0, x1;
-              ptx::f2_split(ptx::ffma2(ptx::f2_bits(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), sc2, nref2),
-                            x0, x1);
-              const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
-              sum2[(e / 2) & 1] = ptx::fadd2(sum2[(e / 2) & 1], ptx::f2_bits(p0, p1));
-              pp[e / 2] = ptx::pack_bf16x2(p0, p1);
-            }
-            ptx::tmem_st16(s_col + c * 16, pp);
-            l_p += sum_packed(pp);
-          };
-          // (a rolled loop: unrolled, the code of the softmax warps pushes that of the
-          // issuers out of the instruction cache)
-          uint32_t xa[32], xb[32];
-          ptx::tmem_ld32(s_col, xa);
-#pragma unroll 1
-          for (int c = 0; c < 4; c += 2) {
-            ptx::tmem_wait_ld();
-            ptx::tmem_ld32(s_col + c * 32 + 32, xb);
-            form(xa, c);
-            ptx::tmem_wait_ld();
-            if (c == 0) ptx::tmem_ld32(s_col + 64, xa);
-            form(xb, c + 1);
-          }
-          float a0, a1;
-          ptx::f2_split(ptx::fadd2(sum2[0], sum2[1]), a0, a1);
-          l_run += a0 + a1;
-          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(bar_p + 16 * w + 8 * part);
         }
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(bar_p + 8 * w);
+        if (!ok) break;
+        ++ns;
       }
       if (!ok) break;
       // ---- the rows of the segment: finished, or left as a partial
@@ -906,7 +946,8 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream, const char** wh
   a.cuts = reinterpret_cast<Cut*>(ws);
   a.part_s = reinterpret_cast<float4*>(ws + kCutBytes);
   a.part_o = a.part_s + (size_t)2 * kCtas * a.row_cap;
-  auto kernel = tree_attn_kernel<D>;
+  // (without units of two query tiles the kernel is the smaller one)
+  auto kernel = p.max_q > tile_nodes ? tree_attn_kernel<D, true> : tree_attn_kernel<D, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e == cudaSuccess) {
     kernel<<<kCtas, kThreads, C::kSmem, stream>>>(tmQ, tmK, tmV, a);
