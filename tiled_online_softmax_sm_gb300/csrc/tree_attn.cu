@@ -95,6 +95,7 @@ struct Args {
   __nv_bfloat16* o;
   float* lse;
   int num_seqs, total_q, max_q, words, H, Hkv, G, tile_nodes, num_pages, max_blocks;
+  unsigned long long per_unit;     // 2^40 / (2 * tile_nodes), rounded up
   float scale_log2;
   int skip_first_copy;
   int* status;
@@ -125,12 +126,19 @@ __device__ __forceinline__ Seq load_seq(const Args& a, int s) {
 
 // Units of a sequence along its nodes, K/V tiles of each, and the cost of one: with
 // two query tiles it takes about half as long again.
+// (a division by 2 * tile_nodes <= 256 as a product with its reciprocal in 2^-40, which is
+// exact below 2^32: the divisions of five roles' segments were a good part of the
+// code, and of a small call's time)
 __device__ __forceinline__ int node_units(const Args& a, const Seq& Q) {
-  return (Q.n + 2 * a.tile_nodes - 1) / (2 * a.tile_nodes);
+  return (int)(((unsigned long long)(Q.n + 2 * a.tile_nodes - 1) * a.per_unit) >> 40);
+}
+__device__ __forceinline__ int ceil_div(int x, int cost) {   // cost 1, 2 or 3; 0 for x < 0
+  const uint32_t y = (uint32_t)(max(x, 0) + cost - 1);
+  return (int)(cost == 3 ? __umulhi(y, 0xaaaaaaabu) >> 1 : y >> (cost - 1));
 }
 __device__ __forceinline__ int key_tiles(const Seq& Q) { return (Q.L + kTile - 1) / kTile; }
 __device__ __forceinline__ int tile_cost(const Args& a, const Seq& Q, bool weighed) {
-  return !weighed ? 1 : Q.n > a.tile_nodes ? 4 : 2;
+  return !weighed ? 1 : Q.n > a.tile_nodes ? 3 : 2;
 }
 // Cost of beginning and ending a unit.
 constexpr int kUnitCost = 6;
@@ -139,9 +147,14 @@ constexpr int kUnitCost = 6;
 // that of a cut unit every piece between its first and its last tile has one, too.)
 constexpr int kWeighedTiles = 8;
 
+// Cost of all units of a sequence.
+__device__ __forceinline__ int seq_cost(const Args& a, const Seq& Q, bool weighed) {
+  return node_units(a, Q) * a.Hkv * ((weighed ? kUnitCost : 0) + key_tiles(Q) * tile_cost(a, Q, weighed));
+}
+
 struct Shared {
   int pre[kMaxTreeSeqs + 1];   // cost of sequences 0 .. s - 1
-  int warp_sum[2][kThreads / 32];
+  int warp_sum[2][32];
   uint64_t q_full[2], q_empty[2];   // Q tile i
   uint64_t kv_full[8], kv_empty[8]; // ring slots
   uint64_t fix_full[8];             // ring slots: a V tile landed that is to be cleaned
@@ -192,15 +205,15 @@ __device__ __forceinline__ bool next_segment(const Args& a, const List& list, in
     S.cost = tile_cost(a, S.Q, list.weighed);
     const int along = node_units(a, S.Q);
     const int unit = list.begin + S.nt * S.cost;
-    const int u = (x - list.pre[s]) / unit;
-    S.first = list.pre[s] + u * unit + list.begin;
+    const unsigned u = (unsigned)(x - list.pre[s]) / (unsigned)unit;
+    S.first = list.pre[s] + (int)u * unit + list.begin;
     x = S.first + S.nt * S.cost;
-    S.g = u / along;
-    S.node0 = (u - S.g * along) * 2 * a.tile_nodes;
+    S.g = along == 1 ? (int)u : (int)(u / (unsigned)along);
+    S.node0 = ((int)u - S.g * along) * 2 * a.tile_nodes;
     S.nodes = min(2 * a.tile_nodes, S.Q.n - S.node0);
     S.pair = PAIRS && S.nodes > a.tile_nodes;
-    S.j0 = max(0, list.xb - S.first + S.cost - 1) / S.cost;
-    S.j1 = min(S.nt, max(0, list.xe - S.first + S.cost - 1) / S.cost);
+    S.j0 = ceil_div(list.xb - S.first, S.cost);
+    S.j1 = min(S.nt, ceil_div(list.xe - S.first, S.cost));
     if (S.j0 < S.j1) return true;
   }
   return false;
@@ -266,7 +279,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   // the merge behind this kernel may start its own set-up (it waits for this
   // kernel's completion before it reads the partials)
   asm volatile("griddepcontrol.launch_dependents;");
+  if (threadIdx.x == 32) {
+    ptx::prefetch_tmap(&tmQ);
+    ptx::prefetch_tmap(&tmK);
+    ptx::prefetch_tmap(&tmV);
+  }
   if (threadIdx.x == 0) {
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bar_q + 8 * i, 1);
       ptx::mbar_init(bar_qe + 8 * i, 2);    // an arrival of each issuer, here and below
@@ -279,6 +298,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       ptx::mbar_init(bar_oe + 8 * i, kTile);
       ptx::mbar_init(bar_drain + 8 * i, 1);
     }
+#pragma unroll 1
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(bar_kvf + 8 * i, 1);
       ptx::mbar_init(bar_kve + 8 * i, 2);
@@ -294,41 +314,44 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     ptx::tmem_alloc(ptx::smem_u32(&sh.tmem_base), 512);
     ptx::tmem_relinquish();
   }
-  // the list: how many tiles there are, whether beginning a unit counts, the offsets
+  // the list: how many tiles there are, whether costs are weighed, the offsets
   const int per = (a.num_seqs + kThreads - 1) / kThreads;
   const int s0 = min(a.num_seqs, (int)threadIdx.x * per), s1 = min(a.num_seqs, s0 + per);
   int tiles = 0;
   List list{sh.pre, false, 0, 0, 0};
   {
-    int mine = 0;
+    int own[2] = {0, 0};   // of this thread's sequences: tiles, weighed cost
+#pragma unroll 1
     for (int s = s0; s < s1; ++s) {
       const Seq Q = load_seq(a, s);
       if (Q.bad && blockIdx.x == 0) atomicExch(status, kDevInvalidArg);
-      if (Q.n > 0) mine += node_units(a, Q) * a.Hkv * key_tiles(Q);
+      own[0] += seq_cost(a, Q, false);
+      own[1] += seq_cost(a, Q, true);
     }
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    if (lane == 0) sh.warp_sum[0][warp] = mine;
+    int run[2] = {own[0], own[1]};
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int v = __shfl_up_sync(0xffffffffu, run[k], o);
+        if (lane >= o) run[k] += v;
+      }
+    if (lane == 31) {
+      sh.warp_sum[0][warp] = run[0];
+      sh.warp_sum[1][warp] = run[1];
+    }
     __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) tiles += sh.warp_sum[0][w];
+    tiles = __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? sh.warp_sum[0][lane] : 0);
     list.weighed = tiles >= kWeighedTiles * (int)gridDim.x;
     list.begin = list.weighed ? kUnitCost : 0;
-    int run = 0;
+    const int k = list.weighed ? 1 : 0;
+    int at = (k ? run[1] - own[1] : run[0] - own[0]);
+    at += __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_sum[k][lane] : 0);
+#pragma unroll 1
     for (int s = s0; s < s1; ++s) {
-      const Seq Q = load_seq(a, s);
-      if (Q.n > 0) run += node_units(a, Q) * a.Hkv * (list.begin + key_tiles(Q) * tile_cost(a, Q, list.weighed));
-      sh.pre[s + 1] = run;
+      at += per == 1 ? (k ? own[1] : own[0]) : seq_cost(a, load_seq(a, s), list.weighed);
+      sh.pre[s + 1] = at;
     }
-    const int own = run;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, run, o);
-      if (lane >= o) run += v;
-    }
-    if (lane == 31) sh.warp_sum[1][warp] = run;
-    __syncthreads();
-    int base = run - own;
-    for (int w = 0; w < warp; ++w) base += sh.warp_sum[1][w];
-    for (int s = s0; s < s1; ++s) sh.pre[s + 1] += base;
     if (threadIdx.x == 0) sh.pre[0] = 0;
   }
   ptx::tc_fence_before();
@@ -647,42 +670,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               }
               return top;
             };
-            float mx = load(0);
-            if constexpr (kParts == 1) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)   // (the registers stay theirs until the loads are done)
-                asm volatile("" ::"r"(x0[e]), "r"(x1[e]));
-              mx = fmaxf(mx, load(1));
-            }
-            const float m_tile = mx * a.scale_log2;   // scale > 0: the maximum commutes with it
-            float alpha = 1.f;
-            if (valid && (m_tile > m_ref + kRaise || (m_ref == -INFINITY && m_tile > -INFINITY))) {
-              alpha = m_ref == -INFINITY ? 1.f : ptx::ex2(m_ref - m_tile);
-              m_ref = m_tile;
-              l_run *= alpha;
-              l_p *= alpha;
-            }
-            // O is rescaled behind the P V of the part before this one
-            if (__any_sync(0xffffffffu, (jl > jw || part > 0) && alpha != 1.f)) {
-              const uint32_t done = kParts == 2 ? part ^ 1 : (ns & 1) ^ 1;   // (the phase before this part's)
-              ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_pv + 8 * w, done, status, abort_flag));
-              if (!ok) break;
-              ptx::tc_fence_after();
-#pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t ov[32];
-                ptx::tmem_ld32(o_col + c * 32, ov);
-                ptx::tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                ptx::tmem_st32(o_col + c * 32, ov);
-              }
-            }
-            const float ref = m_ref == -INFINITY ? 0.f : m_ref;
-            const uint64_t nref2 = ptx::f2_bits(-ref, -ref);
-            uint64_t sum2[2] = {ptx::f2_bits(0.f, 0.f), ptx::f2_bits(0.f, 0.f)};
-            // P (bf16 pairs) overwrites the first half of its scores, which are in
-            // registers
+            float mx = -INFINITY;
+            uint64_t nref2 = 0, sum2[2] = {ptx::f2_bits(0.f, 0.f), ptx::f2_bits(0.f, 0.f)};
+            // P (bf16 pairs) of 32 scores goes to 16 columns of S whose scores are in
+            // registers or done with
             auto form = [&](const uint32_t (&x)[32], int c) __attribute__((always_inline)) {
               uint32_t pp[16];
 #pragma unroll
@@ -697,26 +688,53 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               ptx::tmem_st16(col + c * 16, pp);
               l_p += sum_packed(pp);
             };
-            if constexpr (kParts == 1) {   // (x holds the upper 64: they go last)
-              uint32_t y0[32], y1[32];
-              ptx::tmem_ld32(col, y0);
-              ptx::tmem_ld32(col + 32, y1);
-              ptx::tmem_wait_ld();
-              if (masked) {
+            // Half a tile: one look.  A whole one: both halves for the maximum, then both
+            // again for P.  (Rolled: unrolled over the tile, the code of the softmax warps
+            // pushes that of the issuers out of the instruction cache.)
+            constexpr int kLooks = kParts == 2 ? 1 : 4;
+#pragma unroll 1
+            for (int look = 0; look < kLooks; ++look) {
+              const float top = load(look & 1);
+              if (kParts == 2 || look < 2) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  y0[e] = vis[0] >> e & 1u ? y0[e] : 0xff800000u;
-                  y1[e] = vis[1] >> e & 1u ? y1[e] : 0xff800000u;
-                }
+                for (int e = 0; e < 32; ++e)   // (the registers stay theirs until the loads are done)
+                  asm volatile("" ::"r"(x0[e]), "r"(x1[e]));
+                mx = fmaxf(mx, top);
               }
-              form(y0, 0);
-              form(y1, 1);
-              form(x0, 2);
-              form(x1, 3);
-            } else {
-              form(x0, 0);
-              form(x1, 1);
+              if (kParts == 2 || look == 1) {
+                const float m_tile = mx * a.scale_log2;   // scale > 0: the maximum commutes with it
+                float alpha = 1.f;
+                if (valid && (m_tile > m_ref + kRaise || (m_ref == -INFINITY && m_tile > -INFINITY))) {
+                  alpha = m_ref == -INFINITY ? 1.f : ptx::ex2(m_ref - m_tile);
+                  m_ref = m_tile;
+                  l_run *= alpha;
+                  l_p *= alpha;
+                }
+                // O is rescaled behind the P V of the part before this one
+                if (__any_sync(0xffffffffu, (jl > jw || part > 0) && alpha != 1.f)) {
+                  const uint32_t done = kParts == 2 ? part ^ 1 : (ns & 1) ^ 1;   // (the phase before this part's)
+                  ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_pv + 8 * w, done, status, abort_flag));
+                  if (!ok) break;
+                  ptx::tc_fence_after();
+#pragma unroll 1
+                  for (int c = 0; c < D / 32; ++c) {
+                    uint32_t ov[32];
+                    ptx::tmem_ld32(o_col + c * 32, ov);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                    ptx::tmem_st32(o_col + c * 32, ov);
+                  }
+                }
+                const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+                nref2 = ptx::f2_bits(-ref, -ref);
+              }
+              if (kParts == 2 || look >= 2) {
+                form(x0, 2 * (look & 1));
+                form(x1, 2 * (look & 1) + 1);
+              }
             }
+            if (!ok) break;
             float a0, a1;
             ptx::f2_split(ptx::fadd2(sum2[0], sum2[1]), a0, a1);
             l_run += a0 + a1;
@@ -940,7 +958,7 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream, const char** wh
   }
   Args a{static_cast<const __nv_bfloat16*>(p.q), p.block_table, p.seq_lens, p.cu_q, p.mask,
          static_cast<__nv_bfloat16*>(p.o), p.lse, p.num_seqs, p.total_q, p.max_q, p.words, p.H, p.Hkv, G,
-         tile_nodes, p.num_pages, p.max_blocks, p.scale * kLog2e, skip_first_copy_for_tests(), p.status,
+         tile_nodes, p.num_pages, p.max_blocks, ((1ull << 40) + 2 * tile_nodes - 1) / (2 * tile_nodes), p.scale * kLog2e, skip_first_copy_for_tests(), p.status,
          nullptr, nullptr, nullptr, row_cap(p.max_q, G)};
   char* ws = static_cast<char*>(p.workspace);
   a.cuts = reinterpret_cast<Cut*>(ws);
