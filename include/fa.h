@@ -566,8 +566,10 @@ fa_status fa_tree_layout(const int* parents, const int* seq_lens, const int* cu_
  * The arithmetic is fp32, rounded once to bf16.  A token with a position outside
  * [0, max_positions) is skipped (its rows are not written) and sets
  * FA_ERR_INVALID_ARG in the device status word.
+ * (A head whose values reach 1e18 has squares beyond fp32: its norm is infinite and the
+ * head becomes 0.)
  * Supported: d in {64, 128}; rot_dim a multiple of 8 up to d; 1 <= num_axes <= 4;
- * pointers 16-byte aligned; total*(H + 2*Hkv) below 2^31.
+ * pointers 16-byte aligned; H, Hkv <= 65536; total*(H + 2*Hkv) below 2^31.
  */
 fa_status fa_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight,
                           const float* cos_sin, const int* positions, void* q_out, void* k_out,
@@ -626,7 +628,7 @@ size_t fa_paged_tree_workspace_size(int num_seqs, int max_seqlen_q, int H, int H
  * FA_ERR_BAD_BLOCK_TABLE; the sequence's output is then unspecified.
  * Supported: d in {64, 128}, page_size == 16, H / Hkv <= 128; scale positive and
  * finite; 1 <= mask_words; num_seqs <= 4096; total_q*H and total_q*mask_words below
- * 2^31; num_pages*Hkv*16 below 2^31; units * (3*ceil(max_blocks_per_seq / 8) + 4)
+ * 2^31; num_pages*Hkv*16 below 2^31; units * (3*ceil(max_blocks_per_seq / 8) + 6)
  * below 2^31, where units = num_seqs * Hkv * ceil(max_seqlen_q / (2*floor(128 /
  * (H / Hkv)))).
  */
@@ -646,8 +648,8 @@ fa_status fa_paged_tree_attention(const void* q, const void* k_cache, const void
  *   path          int32 [num_seqs][max_path]: the accepted nodes of sequence s,
  *                 in increasing order, path_lens[s] of them (0 <= path_lens[s] <=
  *                 max_path); the entries behind them may be anything
- *   new_seq_lens  int32 [num_seqs] written: seq_lens[s] - n_s + path_lens[s] (not
- *                 seq_lens itself)
+ *   new_seq_lens  int32 [num_seqs] written: seq_lens[s] - n_s + path_lens[s] (an
+ *                 array of its own, not seq_lens itself)
  * The rows of node path[s][a] are copied to the slot of node a, for every a in
  * turn; the slots behind keep their contents.  A sequence whose path is longer
  * than max_path or n_s, leaves [0, n_s) or does not increase is skipped, its new
@@ -655,8 +657,9 @@ fa_status fa_paged_tree_attention(const void* q, const void* k_cache, const void
  * out of range, its own or its destination's, is skipped and sets
  * FA_ERR_BAD_BLOCK_TABLE.  The pages that hold a sequence's nodes must be its
  * own: two sequences that move rows within one page leave an unspecified mix.
- * Supported: d in {64, 128}, page_size == 16, max_path <= 1024; num_pages*Hkv*16
- * below 2^31, max_blocks_per_seq below 2^26, num_seqs * num_layers below 2^31.
+ * Supported: d in {64, 128}, page_size == 16, max_path <= 1024, Hkv <= 65536,
+ * num_layers <= 65535; num_pages*Hkv*16 below 2^31, max_blocks_per_seq below 2^26,
+ * num_seqs * num_layers below 2^31.
  */
 fa_status fa_paged_kv_accept(void* k_cache, void* v_cache, void* k_scale, void* v_scale,
                              const int* block_table, const int* seq_lens, const int* cu_seqlens,

@@ -66,6 +66,32 @@ def test_rows_of_several_tiles(H, Hkv, new):
     _run(6, [400, 71], new[:1] + [min(71, new[1])], H, Hkv, 64)
 
 
+@pytest.mark.parametrize("G,new", [(128, [3, 1, 5]), (96, [2, 3, 0]), (65, [1, 4, 2]), (43, [2, 5, 7])])
+def test_wide_groups(G, new):
+    """Groups of heads that fill a query tile alone, or leave rows of it unused."""
+    _run(22, [300, 17, 140], new, G, 1, 128)
+    _run(23, [300, 17, 1400], new, 2 * G, 2, 64)
+
+
+def test_most_sequences():
+    """4096 sequences, the most a call takes, of 0 to 3 nodes."""
+    rng = np.random.default_rng(24)
+    new = rng.integers(0, 4, 4096).tolist()
+    lens = [n + int(x) for n, x in zip(new, rng.integers(0, 150, 4096))]
+    _run(25, lens, new, 2, 1, 64, only=range(5, 4096, 331))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_and_two_query_tiles_in_one_batch(d):
+    """Units of both kinds over cut keys, weighed against each other."""
+    _run(26, [6000, 9000, 4000, 128, 7000, 257], [5, 60, 33, 40, 1, 64], 32, 8, d, only=[1, 2, 3, 4, 5])
+
+
+def test_loose_bounds():
+    """More mask words and a larger bound than any sequence needs."""
+    _run(27, [300, 64], [9, 40], 4, 2, 128, words=7, bound=5000)
+
+
 def test_long_context_is_cut():
     _run(7, [9000, 40], [12, 3], 8, 2, 128)
     _run(8, [9000], [70], 8, 2, 128)      # two query tiles over cut keys
@@ -97,6 +123,7 @@ def test_bits_beyond_trees():
 def test_hot_scores(d):
     """Scores of several hundred: the reference is raised often, one key has nearly all the weight."""
     _run(14, [700, 300], [9, 30], 4, 2, d, scale=4.0, spread=1.5)
+    _run(28, [1700, 300], [70, 30], 8, 2, d, scale=4.0, spread=1.5)    # two query tiles
 
 
 @pytest.mark.parametrize("H", [2, 16])
@@ -143,6 +170,23 @@ def test_nan_and_infinite_scores():
         rest = [i for i in range(n) if not (bad and i in (7, 9))]
         ref = T.attend(T.f64(q)[rest], k, v, float(np.float32(0.2)), full[rest])
         T.check_attention(o[rest], lse[rest], ref)
+
+
+@pytest.mark.parametrize("H", [2, 16])
+@pytest.mark.parametrize("at", [0, 100, 300])
+def test_nan_in_the_context(at, H):
+    """Every node sees it: all rows are NaN, those of the other kv head and sequence are not."""
+    rng = np.random.default_rng(29)
+    c = T.Cache(rng, [400, 90], 2, 128)
+    c.k[int(c.bt[0, at // 16]), 1, at % 16, 5] = float("nan")
+    n = 20
+    q = torch.randn((2 * n, 2 * H, 128), device="cuda").bfloat16()
+    mask = np.concatenate([T.pack(np.tril(np.ones((n, n), bool)), 1)] * 2)
+    o, lse = fb.paged_tree_attention(q, *c.args(), T.i32([0, n, 2 * n]), n, T.i32(mask), 0.1)
+    assert o[:n, H:].isnan().all() and lse[H:, :n].isnan().all()
+    assert not o[:n, :H].isnan().any() and not lse[:H, :n].isnan().any()
+    assert not o[n:].isnan().any() and not lse[:, n:].isnan().any()
+    assert fb.fa_get_device_status() == 0
 
 
 def test_rows_behind_the_last_sequence_and_skipped_ones():

@@ -74,7 +74,8 @@ REFUSED = [(dict(S=-1), INV), (dict(T=-1), INV), (dict(P=-1), INV), (dict(maxb=-
            (dict(scale=NAN), INV), (dict(scale=INF), INV), (dict(ws=None), WS), (dict(ws=272), WS),
            (dict(wsb=100), WS), (dict(H=9, scale=0.1), INV), (dict(S=4097, scale=0.1), UNS),
            (dict(ks=16), INV), (dict(vs=16), INV), (dict(mp=1025), UNS), (dict(new=16), INV),
-           (dict(layers=65536), UNS), (dict(N=1 << 26, layers=2), UNS), (dict(words=33, parents=16), UNS),
+           (dict(layers=65536), UNS), (dict(Hkv=65537, kst=65537 * 128, vst=65537 * 128), UNS),
+           (dict(Hkv=65537, layers=1, P=1), UNS), (dict(H=65537, qst=65537 * 128), UNS), (dict(H=258, Hkv=2, scale=0.1), UNS), (dict(N=1 << 26, layers=2), UNS), (dict(words=33, parents=16), UNS),
            (dict(T=1 << 27, words=16, mask=16, H=8), UNS), (dict(qo=16, qst=2048), INV), (dict(ko=16, kst=512), INV)]
 REFUSED += [({x: None}, INV) for x in ("parents", "sl", "cu", "mask", "q", "k", "v", "qo", "ko", "kc", "vc", "bt", "o",
                                        "path", "pl", "new", "pairs")]
@@ -107,7 +108,7 @@ def test_empty_calls(lib):
 def test_list_of_tiles_is_bounded(lib):
     """The K/V tiles of all units are numbered in 32 bits."""
     assert _tree(lib, S=4096, T=4096 * 1000, mq=1000, words=32, H=64, Hkv=1, maxb=1 << 20) == UNS
-    assert _tree(lib, T=2000000, mq=2000000, H=2000, Hkv=1) == UNS
+    assert _tree(lib, T=2000000, mq=2000000, H=2000, Hkv=20) == UNS
 
 
 def test_workspace_size(lib):
@@ -119,6 +120,13 @@ def test_workspace_size(lib):
     assert size(4, 64, 8, 2, 128) == size(4, 100000, 8, 2, 128) == size(4096, 2147483647, 8, 2, 128)
     need = size(4, 4, 8, 2, 128)
     assert _tree(lib, wsb=need - 1) == WS
+
+
+def test_new_lengths_are_an_array_of_their_own(lib):
+    assert _accept(lib, sl=48, cu=64, path=80, pl=96, new=48) == INV
+    for x in ("sl", "cu", "path", "pl"):
+        a = dict(sl=48, cu=64, path=80, pl=96)
+        assert _accept(lib, new=a[x], **a) == INV, x
 
 
 def test_helpers_refuse_sections_that_do_not_fit():

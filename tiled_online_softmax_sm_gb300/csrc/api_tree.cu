@@ -49,7 +49,7 @@ fa_status check_caches(const char* fn, const void* k_cache, const void* v_cache,
   if ((k_scale == nullptr) != (v_scale == nullptr))
     return fail(FA_ERR_INVALID_ARG, "%s: one of k_scale and v_scale is null", fn);
   if (num_pages == 0) return fail(FA_ERR_INVALID_ARG, "%s: empty page pool", fn);
-  if ((long long)num_pages * Hkv * 16 > kInt || num_layers > 65535)
+  if ((long long)num_pages * Hkv * 16 > kInt || num_layers > 65535 || Hkv > 65536)
     return fail(FA_ERR_UNSUPPORTED, "%s: page pool or layers too large", fn);
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 16) || !aligned(v_scale, 16))
     return fail(FA_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
@@ -107,8 +107,8 @@ fa_status rows_setup(const char* fn, const void* q, const void* k, const void* q
   if (q == nullptr || k == nullptr || q_out == nullptr) return fail(FA_ERR_INVALID_ARG, "%s: null pointer", fn);
   if (rot_dim > 0 && (cos_sin == nullptr || positions == nullptr || max_positions == 0))
     return fail(FA_ERR_INVALID_ARG, "%s: a rotation needs cos_sin and positions", fn);
-  if ((long long)H + 2ll * Hkv > kInt || (long long)total * ((long long)H + 2ll * Hkv) > kInt)
-    return fail(FA_ERR_UNSUPPORTED, "%s: total*(H + 2*Hkv) must stay below 2^31", fn);
+  if (H > 65536 || Hkv > 65536 || (long long)total * ((long long)H + 2ll * Hkv) > kInt)
+    return fail(FA_ERR_UNSUPPORTED, "%s: H, Hkv <= 65536, total*(H + 2*Hkv) below 2^31", fn);
   if (q_stride < (long long)H * d || k_stride < (long long)Hkv * d || q_stride % 8 != 0 || k_stride % 8 != 0)
     return fail(FA_ERR_INVALID_ARG, "%s: q_stride=%lld k_stride=%lld (multiples of 8, at least heads*d)", fn,
                 q_stride, k_stride);
@@ -257,12 +257,12 @@ fa_status fa_paged_tree_attention(const void* q, const void* k_cache, const void
     return fail(FA_ERR_WORKSPACE, "%s: workspace %p of %zu bytes (need %zu, 256-byte aligned)", fn, workspace,
                 workspace_bytes, need);
   if (max_seqlen_q > total_q) max_seqlen_q = total_q;   // no sequence has more
-  // rows, mask words and positions in the list of K/V tiles (at most 3 a tile and 4 a
-  // unit of two query tiles) are numbered in 32 bits
+  // rows, mask words and positions in the list of K/V tiles (at most 3 a tile and 6 a
+  // unit) are numbered in 32 bits
   const long long nodes = 2 * (128 / (H / Hkv));
   const double units = (double)num_seqs * Hkv * (double)((max_seqlen_q + nodes - 1) / nodes);
   if ((long long)total_q * H > kInt || (long long)total_q * mask_words > kInt ||
-      units * (3.0 * ((max_blocks_per_seq + 7) / 8) + 4.0) > (double)kInt)
+      units * (3.0 * ((max_blocks_per_seq + 7) / 8) + 6.0) > (double)kInt)
     return fail(FA_ERR_UNSUPPORTED, "%s: total_q*H, total_q*mask_words or the K/V tiles of all units exceed 2^31", fn);
   fa::TreeAttnParams p{q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, mask, o, lse, num_seqs, total_q,
                        max_seqlen_q, mask_words, H, Hkv, d, num_pages, max_blocks_per_seq, scale, workspace,
@@ -292,7 +292,8 @@ fa_status fa_paged_kv_accept(void* k_cache, void* v_cache, void* k_scale, void* 
     return fail(FA_ERR_INVALID_ARG, "%s: null pointer", fn);
   if (!aligned(path, 4) || !aligned(path_lens, 4) || !aligned(new_seq_lens, 4))
     return fail(FA_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
-  if (new_seq_lens == seq_lens) return fail(FA_ERR_INVALID_ARG, "%s: new_seq_lens is seq_lens", fn);
+  if (new_seq_lens == seq_lens || new_seq_lens == cu_seqlens || new_seq_lens == path || new_seq_lens == path_lens)
+    return fail(FA_ERR_INVALID_ARG, "%s: new_seq_lens is one of the inputs", fn);
   if ((long long)num_seqs * num_layers > kInt)
     return fail(FA_ERR_UNSUPPORTED, "%s: num_seqs*num_layers must stay below 2^31", fn);
   fa::KvAcceptParams p{{k_cache, v_cache, k_scale, v_scale, num_layers, Hkv, k_scale != nullptr ? d : 2 * d,
