@@ -600,7 +600,8 @@ fa_status fa_paged_qkv_write(const void* q, const void* k, const void* v, const 
                              int num_pages, int max_blocks_per_seq, void* stream);
 
 /*
- * fa_paged_tree_workspace_size — bytes of workspace fa_paged_tree_attention needs
+ * fa_paged_tree_workspace_size — bytes of workspace fa_paged_tree_attention and
+ * fa_paged_tree_attention_e4m3 need
  * (0 on invalid sizes): partials of the units whose keys are split.
  */
 size_t fa_paged_tree_workspace_size(int num_seqs, int max_seqlen_q, int H, int Hkv, int d);
@@ -639,6 +640,23 @@ fa_status fa_paged_tree_attention(const void* q, const void* k_cache, const void
                                   int Hkv, int d, int page_size, int num_pages,
                                   int max_blocks_per_seq, float scale, void* workspace,
                                   size_t workspace_bytes, void* stream);
+
+/*
+ * fa_paged_tree_attention_e4m3 — the same over the e4m3 paged cache
+ * (fa_paged_kv_write_e4m3 fills it): K and V are the values that
+ * fa_paged_kv_read_e4m3 returns.
+ *   k_cache, v_cache, k_scale, v_scale  as fa_paged_prefill_e4m3
+ * The other arguments, the conventions and the limits are as for
+ * fa_paged_tree_attention.
+ */
+fa_status fa_paged_tree_attention_e4m3(const void* q, const void* k_cache, const void* v_cache,
+                                       const void* k_scale, const void* v_scale,
+                                       const int* block_table, const int* seq_lens,
+                                       const int* cu_seqlens_q, const int* mask, void* o, float* lse,
+                                       int num_seqs, int total_q, int max_seqlen_q, int mask_words,
+                                       int H, int Hkv, int d, int page_size, int num_pages,
+                                       int max_blocks_per_seq, float scale, void* workspace,
+                                       size_t workspace_bytes, void* stream);
 
 /*
  * fa_paged_kv_accept — the accepted path's rows moved behind the context.

@@ -10,7 +10,7 @@ from test_gpu_debug_build import CHILD, ROOT
 
 pytestmark = pytest.mark.gpu
 
-CASES = ["tests/test_gpu_tree_attention.py", "tests/test_gpu_tree_cache.py"]
+CASES = ["tests/test_gpu_tree_attention.py", "tests/test_gpu_tree_cache.py", "tests/test_gpu_tree_e4m3.py"]
 
 
 def test_debug_build_passes_the_tree_cases():

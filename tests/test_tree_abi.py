@@ -44,6 +44,12 @@ def _tree(lib, q=16, kc=16, vc=16, bt=16, sl=16, cu=16, mask=16, o=16, lse=16, S
                                        scale, ws, wsb, None)
 
 
+def _tree8(lib, q=16, kc=16, vc=16, ks=16, vs=16, bt=16, sl=16, cu=16, mask=16, o=16, lse=16, S=4, T=10, mq=4, words=1,
+           H=8, Hkv=2, d=128, page=16, P=100, maxb=8, scale=0.1, ws=256, wsb=1 << 30):
+    return lib.fa_paged_tree_attention_e4m3(q, kc, vc, ks, vs, bt, sl, cu, mask, o, lse, S, T, mq, words, H, Hkv, d,
+                                            page, P, maxb, scale, ws, wsb, None)
+
+
 def _accept(lib, kc=16, vc=16, ks=None, vs=None, bt=16, sl=16, cu=16, path=16, pl=16, new=32, S=4, T=10, mp=4, layers=1,
             Hkv=2, d=128, page=16, P=100, maxb=8):
     return lib.fa_paged_kv_accept(kc, vc, ks, vs, bt, sl, cu, path, pl, new, S, T, mp, layers, Hkv, d, page, P, maxb,
@@ -94,6 +100,15 @@ def test_refusals(lib, call):
         assert lib.fa_last_error(), kw
         tried += 1
     assert tried >= 5
+
+
+def test_refusals_e4m3(lib):
+    for kw, status in REFUSED:
+        if _takes(_tree8, kw) and kw not in (dict(ks=16), dict(vs=16)):
+            assert _tree8(lib, **kw) == status, kw
+    for kw in (dict(ks=None), dict(vs=None), dict(ks=None, vs=None), dict(ks=24), dict(vs=8)):
+        assert _tree8(lib, **kw) == INV, kw
+    assert _tree8(lib, S=0, ks=None, vs=None) == OK and _tree8(lib, T=0, ks=None, vs=None, ws=None) == OK
 
 
 def test_empty_calls(lib):

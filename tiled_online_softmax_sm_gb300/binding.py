@@ -10,7 +10,8 @@ library is missing or cannot be loaded, the first call raises.
 The helpers at the end (``forward``, ``forward_f32``, ``forward_varlen``,
 ``paged_decode``, ``paged_decode_fused``, the e4m3 cache's ``paged_..._e4m3``,
 ``split_combine``, and those of drafted trees: ``tree_layout``, ``qk_norm_rope``,
-``paged_qkv_write``, ``paged_tree_attention``, ``paged_kv_accept``,
+``paged_qkv_write``, ``paged_tree_attention``,
+``paged_tree_attention_e4m3``, ``paged_kv_accept``,
 ``paged_copy_pages``) allocate outputs with torch and then call the same entry
 points.  Only they and a call's default stream import torch: the entry points
 themselves, with plain addresses and a given stream, do without it.
@@ -43,8 +44,8 @@ EXPORTED = ("fa_forward", "fa_forward_fp8", "fa_forward_f32", "fa_forward_varlen
             "fa_paged_kv_write_e4m3", "fa_paged_kv_read_e4m3", "fa_paged_e4m3_workspace_size",
             "fa_paged_e4m3_workspace_used", "fa_paged_decode_e4m3", "fa_paged_prefill_e4m3",
             "fa_tree_layout", "fa_qk_norm_rope", "fa_paged_qkv_write", "fa_paged_tree_workspace_size",
-            "fa_paged_tree_attention", "fa_paged_kv_accept", "fa_paged_copy_pages",
-            "fa_last_error",
+            "fa_paged_tree_attention", "fa_paged_tree_attention_e4m3", "fa_paged_kv_accept",
+            "fa_paged_copy_pages", "fa_last_error",
             "fa_get_device_status")
 FA_NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -101,6 +102,7 @@ def load(path: str = LIB_PATH):
         lib.fa_paged_tree_workspace_size.argtypes = [I] * 5
         lib.fa_paged_tree_workspace_size.restype = Z
         lib.fa_paged_tree_attention.argtypes = [P] * 9 + [I] * 10 + [F, P, Z, P]
+        lib.fa_paged_tree_attention_e4m3.argtypes = [P] * 11 + [I] * 10 + [F, P, Z, P]
         lib.fa_paged_kv_accept.argtypes = [P] * 10 + [I] * 9 + [P]
         lib.fa_paged_copy_pages.argtypes = [P] * 5 + [I] * 6 + [P]
         lib.fa_last_error.argtypes = []
@@ -376,6 +378,17 @@ def fa_paged_tree_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqle
                                           max_seqlen_q, mask_words, H, Hkv, d, page_size, num_pages,
                                           max_blocks_per_seq, scale, _p(workspace), workspace_bytes,
                                           _stream(stream)))
+
+
+def fa_paged_tree_attention_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                                 cu_seqlens_q, mask, o, lse, num_seqs, total_q, max_seqlen_q, mask_words,
+                                 H, Hkv, d, page_size, num_pages, max_blocks_per_seq, scale, workspace,
+                                 workspace_bytes, stream=None):
+    _check(load().fa_paged_tree_attention_e4m3(_p(q), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale),
+                                               _p(block_table), _p(seq_lens), _p(cu_seqlens_q), _p(mask),
+                                               _p(o), _p(lse), num_seqs, total_q, max_seqlen_q, mask_words,
+                                               H, Hkv, d, page_size, num_pages, max_blocks_per_seq, scale,
+                                               _p(workspace), workspace_bytes, _stream(stream)))
 
 
 def fa_paged_kv_accept(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, path,
@@ -931,6 +944,45 @@ def paged_tree_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
         cu_seqlens_q.data_ptr(), mask.data_ptr(), o.data_ptr(), lse.data_ptr(), S, T, max_seqlen_q, words,
         H, Hkv, d, page, P, max_blocks, scale, workspace.data_ptr(), size, _current_raw_stream(device))
+    if rc:
+        _check(rc)
+    return o, lse
+
+
+def paged_tree_attention_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens_q,
+                              max_seqlen_q, mask, scale, workspace=None, stream=None):
+    """paged_tree_attention over the e4m3 cache [P,Hkv,16,d] with scale bytes [P,Hkv,16]."""
+    if stream is not None:
+        with _given(stream):
+            return paged_tree_attention_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                                             cu_seqlens_q, max_seqlen_q, mask, scale, workspace)
+    fn = "paged_tree_attention_e4m3"
+    device = q.get_device()
+    _check_cache(fn, device, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens)
+    P, Hkv, page, d = k_cache.shape
+    S, max_blocks = block_table.shape
+    T, H = q.shape[:2]
+    words = mask.shape[-1]
+    _check_rows(fn, device, "q", q, torch.bfloat16, (T, H, d))
+    _check_rows(fn, device, "mask", mask, torch.int32, (T, words))
+    _check_rows(fn, device, "cu_seqlens_q", cu_seqlens_q, torch.int32, (S + 1,))
+    if workspace is None:   # (a caller's own is sized for the caller's bound)
+        max_seqlen_q = min(max_seqlen_q, T)
+        size = _tree_workspace(S, max_seqlen_q, H, Hkv, d)
+        workspace = _empty(size, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise FaError(FA_ERR_WORKSPACE, f"{fn}: the workspace is on {workspace.device} with strides "
+                                        f"{workspace.stride()}")
+    else:
+        size = workspace.nbytes
+    o = torch.empty_like(q)
+    lse = _empty((H, T), dtype=_F32, device=q.device)
+    lib = _lib or load()
+    rc = lib.fa_paged_tree_attention_e4m3(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens_q.data_ptr(), mask.data_ptr(), o.data_ptr(),
+        lse.data_ptr(), S, T, max_seqlen_q, words, H, Hkv, d, page, P, max_blocks, scale,
+        workspace.data_ptr(), size, _current_raw_stream(device))
     if rc:
         _check(rc)
     return o, lse

@@ -67,6 +67,52 @@ fa_status check_table(const char* fn, const int* block_table, const int* seq_len
   return FA_OK;
 }
 
+// fa_paged_tree_attention, or (scales given) fa_paged_tree_attention_e4m3.
+fa_status tree_attention(const char* fn, const void* q, const void* k_cache, const void* v_cache,
+                         const void* k_scale, const void* v_scale, const int* block_table,
+                         const int* seq_lens, const int* cu_seqlens_q, const int* mask, void* o,
+                         float* lse, int num_seqs, int total_q, int max_seqlen_q, int mask_words, int H,
+                         int Hkv, int d, int page_size, int num_pages, int max_blocks_per_seq,
+                         float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  if (num_seqs < 0 || total_q < 0 || max_seqlen_q < 0 || num_pages < 0 || max_blocks_per_seq < 0)
+    return fail(FA_ERR_INVALID_ARG, "%s: negative size", fn);
+  if (H <= 0 || Hkv <= 0 || H % Hkv != 0)
+    return fail(FA_ERR_INVALID_ARG, "%s: H=%d Hkv=%d (need H %% Hkv == 0)", fn, H, Hkv);
+  if (mask_words < 1) return fail(FA_ERR_INVALID_ARG, "%s: mask_words=%d", fn, mask_words);
+  if (!(scale > 0.f) || scale == INFINITY)
+    return fail(FA_ERR_INVALID_ARG, "%s: scale must be positive and finite", fn);
+  fa_status st = check_dims(fn, d, page_size);
+  if (st != FA_OK) return st;
+  if (H / Hkv > 128) return fail(FA_ERR_UNSUPPORTED, "%s: H/Hkv=%d > 128", fn, H / Hkv);
+  if (num_seqs > fa::kMaxTreeSeqs)
+    return fail(FA_ERR_UNSUPPORTED, "%s: num_seqs=%d > %d", fn, num_seqs, fa::kMaxTreeSeqs);
+  if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return FA_OK;
+  if (q == nullptr || o == nullptr || mask == nullptr) return fail(FA_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if ((st = check_caches(fn, k_cache, v_cache, k_scale, v_scale, 1, Hkv, num_pages)) != FA_OK) return st;
+  if ((st = check_table(fn, block_table, seq_lens, cu_seqlens_q, max_blocks_per_seq)) != FA_OK) return st;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(mask, 4) || !aligned(lse, 4))
+    return fail(FA_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+  const size_t need = fa::tree_attn_workspace(max_seqlen_q, H, Hkv, d);
+  if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256))
+    return fail(FA_ERR_WORKSPACE, "%s: workspace %p of %zu bytes (need %zu, 256-byte aligned)", fn, workspace,
+                workspace_bytes, need);
+  if (max_seqlen_q > total_q) max_seqlen_q = total_q;   // no sequence has more
+  // rows, mask words and positions in the list of K/V tiles (at most 3 a tile and 6 a
+  // unit) are numbered in 32 bits
+  const long long nodes = 2 * (128 / (H / Hkv));
+  const double units = (double)num_seqs * Hkv * (double)((max_seqlen_q + nodes - 1) / nodes);
+  if ((long long)total_q * H > kInt || (long long)total_q * mask_words > kInt ||
+      units * (3.0 * ((max_blocks_per_seq + 7) / 8) + 6.0) > (double)kInt)
+    return fail(FA_ERR_UNSUPPORTED, "%s: total_q*H, total_q*mask_words or the K/V tiles of all units exceed 2^31", fn);
+  fa::TreeAttnParams p{q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens_q, mask, o, lse,
+                       num_seqs, total_q, max_seqlen_q, mask_words, H, Hkv, d, num_pages, max_blocks_per_seq,
+                       scale, workspace, nullptr};
+  if ((st = fa::api_status_ptr(&p.status)) != FA_OK) return st;
+  const char* why = "tree attention launch";
+  const cudaError_t e = fa::launch_tree_attn(p, static_cast<cudaStream_t>(stream), &why);
+  return launched(e, why);
+}
+
 // What fa_qk_norm_rope and fa_paged_qkv_write share; fills p.
 fa_status rows_setup(const char* fn, const void* q, const void* k, const void* q_weight,
                      const void* k_weight, const float* cos_sin, const int* positions, void* q_out,
@@ -233,44 +279,25 @@ fa_status fa_paged_tree_attention(const void* q, const void* k_cache, const void
                                   int Hkv, int d, int page_size, int num_pages,
                                   int max_blocks_per_seq, float scale, void* workspace,
                                   size_t workspace_bytes, void* stream) {
-  const char* fn = "fa_paged_tree_attention";
-  if (num_seqs < 0 || total_q < 0 || max_seqlen_q < 0 || num_pages < 0 || max_blocks_per_seq < 0)
-    return fail(FA_ERR_INVALID_ARG, "%s: negative size", fn);
-  if (H <= 0 || Hkv <= 0 || H % Hkv != 0)
-    return fail(FA_ERR_INVALID_ARG, "%s: H=%d Hkv=%d (need H %% Hkv == 0)", fn, H, Hkv);
-  if (mask_words < 1) return fail(FA_ERR_INVALID_ARG, "%s: mask_words=%d", fn, mask_words);
-  if (!(scale > 0.f) || scale == INFINITY)
-    return fail(FA_ERR_INVALID_ARG, "%s: scale must be positive and finite", fn);
-  fa_status st = check_dims(fn, d, page_size);
-  if (st != FA_OK) return st;
-  if (H / Hkv > 128) return fail(FA_ERR_UNSUPPORTED, "%s: H/Hkv=%d > 128", fn, H / Hkv);
-  if (num_seqs > fa::kMaxTreeSeqs)
-    return fail(FA_ERR_UNSUPPORTED, "%s: num_seqs=%d > %d", fn, num_seqs, fa::kMaxTreeSeqs);
-  if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return FA_OK;
-  if (q == nullptr || o == nullptr || mask == nullptr) return fail(FA_ERR_INVALID_ARG, "%s: null pointer", fn);
-  if ((st = check_caches(fn, k_cache, v_cache, nullptr, nullptr, 1, Hkv, num_pages)) != FA_OK) return st;
-  if ((st = check_table(fn, block_table, seq_lens, cu_seqlens_q, max_blocks_per_seq)) != FA_OK) return st;
-  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(mask, 4) || !aligned(lse, 4))
-    return fail(FA_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
-  const size_t need = fa::tree_attn_workspace(max_seqlen_q, H, Hkv, d);
-  if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256))
-    return fail(FA_ERR_WORKSPACE, "%s: workspace %p of %zu bytes (need %zu, 256-byte aligned)", fn, workspace,
-                workspace_bytes, need);
-  if (max_seqlen_q > total_q) max_seqlen_q = total_q;   // no sequence has more
-  // rows, mask words and positions in the list of K/V tiles (at most 3 a tile and 6 a
-  // unit) are numbered in 32 bits
-  const long long nodes = 2 * (128 / (H / Hkv));
-  const double units = (double)num_seqs * Hkv * (double)((max_seqlen_q + nodes - 1) / nodes);
-  if ((long long)total_q * H > kInt || (long long)total_q * mask_words > kInt ||
-      units * (3.0 * ((max_blocks_per_seq + 7) / 8) + 6.0) > (double)kInt)
-    return fail(FA_ERR_UNSUPPORTED, "%s: total_q*H, total_q*mask_words or the K/V tiles of all units exceed 2^31", fn);
-  fa::TreeAttnParams p{q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, mask, o, lse, num_seqs, total_q,
-                       max_seqlen_q, mask_words, H, Hkv, d, num_pages, max_blocks_per_seq, scale, workspace,
-                       nullptr};
-  if ((st = fa::api_status_ptr(&p.status)) != FA_OK) return st;
-  const char* why = "fa_paged_tree_attention launch";
-  const cudaError_t e = fa::launch_tree_attn(p, static_cast<cudaStream_t>(stream), &why);
-  return launched(e, why);
+  return tree_attention("fa_paged_tree_attention", q, k_cache, v_cache, nullptr, nullptr, block_table, seq_lens,
+                        cu_seqlens_q, mask, o, lse, num_seqs, total_q, max_seqlen_q, mask_words, H, Hkv, d,
+                        page_size, num_pages, max_blocks_per_seq, scale, workspace, workspace_bytes, stream);
+}
+
+fa_status fa_paged_tree_attention_e4m3(const void* q, const void* k_cache, const void* v_cache,
+                                       const void* k_scale, const void* v_scale,
+                                       const int* block_table, const int* seq_lens,
+                                       const int* cu_seqlens_q, const int* mask, void* o, float* lse,
+                                       int num_seqs, int total_q, int max_seqlen_q, int mask_words,
+                                       int H, int Hkv, int d, int page_size, int num_pages,
+                                       int max_blocks_per_seq, float scale, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  const char* fn = "fa_paged_tree_attention_e4m3";
+  if (num_seqs > 0 && total_q > 0 && max_seqlen_q > 0 && k_scale == nullptr && v_scale == nullptr)
+    return fail(FA_ERR_INVALID_ARG, "%s: null scales", fn);
+  return tree_attention(fn, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens_q, mask, o,
+                        lse, num_seqs, total_q, max_seqlen_q, mask_words, H, Hkv, d, page_size, num_pages,
+                        max_blocks_per_seq, scale, workspace, workspace_bytes, stream);
 }
 
 fa_status fa_paged_kv_accept(void* k_cache, void* v_cache, void* k_scale, void* v_scale,

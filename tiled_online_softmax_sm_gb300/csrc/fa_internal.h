@@ -323,12 +323,14 @@ cudaError_t launch_kv_accept(const KvAcceptParams& p, cudaStream_t stream);
 cudaError_t launch_copy_pages(const KvMoveParams& c, const int* pairs, int num_pairs,
                               cudaStream_t stream);
 
-// Attention of drafted nodes over the bf16 paged cache.
+// Attention of drafted nodes over a paged cache: bf16, or e4m3 where k_scale is given.
 constexpr int kMaxTreeSeqs = 4096;
 struct TreeAttnParams {
   const void* q;
   const void* k_cache;
   const void* v_cache;
+  const void* k_scale;
+  const void* v_scale;
   const int* block_table;
   const int* seq_lens;
   const int* cu_q;

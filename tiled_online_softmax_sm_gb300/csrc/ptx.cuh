@@ -325,6 +325,14 @@ __device__ __forceinline__ void widen16(const uint4& x, uint32_t b, uint4& lo, u
   hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
+// 16 bytes into shared memory, and an arrival when this thread's copies so far are there.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // Pack two floats into bf16x2 (round to nearest even); `lo` lands in the low half.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;

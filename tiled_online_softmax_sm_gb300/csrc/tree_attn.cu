@@ -1,4 +1,4 @@
-// Attention of drafted nodes over the bf16 paged cache, on the tcgen05 tensor
+// Attention of drafted nodes over a paged cache, bf16 or e4m3, on the tcgen05 tensor
 // cores: node i of a sequence sees every key of the context (the first p0 = L - n
 // tokens) and the nodes whose bit is set in its row of the mask.
 //
@@ -22,6 +22,7 @@
 //                behind its waits and commits)
 //   warp 3       V rows that no node sees are zeroed before the MMA reads them
 //   warps 4-11   softmax, thread = query row = tensor-memory lane
+//   warps 12-19  e4m3 cache: K and V are widened to bf16 (warp 3 then has no work)
 //
 // The two softmax warpgroups w have a score tile S_w and an accumulator O_w each.
 // A unit of two query tiles gives one to each (every K/V tile is used by both); a
@@ -34,7 +35,7 @@
 // and of the bf16-rounded p that the P V MMA multiplies for O.
 //
 // Measured (d = 128, 32 heads of 8, contexts uniform on the range): 64 x 16 nodes over
-// [512, 8192] tokens, one query tile a unit, 177 us for 1.04 GB (5.9 TB/s, 0.88 of a
+// [512, 8192] tokens, one query tile a unit, 175 us for 1.04 GB (6.0 TB/s, 0.89 of a
 // plain copy; a unit's beginning and end cost as much as three K/V tiles of 350). 4 x
 // [48, 64] nodes over [16384, 65536], two query tiles, 128 us for 0.56 GB (4.4 TB/s):
 // a K/V tile's MMAs for 256 rows take 2050 clocks at d = 128 (3070 in halves) and its
@@ -43,6 +44,13 @@
 // shared through L2, took longer (157 us): L2 delivers every K/V tile twice.  What the
 // roles' loops have in common is the instruction cache: with the softmax loops
 // unrolled over a whole tile the issuers' code was pushed out of it (64 x 16 198 us).
+// A small call (1 x 8 nodes over 1000 tokens, 12 us) is start-up: code that is read for
+// the first time, the list, one chain of copy, scores, softmax, values and the merge.
+// From the e4m3 cache, half the bytes, the same two take 236 and 154 us: widening 128 x 128
+// codes keeps the integer and conversion pipes of an SM busy for some 1000 clocks, a tile
+// of K and one of V, beside the softmax.  One warpgroup for it took 246 and 160 us, codes
+// widened by integer instructions and a bf16 product 290 and 178, four rows a step
+// instead of two 283 and 162 (the instruction cache again).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -58,7 +66,6 @@ namespace {
 
 constexpr int kPage = 16;
 constexpr int kTile = 128;        // keys of a K/V tile, rows of a query tile
-constexpr int kThreads = 384;
 constexpr int kCtas = 152;        // one per SM
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -67,17 +74,29 @@ constexpr float kLn2 = 0.6931471805599453f;
 // tensor memory.
 constexpr float kRaise = 24.f;
 
-template <int D>
+// E4M3: K and V come from the e4m3 cache.  Warp 0 then stages their codes and scale
+// bytes, and two more warpgroups widen them to bf16 (exactly: a code has 4 significant
+// bits and its scale is a power of two) into the ring that the MMAs read.
+template <int D, bool PAIRS, bool E4M3>
 struct Cfg {
+  static constexpr int kThreads = E4M3 ? 640 : 384;
   static constexpr int kChunks = D / 64;             // 128-byte pieces of a row
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kStages = D == 128 ? 4 : 8;   // K/V ring slots
+  static constexpr int kStages = D == 64 ? (E4M3 ? 6 : 8) : E4M3 ? 3 : 4;   // K/V ring slots
+  static constexpr int kQ = E4M3 && !PAIRS ? 1 : 2;        // query tiles
+  static constexpr int kRawTile = kTile * D + kTile;       // staged codes and scale bytes
+  static constexpr int kRawStages = !E4M3 ? 0 : D == 64 ? 6 : PAIRS ? 2 : 4;   // tiles staged
   // K/V tiles are laid out in groups of eight keys, a group's 1 KB pieces (64
   // values of each key) side by side, so that one copy brings a whole page
   static constexpr int kGroup = 1024 * kChunks;
-  static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;   // + alignment slack
+  static constexpr int kSmem = (kQ + kStages) * kTileBytes + kRawStages * kRawTile + 1024;   // + alignment slack
   static constexpr uint32_t kIdescO = ptx::idesc_bf16_f32(128, D, false, true);
 };
+
+// Registers of the E4M3 instances: 640 threads at 96, split again among copies and
+// issuers, softmax, and widening.
+constexpr int kRegsIssue = 64, kRegsSoftmax = 152, kRegsWiden = 56;
+static_assert(kRegsIssue + 2 * kRegsSoftmax + 2 * kRegsWiden <= 5 * 96, "register split");
 
 // The unit whose first tile lies in a CTA's piece and whose last one in a later one's.
 struct Cut {
@@ -88,6 +107,8 @@ struct Cut {
 
 struct Args {
   const __nv_bfloat16* q;
+  const uint8_t* codes[2];   // E4M3: of K and V, and their scale bytes
+  const uint8_t* scales[2];
   const int* block_table;
   const int* seq_lens;
   const int* cu_q;
@@ -155,6 +176,7 @@ __device__ __forceinline__ int seq_cost(const Args& a, const Seq& Q, bool weighe
 struct Shared {
   int pre[kMaxTreeSeqs + 1];   // cost of sequences 0 .. s - 1
   int warp_sum[2][32];
+  uint64_t raw_full[8], raw_empty[8];   // E4M3: staged tiles
   uint64_t q_full[2], q_empty[2];   // Q tile i
   uint64_t kv_full[8], kv_empty[8]; // ring slots
   uint64_t fix_full[8];             // ring slots: a V tile landed that is to be cleaned
@@ -247,12 +269,12 @@ __device__ __forceinline__ float sum_packed(const uint32_t (&p)[16]) {
   return (x0 + x1) + (x2 + x3);
 }
 
-template <int D, bool PAIRS>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, bool PAIRS, bool E4M3>
+__global__ void __launch_bounds__(Cfg<D, PAIRS, E4M3>::kThreads, 1)
 tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const Args a) {
-  using C = Cfg<D>;
-  constexpr int kStages = C::kStages;
+  using C = Cfg<D, PAIRS, E4M3>;
+  constexpr int kStages = C::kStages, kThreads = C::kThreads, kRawStages = E4M3 ? C::kRawStages : 1;
   // Scores are formed and used in parts of a K/V tile: halves where units have two query
   // tiles, so that a softmax warpgroup works on one half while the other is multiplied (an
   // MMA of 64 columns takes as long as one of 128, but waiting costs more: 4 x 64 nodes
@@ -263,7 +285,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sQ = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
-  uint8_t* sKV = sQ + 2 * C::kTileBytes;
+  uint8_t* sKV = sQ + C::kQ * C::kTileBytes;
+  uint8_t* sRaw = sKV + kStages * C::kTileBytes;
   __shared__ Shared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* const status = a.status;
@@ -271,6 +294,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const uint32_t bar_q = ptx::smem_u32(sh.q_full), bar_qe = ptx::smem_u32(sh.q_empty);
   const uint32_t bar_kvf = ptx::smem_u32(sh.kv_full), bar_kve = ptx::smem_u32(sh.kv_empty);
   const uint32_t bar_fix = ptx::smem_u32(sh.fix_full);
+  const uint32_t bar_rf = ptx::smem_u32(sh.raw_full), bar_re = ptx::smem_u32(sh.raw_empty);
   const uint32_t bar_s = ptx::smem_u32(sh.s_full), bar_p = ptx::smem_u32(sh.p_full);
   const uint32_t bar_pv = ptx::smem_u32(sh.pv_done), bar_o = ptx::smem_u32(sh.o_done), bar_oe = ptx::smem_u32(sh.o_empty);
   const uint32_t bar_sf = ptx::smem_u32(&sh.stat_full), bar_se = ptx::smem_u32(&sh.stat_empty);
@@ -298,9 +322,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       ptx::mbar_init(bar_oe + 8 * i, kTile);
       ptx::mbar_init(bar_drain + 8 * i, 1);
     }
+    for (int i = 0; i < (E4M3 ? kRawStages : 0); ++i) {
+      ptx::mbar_init(bar_rf + 8 * i, 33);   // the codes' bytes and each lane's scale bytes
+      ptx::mbar_init(bar_re + 8 * i, 8);
+    }
 #pragma unroll 1
     for (int i = 0; i < kStages; ++i) {
-      ptx::mbar_init(bar_kvf + 8 * i, 1);
+      ptx::mbar_init(bar_kvf + 8 * i, E4M3 ? 8 : 1);   // (an arrival of each widening warp)
       ptx::mbar_init(bar_kve + 8 * i, 2);
       ptx::mbar_init(bar_fix + 8 * i, 1);
     }
@@ -374,7 +402,22 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   }
 
   int x = list.xb, s = s_first;
-  Seg S;
+  Seg S{};
+  if constexpr (E4M3) {
+    if (warp < 4) ptx::setmaxnreg_dec<kRegsIssue>();
+    else if (warp < 12) ptx::setmaxnreg_inc<kRegsSoftmax>();
+    else ptx::setmaxnreg_dec<kRegsWiden>();
+  }
+  // Which nodes' V rows any node of the segment's unit sees, of keys k0 .. k0 + 127 (lane c:
+  // 32 of them, c mod 4); the others may hold anything, and 0 * NaN is NaN.
+  auto seen_of = [&](int k0) __attribute__((always_inline)) -> uint32_t {
+    uint32_t seen = 0u;
+#pragma unroll 1
+    for (int i = S.node0 + (lane >> 2); i < S.node0 + S.nodes; i += 8) seen |= sees(a, S.Q, i, k0 + 32 * (lane & 3));
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) seen |= __shfl_xor_sync(0xffffffffu, seen, o);
+    return seen;
+  };
   if (warp == 0) {
     // -------------------------------------------------------------- copies
     int li = 0;                 // tiles issued
@@ -402,7 +445,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         __syncwarp();
       }
       if (!ok) break;
-      if (!S.pair) half ^= 1;
+      if (!S.pair && C::kQ == 2) half ^= 1;
       const int* ids = a.block_table + (size_t)S.s * a.max_blocks;
       // (lane pg: page pg of tile j)
       auto look_up = [&](int j) {
@@ -413,6 +456,24 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (lane < npages && (id < 0 || id >= a.num_pages)) {
           atomicExch(status, kDevBadBlockTable);
           id = 0;
+        }
+        if constexpr (E4M3) {
+          const int rslot = li % kRawStages;
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_re + 8 * rslot, ((li / kRawStages) & 1) ^ 1, status,
+                                                      abort_flag));
+          if (!ok) return;
+          const uint32_t bar = bar_rf + 8 * rslot, dst = ptx::smem_u32(sRaw) + rslot * C::kRawTile;
+          if (lane == 0 && !skip) ptx::mbar_arrive_expect_tx(bar, npages * kPage * D);
+          __syncwarp();
+          if (lane < npages && !skip) {
+            const size_t row = (size_t)(id * a.Hkv + S.g) * kPage;
+            ptx::bulk_load(dst + lane * kPage * D, (which ? a.codes[1] : a.codes[0]) + row * D, kPage * D, bar);
+            ptx::cp_async16(dst + kTile * D + lane * kPage, (which ? a.scales[1] : a.scales[0]) + row);
+          }
+          if (!skip) ptx::cp_async_arrive(bar);
+          skip = false;
+          ++li;
+          return;
         }
         const int slot = li % kStages;
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar_kve + 8 * slot, ((li / kStages) & 1) ^ 1, status,
@@ -446,7 +507,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
     }
     if (!ok && lane == 0) {   // let the copies in flight land before shared memory is released
-      for (int l = max(0, li - kStages); l < li; ++l) {
+      for (int l = max(0, li - kRawStages); E4M3 && l < li; ++l)
+        ptx::mbar_wait(bar_rf + 8 * (l % kRawStages), (l / kRawStages) & 1, nullptr);
+      for (int l = max(0, li - kStages); !E4M3 && l < li; ++l) {
         const int slot = l % kStages;
         if (to_fix >> slot & 1u) ptx::mbar_wait(bar_fix + 8 * slot, (fixes >> slot & 1u) ^ 1u, nullptr);
         else ptx::mbar_wait(bar_kvf + 8 * slot, (l / kStages) & 1, nullptr);
@@ -513,7 +576,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           ++nq[i];
           if (ok && (i != qb || j0 >= nt)) ptx::mbar_arrive(bar_qe + 8 * i);
         }
-        if (!S.pair) half ^= 1;
+        if (!S.pair && C::kQ == 2) half ^= 1;
         auto k_done = [&](int l, bool last) {      // all of K's scores are on their way
           ptx::tc_commit(bar_kve + 8 * (l % kStages));
           if (last) ptx::tc_commit(bar_qe + 8 * qb);
@@ -560,21 +623,15 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       ptx::mbar_wait(bar_drain + 8 * w, 0, nullptr);
     }
     __syncwarp();
-  } else if (warp == 3) {
+  } else if (!E4M3 && warp == 3) {
     // ------------------------------------------------- V rows nobody sees
-    // Their weights are exactly 0, but they may hold anything and 0 * NaN is NaN.
     int lc = 0;
     uint32_t fixes = 0u;   // parity of each slot's copies to the fix barrier
     bool ok = true;
     while (ok && next_segment<PAIRS>(a, list, x, s, S)) {
-      const int i0 = S.node0, i1 = S.node0 + S.nodes;
       const int fix0 = (S.Q.L - S.Q.n) / kTile;   // first tile with nodes
       for (int j = max(S.j0, fix0); j < S.j1; ++j) {
-        // lane: the union over every eighth node of 32 keys' bits
-        uint32_t seen = 0u;
-        for (int i = i0 + (lane >> 2); i < i1; i += 8) seen |= sees(a, S.Q, i, j * kTile + 32 * (lane & 3));
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) seen |= __shfl_xor_sync(0xffffffffu, seen, o);
+        const uint32_t seen = seen_of(j * kTile);
         const int slot = (lc + copy_v(S.pair, j - S.j0, S.j1 - S.j0)) % kStages;
         ok = __all_sync(0xffffffffu,
                         ptx::mbar_wait(bar_fix + 8 * slot, fixes >> slot & 1u, status, abort_flag));
@@ -605,7 +662,76 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
       lc += 2 * (S.j1 - S.j0);
     }
-  } else if (warp >= 4) {
+  } else if (E4M3 && warp >= 12) {
+    if constexpr (E4M3) {
+      // ---------------------------------------------------------- widening
+      // 16 codes of a row (a 16-byte unit) become two units of its bf16 row, where the
+      // MMAs' swizzle puts them; rows of V that no node sees become zeros.
+      constexpr int kStep = 256 / (D / 16), kB = 2;   // rows a step, steps at once
+      const int tid = threadIdx.x - 12 * 32;
+      // (d = 128: eight lanes take a half of a row and the other half of the next one, which
+      // lie in different banks here and there)
+      const int un = D == 128 ? (lane & 3) | ((lane >> 2 ^ lane >> 3) & 1) << 2 : lane & 3;
+      const int row0 = D == 128 ? (tid >> 5) * 4 + (lane >> 2 & 1) + (lane >> 4) * 2 : tid >> 2;
+      int lc = 0;
+      bool ok = true;
+      while (ok && next_segment<PAIRS>(a, list, x, s, S)) {
+        const int ahead = S.pair ? 1 : 2;
+        int kj = S.j0, vj = S.j0;
+        while (vj < S.j1 && ok) {                            // in the copies' order
+          const bool is_v = !(kj < S.j1 && kj < vj + ahead);
+          const int j = is_v ? vj++ : kj++;
+          const int slot = lc % kStages, rslot = lc % kRawStages;
+          const bool cleaned = is_v && (j + 1) * kTile > S.Q.L - S.Q.n;
+          const uint32_t seen = cleaned ? seen_of(j * kTile) : 0u;
+          ok = __all_sync(0xffffffffu,
+                          ptx::mbar_wait(bar_rf + 8 * rslot, (lc / kRawStages) & 1, status, abort_flag) &&
+                              ptx::mbar_wait(bar_kve + 8 * slot, ((lc / kStages) & 1) ^ 1, status, abort_flag));
+          if (!ok) break;
+          const uint8_t* raw = sRaw + rslot * C::kRawTile;
+          uint8_t* tile = sKV + slot * C::kTileBytes;
+          auto put = [&](int r, const uint4& lo, const uint4& hi) {
+            uint8_t* at = tile + (r >> 3) * C::kGroup + (un >> 2) * 1024 + (r & 7) * 128;
+            *reinterpret_cast<uint4*>(at + (((2 * un) & 7) ^ (r & 7)) * 16) = lo;
+            *reinterpret_cast<uint4*>(at + (((2 * un + 1) & 7) ^ (r & 7)) * 16) = hi;
+          };
+#pragma unroll 1
+          for (int r0 = row0; r0 < kTile; r0 += kB * kStep) {
+            uint4 c[kB];
+            uint32_t b[kB];
+#pragma unroll
+            for (int i = 0; i < kB; ++i) {
+              c[i] = *reinterpret_cast<const uint4*>(raw + (r0 + i * kStep) * D + un * 16);
+              b[i] = raw[kTile * D + r0 + i * kStep];
+            }
+            if (cleaned) {
+#pragma unroll
+              for (int i = 0; i < kB; ++i) {
+                const int r = r0 + i * kStep;
+                if (!(__shfl_sync(0xffffffffu, seen, r >> 5) >> (r & 31) & 1u)) {
+                  c[i] = make_uint4(0u, 0u, 0u, 0u);
+                  b[i] = 0u;
+                }
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < kB; ++i) {
+              uint4 lo, hi;
+              ptx::widen16(c[i], b[i], lo, hi);
+              put(r0 + i * kStep, lo, hi);
+            }
+          }
+          ptx::fence_proxy_async_smem();   // the MMA (and the next copy) come behind these accesses
+          __syncwarp();
+          if (lane == 0) {
+            ptx::mbar_arrive(bar_kvf + 8 * slot);
+            ptx::mbar_arrive(bar_re + 8 * rslot);
+          }
+          ++lc;
+        }
+      }
+    }
+  } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------ softmax
     const int w = (warp - 4) >> 2;          // warpgroup
     const int quarter = warp & 3;           // tensor-memory lane quarter
@@ -936,9 +1062,10 @@ int row_cap(int max_q, int G) {
 }
 constexpr size_t kCutBytes = (kCtas * sizeof(Cut) + 255) / 256 * 256;
 
-template <int D>
+template <int D, bool E4M3>
 cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream, const char** why) {
-  using C = Cfg<D>;
+  using C = Cfg<D, true, E4M3>;
+  using C1 = Cfg<D, false, E4M3>;
   CUtensorMap tmQ, tmK, tmV;
   // (value of 64, key of 8, piece of 64 values, group of 8 keys): one box = a page of
   // one kv head, in the order of the tile
@@ -950,25 +1077,32 @@ cudaError_t launch(const TreeAttnParams& p, cudaStream_t stream, const char** wh
   const uint64_t q_dims[3] = {(uint64_t)D, (uint64_t)p.H, (uint64_t)p.total_q};
   const uint64_t q_strides[2] = {(uint64_t)D * 2, (uint64_t)p.H * D * 2};
   const uint32_t q_box[3] = {64, (uint32_t)G, (uint32_t)tile_nodes};
-  if (!make_tmap_bf16(&tmQ, p.q, 3, q_dims, q_strides, q_box) ||
-      !make_tmap_bf16(&tmK, p.k_cache, 4, dims, strides, box) ||
-      !make_tmap_bf16(&tmV, p.v_cache, 4, dims, strides, box)) {
+  bool made = make_tmap_bf16(&tmQ, p.q, 3, q_dims, q_strides, q_box);
+  if constexpr (E4M3) tmK = tmV = tmQ;   // unused: pages are copied untiled
+  else made = made && make_tmap_bf16(&tmK, p.k_cache, 4, dims, strides, box) &&
+              make_tmap_bf16(&tmV, p.v_cache, 4, dims, strides, box);
+  if (!made) {
     *why = "tensor map for the queries and caches";
     return cudaErrorInvalidValue;
   }
-  Args a{static_cast<const __nv_bfloat16*>(p.q), p.block_table, p.seq_lens, p.cu_q, p.mask,
+  const auto bytes = [](const void* x) { return static_cast<const uint8_t*>(x); };
+  Args a{static_cast<const __nv_bfloat16*>(p.q), {bytes(p.k_cache), bytes(p.v_cache)},
+         {bytes(p.k_scale), bytes(p.v_scale)}, p.block_table, p.seq_lens, p.cu_q, p.mask,
          static_cast<__nv_bfloat16*>(p.o), p.lse, p.num_seqs, p.total_q, p.max_q, p.words, p.H, p.Hkv, G,
-         tile_nodes, p.num_pages, p.max_blocks, ((1ull << 40) + 2 * tile_nodes - 1) / (2 * tile_nodes), p.scale * kLog2e, skip_first_copy_for_tests(), p.status,
+         tile_nodes, p.num_pages, p.max_blocks, ((1ull << 40) + 2 * tile_nodes - 1) / (2 * tile_nodes), p.scale * kLog2e,
+         skip_first_copy_for_tests(), p.status,
          nullptr, nullptr, nullptr, row_cap(p.max_q, G)};
   char* ws = static_cast<char*>(p.workspace);
   a.cuts = reinterpret_cast<Cut*>(ws);
   a.part_s = reinterpret_cast<float4*>(ws + kCutBytes);
   a.part_o = a.part_s + (size_t)2 * kCtas * a.row_cap;
   // (without units of two query tiles the kernel is the smaller one)
-  auto kernel = p.max_q > tile_nodes ? tree_attn_kernel<D, true> : tree_attn_kernel<D, false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  const bool pairs = p.max_q > tile_nodes;
+  auto kernel = pairs ? tree_attn_kernel<D, true, E4M3> : tree_attn_kernel<D, false, E4M3>;
+  const int smem = pairs ? C::kSmem : C1::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) {
-    kernel<<<kCtas, kThreads, C::kSmem, stream>>>(tmQ, tmK, tmV, a);
+    kernel<<<kCtas, C::kThreads, smem, stream>>>(tmQ, tmK, tmV, a);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) {
@@ -996,7 +1130,8 @@ size_t tree_attn_workspace(int max_q, int H, int Hkv, int d) {
 }
 
 cudaError_t launch_tree_attn(const TreeAttnParams& p, cudaStream_t stream, const char** why) {
-  return p.d == 128 ? launch<128>(p, stream, why) : launch<64>(p, stream, why);
+  if (p.k_scale != nullptr) return p.d == 128 ? launch<128, true>(p, stream, why) : launch<64, true>(p, stream, why);
+  return p.d == 128 ? launch<128, false>(p, stream, why) : launch<64, false>(p, stream, why);
 }
 
 }  // namespace fa
