@@ -17,6 +17,11 @@ Workloads (sizes as in the bench and the parity tests):
   draft_e4m3   4 new tokens of 16 sequences over an e4m3 cache
   prefill_e4m3 512-token chunks of those sequences
   window_c3    causal bf16 forward, n=m=8192 H=32 d=128, window 1024 with 4 sinks
+  tree_c4      attention of 16 drafted nodes of each of the decode pool's 64 sequences
+  tree_e4m3    the same over an e4m3 cache
+  tree_long    64 drafted nodes of 4 sequences of [16384, 65536] tokens
+  qkv_rows     q, k and v rows of 16 x 1024 new tokens: norms, rotation and cache write
+  copy_pages   2048 pages of a bf16 cache (64 KB each with K and V) copied
 Inputs come from the same seeded generators; nothing is checked here.
 """
 from __future__ import annotations
@@ -57,6 +62,29 @@ def e4m3_cache(seed: int, S: int, Hkv: int = 8, d: int = 128):
 
 def offsets(n):
     return torch.from_numpy(np.concatenate([[0], np.cumsum(n)]).astype(np.int32)).cuda()
+
+
+def bf16_cache(lens, Hkv: int = 8, d: int = 128, seed: int = I.BASE_SEED):
+    """Random pages for sequences of these lengths, their table (randomly ordered pages) and lengths."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    need = (np.asarray(lens) + 15) // 16
+    table = np.full((len(lens), int(need.max())), -1, np.int32)
+    ids = np.random.default_rng(seed).permutation(int(need.sum())).astype(np.int32)
+    for s, at in enumerate(np.cumsum(need) - need):
+        table[s, :need[s]] = ids[at:at + need[s]]
+    shape = (int(need.sum()), Hkv, 16, d)
+    k, v = (torch.randn(shape, device="cuda", generator=g, dtype=torch.bfloat16) for _ in range(2))
+    return k, v, torch.from_numpy(table).cuda(), torch.from_numpy(np.asarray(lens, np.int32)).cuda()
+
+
+def drafted(sl, n: int, H: int = 32, d: int = 128, seed: int = I.BASE_SEED):
+    """Random trees of n nodes at the end of each sequence: q rows, offsets, ancestor bits, positions."""
+    rng = np.random.default_rng(seed)
+    S = len(sl)
+    parents = np.concatenate([[rng.integers(-1, i) for i in range(n)] for _ in range(S)]).astype(np.int32)
+    cu = offsets([n] * S)
+    mask, pos = fb.tree_layout(torch.from_numpy(parents).cuda(), sl, cu, (n + 31) // 32)
+    return torch.randn((S * n, H, d), device="cuda").bfloat16(), cu, mask, pos
 
 
 def make(name: str, splits: int = 8):
@@ -137,6 +165,31 @@ def make(name: str, splits: int = 8):
     if name == "window_c3":
         q, k, v = (torch.randn((1, 8192, 32, 128), device="cuda").bfloat16() for _ in range(3))
         return lambda: fb.forward_window(q, k, v, I.fp32_scale(128), 1024, 4)
+    if name in ("tree_c4", "tree_long"):
+        S, n, at = (64, 16, (512, 8192)) if name == "tree_c4" else (4, 64, (16384, 65536))
+        cache = bf16_cache(I.uniform_lengths(I.BASE_SEED, S, *at))
+        q, cu, mask, _ = drafted(cache[3], n)
+        return lambda: fb.paged_tree_attention(q, *cache, cu, n, mask, I.fp32_scale(128))
+    if name == "tree_e4m3":
+        k, v, cache, cu, _ = e4m3_cache(I.BASE_SEED, 64)
+        fb.paged_kv_write_e4m3(k, v, *cache, cu)
+        q, cu, mask, _ = drafted(cache[5], 16)
+        return lambda: fb.paged_tree_attention_e4m3(q, *cache, cu, 16, mask, I.fp32_scale(128))
+    if name == "qkv_rows":
+        lens = np.full(16, 1024)
+        k_cache, v_cache, bt, sl = bf16_cache(lens)
+        T, cu = int(lens.sum()), offsets(lens)
+        q, k, v = (torch.randn((T, h, 128), device="cuda").bfloat16() for h in (32, 8, 8))
+        wq, wk = (torch.ones(128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        angles = torch.arange(1024, device="cuda")[:, None] / 10000.0 ** (torch.arange(64, device="cuda") / 64)
+        cos_sin = torch.stack([angles.cos(), angles.sin()], -1).float().contiguous()
+        pos = torch.arange(1024, dtype=torch.int32, device="cuda").repeat(16)[None].contiguous()
+        return lambda: fb.paged_qkv_write(q, k, v, wq, wk, cos_sin, pos, k_cache, v_cache, bt, sl, cu)
+    if name == "copy_pages":
+        k_cache, v_cache = bf16_cache([16 * 4096])[:2]
+        ids = np.random.default_rng(I.BASE_SEED).permutation(4096).astype(np.int32).reshape(2048, 2)
+        pairs = torch.from_numpy(ids).cuda()
+        return lambda: fb.paged_copy_pages(k_cache, v_cache, pairs)
     raise SystemExit(f"unknown workload {name}")
 
 

@@ -13,8 +13,9 @@ replays of 20 launches, per launch.  Inputs smaller than L2 (the n=m=2048
 shapes, the fp32 case) stay L2-resident across launches; the long-context,
 decode, prefill and ragged inputs are larger than L2.  Rates use nominal work:
 4*n*m*d*H*B FLOPs (halved when causal; the ragged and paged rows sum their
-sequences, the windowed one its visible pairs), and for the decode the K and
-V bytes of every valid token (with their scale bytes in the e4m3 cache).
+sequences, the windowed one its visible pairs), and for the decode and the drafted
+nodes' attention the K and V bytes of every valid token (with their scale bytes in the
+e4m3 cache); the q, k and v rows and the copied pages count what is read and written.
 Nothing is checked here; parity lives in the tests.
 
 --naive times instead the materialised-score path against fa_forward at N =
@@ -35,7 +36,7 @@ import torch
 
 from . import binding as fb
 from . import inputs as I
-from .profile_case import e4m3_cache, offsets
+from .profile_case import e4m3_cache, make, offsets
 
 
 def _dev(t):
@@ -166,7 +167,7 @@ def rows(iters: int, warmup: int):
                                                      1), iters, warmup)
         fl = sum(4.0 * int(L) * int(L) * d * vcase.H / 2 for L in vcase.lens)
         out.append((f"ragged causal varlen 16 seqs H=16 d={d}", ms, fl / (ms * 1e9), "TFLOP/s"))
-    return out + _e4m3_cache_rows(iters, warmup) + _window_rows(iters, warmup)
+    return out + _e4m3_cache_rows(iters, warmup) + _window_rows(iters, warmup) + _tree_rows(iters, warmup)
 
 
 def _e4m3_cache_rows(iters, warmup):
@@ -205,6 +206,23 @@ def _window_rows(iters, warmup, n=8192, H=32, d=128, window=1024, sinks=4):
     pairs = (np.minimum(p + 1, window) + np.minimum(sinks, np.maximum(0, p + 1 - window))).sum()
     return [(f"bf16 window {window} sinks {sinks} n=m={n} H={H} d={d}", ms, 4.0 * d * H * float(pairs) / (ms * 1e9),
              "TFLOP/s")]
+
+
+def _tree_rows(iters, warmup):
+    """What a step of drafted token trees runs (the profiled workloads, H = 32, Hkv = 8, d = 128)."""
+    row = 8 * 2 * 128                              # values of a token's K and V
+    pool, long = (int(I.uniform_lengths(I.BASE_SEED, S, *at).sum()) for S, at in ((64, (512, 8192)), (4, (16384, 65536))))
+    out = []
+    for name, what, nbytes in (
+            ("tree_c4", "drafted trees 64 seqs x 16 nodes H=32 Hkv=8", pool * row * 2),
+            ("tree_e4m3", "e4m3 drafted trees 64 seqs x 16 nodes H=32 Hkv=8", pool * (row + 16)),
+            ("tree_long", "drafted trees 4 long seqs x 64 nodes H=32 Hkv=8", long * row * 2),
+            ("qkv_rows", "q, k, v rows of 16384 tokens H=32 Hkv=8 into the cache", 16384 * 48 * 128 * 2 * 2),
+            ("copy_pages", "2048 cache pages copied Hkv=8 d=128", 2048 * 16 * row * 2 * 2)):
+        ms = _median_ms(make(name), iters, warmup)
+        out.append((what, ms, nbytes / (ms * 1e6), "GB/s"))
+        torch.cuda.empty_cache()
+    return out
 
 
 def fp8_gemm_peak(n: int = 8192, reps: int = 10):
