@@ -46,11 +46,12 @@
 // unrolled over a whole tile the issuers' code was pushed out of it (64 x 16 198 us).
 // A small call (1 x 8 nodes over 1000 tokens, 12 us) is start-up: code that is read for
 // the first time, the list, one chain of copy, scores, softmax, values and the merge.
-// From the e4m3 cache, half the bytes, the same two take 236 and 154 us: widening 128 x 128
-// codes keeps the integer and conversion pipes of an SM busy for some 1000 clocks, a tile
-// of K and one of V, beside the softmax.  One warpgroup for it took 246 and 160 us, codes
-// widened by integer instructions and a bf16 product 290 and 178, four rows a step
-// instead of two 283 and 162 (the instruction cache again).
+// From the e4m3 cache, half the bytes, the same two take 236 and 154 us: a tile of 128 x
+// 128 codes takes the widening warps 1500 clocks beside the softmax, two of them a step,
+// the conversions' own rate (the scale as a bf16 product instead of an fp32 one changed
+// nothing; codes assembled by integer instructions, all of them or half, 290 and 270 us).
+// One warpgroup for it took 246 and 160 us, four rows at once instead of two 283 and 162
+// (the instruction cache again); deeper rings gained nothing.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
