@@ -601,13 +601,14 @@ fa_status fa_paged_qkv_write(const void* q, const void* k, const void* v, const 
 
 /*
  * fa_paged_tree_workspace_size — bytes of workspace fa_paged_tree_attention and
- * fa_paged_tree_attention_e4m3 need
- * (0 on invalid sizes): partials of the units whose keys are split.
+ * fa_paged_tree_attention_e4m3 need (0 on invalid sizes): partials of the units
+ * whose keys are split.
  */
 size_t fa_paged_tree_workspace_size(int num_seqs, int max_seqlen_q, int H, int Hkv, int d);
 
 /*
- * fa_paged_tree_attention — attention of drafted nodes over the bf16 paged cache.
+ * fa_paged_tree_attention — attention of drafted nodes over the bf16 paged cache
+ * (fa_paged_qkv_write fills it).
  * Passage: as fa_paged_prefill.
  *   q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, o, lse
  *                 as fa_paged_prefill
@@ -622,8 +623,8 @@ size_t fa_paged_tree_workspace_size(int num_seqs, int max_seqlen_q, int H, int H
  *                 workspace must not overlap on the GPU
  * Cache contents of keys that no node of a sequence sees (past its end, or of
  * nodes whose bit nobody has) are never used, NaN included; a NaN in a key that
- * one node sees may reach others of its sequence.  A row whose visible scores
- * hold a NaN gets O = LSE = NaN.
+ * one node sees, or an infinite value in its V, may reach others of its sequence.
+ * A row whose visible scores hold a NaN gets O = LSE = NaN.
  * A sequence of more than max_seqlen_q or 32*mask_words nodes is skipped and sets
  * FA_ERR_INVALID_ARG.  Page ids outside [0, num_pages) set
  * FA_ERR_BAD_BLOCK_TABLE; the sequence's output is then unspecified.
@@ -647,7 +648,8 @@ fa_status fa_paged_tree_attention(const void* q, const void* k_cache, const void
  * fa_paged_kv_read_e4m3 returns.
  *   k_cache, v_cache, k_scale, v_scale  as fa_paged_prefill_e4m3
  * The other arguments, the conventions and the limits are as for
- * fa_paged_tree_attention.
+ * fa_paged_tree_attention.  (fa_qk_norm_rope and fa_paged_kv_write_e4m3 together
+ * do for this cache what fa_paged_qkv_write does for the bf16 one.)
  */
 fa_status fa_paged_tree_attention_e4m3(const void* q, const void* k_cache, const void* v_cache,
                                        const void* k_scale, const void* v_scale,

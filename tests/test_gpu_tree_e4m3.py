@@ -229,6 +229,26 @@ def test_a_wait_that_runs_out_is_reported(monkeypatch):
     assert fb.fa_get_device_status() == 0
 
 
+def test_pages_past_32_bits():
+    """Codes past 2^31 bytes: the same pages at the pool's end and at its beginning give the same bits."""
+    pool, Hkv, d, n = 140000, 8, 128, 9            # 2.3e9 bytes a cache
+    k, v = (torch.empty((pool, Hkv, 16, d), dtype=torch.uint8, device="cuda") for _ in "kv")
+    ks, vs = (torch.empty((pool, Hkv, 16), dtype=torch.uint8, device="cuda") for _ in "kv")
+    near, far = [5, 1, 7], [139999, 137000, 139001]
+    for x in (k, v):
+        x[near] = torch.randn((3, Hkv, 16, d), device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+    for x in (ks, vs):
+        x[near] = torch.randint(120, 130, (3, Hkv, 16), dtype=torch.uint8, device="cuda")
+    for x in (k, v, ks, vs):
+        x[far] = x[near]
+    q = torch.randn((n, 16, d), device="cuda").bfloat16()
+    mask = T.i32(T.pack(T.ancestors(T.random_parents(np.random.default_rng(2), n))[0], 1))
+    out = [fb.paged_tree_attention_e4m3(q, k, v, ks, vs, T.i32([pages]), T.i32([45]), T.i32([0, n]), n, mask, 0.125)
+           for pages in (near, far)]
+    assert all(torch.equal(a, b) for a, b in zip(*out)) and not out[0][0].isnan().any()
+    assert fb.fa_get_device_status() == 0
+
+
 def test_helper_refuses():
     c = Cache(np.random.default_rng(1), [40], 1, 64)
     q = torch.randn((4, 2, 64), device="cuda").bfloat16()
