@@ -630,7 +630,7 @@ size_t fa_paged_tree_workspace_size(int num_seqs, int max_seqlen_q, int H, int H
  * FA_ERR_BAD_BLOCK_TABLE; the sequence's output is then unspecified.
  * Supported: d in {64, 128}, page_size == 16, H / Hkv <= 128; scale positive and
  * finite; 1 <= mask_words; num_seqs <= 4096; total_q*H and total_q*mask_words below
- * 2^31; num_pages*Hkv*16 below 2^31; units * (3*ceil(max_blocks_per_seq / 8) + 6)
+ * 2^31; num_pages*Hkv*16 below 2^31; units * (4*ceil(max_blocks_per_seq / 8) + 9)
  * below 2^31, where units = num_seqs * Hkv * ceil(max_seqlen_q / (2*floor(128 /
  * (H / Hkv)))).
  */

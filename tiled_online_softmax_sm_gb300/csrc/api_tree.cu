@@ -97,12 +97,12 @@ fa_status tree_attention(const char* fn, const void* q, const void* k_cache, con
     return fail(FA_ERR_WORKSPACE, "%s: workspace %p of %zu bytes (need %zu, 256-byte aligned)", fn, workspace,
                 workspace_bytes, need);
   if (max_seqlen_q > total_q) max_seqlen_q = total_q;   // no sequence has more
-  // rows, mask words and positions in the list of K/V tiles (at most 3 a tile and 6 a
+  // rows, mask words and positions in the list of K/V tiles (at most 4 a tile and 9 a
   // unit) are numbered in 32 bits
   const long long nodes = 2 * (128 / (H / Hkv));
   const double units = (double)num_seqs * Hkv * (double)((max_seqlen_q + nodes - 1) / nodes);
   if ((long long)total_q * H > kInt || (long long)total_q * mask_words > kInt ||
-      units * (3.0 * ((max_blocks_per_seq + 7) / 8) + 6.0) > (double)kInt)
+      units * (4.0 * ((max_blocks_per_seq + 7) / 8) + 9.0) > (double)kInt)
     return fail(FA_ERR_UNSUPPORTED, "%s: total_q*H, total_q*mask_words or the K/V tiles of all units exceed 2^31", fn);
   fa::TreeAttnParams p{q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens_q, mask, o, lse,
                        num_seqs, total_q, max_seqlen_q, mask_words, H, Hkv, d, num_pages, max_blocks_per_seq,

@@ -32,7 +32,8 @@
 //
 // Softmax as in the forward: p = 2^(s scale log2 e - ref), the reference raised
 // only when a tile's maximum passes it by far; two sums are kept, of p for the LSE
-// and of the bf16-rounded p that the P V MMA multiplies for O.
+// and of the bf16-rounded p that the P V MMA multiplies for O (which forms that sum itself
+// at d = 64).
 //
 // Measured (d = 128, 32 heads of 8, contexts uniform on the range): 64 x 16 nodes over
 // [512, 8192] tokens, one query tile a unit, 175 us for 1.04 GB (6.0 TB/s, 0.89 of a
@@ -46,7 +47,7 @@
 // unrolled over a whole tile the issuers' code was pushed out of it (64 x 16 198 us).
 // A small call (1 x 8 nodes over 1000 tokens, 12 us) is start-up: code that is read for
 // the first time, the list, one chain of copy, scores, softmax, values and the merge.
-// From the e4m3 cache, half the bytes, the same two take 236 and 154 us: a tile of 128 x
+// From the e4m3 cache, half the bytes, the same two take 237 and 153 us: a tile of 128 x
 // 128 codes takes the widening warps 1500 clocks beside the softmax, two of them a step,
 // the conversions' own rate (the scale as a bf16 product instead of an fp32 one changed
 // nothing; codes assembled by integer instructions, all of them or half, 290 and 270 us).
@@ -90,8 +91,15 @@ struct Cfg {
   // K/V tiles are laid out in groups of eight keys, a group's 1 KB pieces (64
   // values of each key) side by side, so that one copy brings a whole page
   static constexpr int kGroup = 1024 * kChunks;
-  static constexpr int kSmem = (kQ + kStages) * kTileBytes + kRawStages * kRawTile + 1024;   // + alignment slack
-  static constexpr uint32_t kIdescO = ptx::idesc_bf16_f32(128, D, false, true);
+  // The sum of the rounded weights, O's divisor: at d = 64 the P V MMA forms it as 16
+  // more columns of O, with a block of ones for V (an MMA of 80 columns takes as long as
+  // one of 64; 16 x [20, 64] nodes, 24 heads of 8: 62 us where the softmax warps add, 59 so).
+  // At d = 128 tensor memory is full.
+  static constexpr bool kOnes = D == 64;
+  static constexpr int kOnesBytes = kOnes ? kTile * 128 : 0;
+  static constexpr int kSmem =
+      (kQ + kStages) * kTileBytes + kOnesBytes + kRawStages * kRawTile + 1024;   // + alignment slack
+  static constexpr uint32_t kIdescO = ptx::idesc_bf16_f32(128, kOnes ? D + 16 : D, false, true);
 };
 
 // Registers of the E4M3 instances: 640 threads at 96, split again among copies and
@@ -147,23 +155,25 @@ __device__ __forceinline__ Seq load_seq(const Args& a, int s) {
 }
 
 // Units of a sequence along its nodes, K/V tiles of each, and the cost of one: with
-// two query tiles it takes about half as long again.
+// two query tiles it takes about a third longer (16 x [20, 64] nodes at d = 64, where both
+// occur: 2 : 3 59 us, 3 : 4 57, 4 : 5 58; 2 : 4 cost 12 us more than 2 : 3).
 // (a division by 2 * tile_nodes <= 256 as a product with its reciprocal in 2^-40, which is
 // exact below 2^32: the divisions of five roles' segments were a good part of the
 // code, and of a small call's time)
 __device__ __forceinline__ int node_units(const Args& a, const Seq& Q) {
   return (int)(((unsigned long long)(Q.n + 2 * a.tile_nodes - 1) * a.per_unit) >> 40);
 }
-__device__ __forceinline__ int ceil_div(int x, int cost) {   // cost 1, 2 or 3; 0 for x < 0
+__device__ __forceinline__ int ceil_div(int x, int cost) {   // cost 1, 3 or 4; 0 for x < 0
   const uint32_t y = (uint32_t)(max(x, 0) + cost - 1);
-  return (int)(cost == 3 ? __umulhi(y, 0xaaaaaaabu) >> 1 : y >> (cost - 1));
+  return (int)(cost == 3 ? __umulhi(y, 0xaaaaaaabu) >> 1 : y >> (cost >> 1));
 }
 __device__ __forceinline__ int key_tiles(const Seq& Q) { return (Q.L + kTile - 1) / kTile; }
 __device__ __forceinline__ int tile_cost(const Args& a, const Seq& Q, bool weighed) {
-  return !weighed ? 1 : Q.n > a.tile_nodes ? 3 : 2;
+  return !weighed ? 1 : Q.n > a.tile_nodes ? 4 : 3;
 }
-// Cost of beginning and ending a unit.
-constexpr int kUnitCost = 6;
+// Cost of beginning and ending a unit, about three tiles (64 x 16 nodes: 9 174 us, 6 178,
+// 4 185).
+constexpr int kUnitCost = 9;
 // Tiles a CTA from which on costs are weighed.  (Below, a tile costs 1 and a unit
 // nothing, so that every piece has a tile; above, a piece is longer than any cost, so
 // that of a cut unit every piece between its first and its last tile has one, too.)
@@ -287,7 +297,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   uint8_t* sQ = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
   uint8_t* sKV = sQ + C::kQ * C::kTileBytes;
-  uint8_t* sRaw = sKV + kStages * C::kTileBytes;
+  uint8_t* sOnes = sKV + kStages * C::kTileBytes;
+  uint8_t* sRaw = sOnes + C::kOnesBytes;
   __shared__ Shared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* const status = a.status;
@@ -337,6 +348,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     ptx::mbar_init(bar_se, kTile);
     sh.abort = 0;
     ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+  }
+  if constexpr (C::kOnes) {
+    for (int i = threadIdx.x; i < C::kOnesBytes / 16; i += kThreads)
+      reinterpret_cast<uint4*>(sOnes)[i] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
     ptx::fence_proxy_async_smem();
   }
   if (warp == 1) {
@@ -526,7 +542,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const int w = warp - 1;
       const uint64_t qdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sQ), 16, 1024);
       const uint64_t kdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 16, C::kGroup);
-      const uint64_t vdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 1024, C::kGroup);
+      // (V's second 64 columns lie 1 KB behind the first, or are the ones)
+      const uint64_t vdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sKV), C::kOnes ? 0 : 1024, C::kGroup);
       const uint32_t s_tm = tbase + w * kTile, o_tm = tbase + 256 + w * 128;
       int lc = 0;                    // copies of the segments so far
       int nq[2] = {0, 0}, half = 0;  // query tiles used, the buffer of the next single one
@@ -558,7 +575,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       auto values = [&](int l, int part, bool first) {
         if (!ptx::mbar_wait(bar_p + 16 * w + 8 * part, np & 1, status, abort_flag)) return false;
         ptx::tc_fence_after();
-        const uint64_t vd = vdesc0 + (uint64_t)((l % kStages) * (C::kTileBytes >> 4) + part * (C::kGroup >> 1));
+        const int slot = l % kStages;
+        uint64_t vd = vdesc0 + (uint64_t)(slot * (C::kTileBytes >> 4) + part * (C::kGroup >> 1));
+        if constexpr (C::kOnes) vd += (uint64_t)((kStages - slot) * (C::kTileBytes >> 4)) << 16;
 #pragma unroll
         for (int k = 0; k < kCols / 16; ++k)
           ptx::mma_ts(o_tm, s_tm + kCols * part + k * 8, vd + (uint64_t)(k * (C::kGroup >> 3)), C::kIdescO,
@@ -813,7 +832,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 pp[e / 2] = ptx::pack_bf16x2(p0, p1);
               }
               ptx::tmem_st16(col + c * 16, pp);
-              l_p += sum_packed(pp);
+              if constexpr (!C::kOnes) l_p += sum_packed(pp);
             };
             // Half a tile: one look.  A whole one: both halves for the maximum, then both
             // again for P.  (Rolled: unrolled over the tile, the code of the softmax warps
@@ -844,7 +863,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                   if (!ok) break;
                   ptx::tc_fence_after();
 #pragma unroll 1
-                  for (int c = 0; c < D / 32; ++c) {
+                  for (int c = 0; c < D / 32 + (C::kOnes ? 1 : 0); ++c) {   // (O, and its sum)
                     uint32_t ov[32];
                     ptx::tmem_ld32(o_col + c * 32, ov);
                     ptx::tmem_wait_ld();
@@ -901,8 +920,18 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       ok = __all_sync(0xffffffffu, there);
       if (!ok) break;
       ptx::tc_fence_after();
+      float lp1 = 0.f;
+      if constexpr (C::kOnes) {
+        uint32_t own, other = 0u;
+        ptx::tmem_ld1(o_col + D, own);
+        if (two) ptx::tmem_ld1(o_col + 128 + D, other);
+        ptx::tmem_wait_ld();
+        l_p = __uint_as_float(own);
+        lp1 = __uint_as_float(other);
+      }
       if (two) {
-        const float m1 = sh.stat[r][0], l1 = sh.stat[r][1], lp1 = sh.stat[r][2];
+        const float m1 = sh.stat[r][0], l1 = sh.stat[r][1];
+        if constexpr (!C::kOnes) lp1 = sh.stat[r][2];
         ptx::mbar_arrive(bar_se);
         m = fmaxf(m_ref, m1);
         c0 = m_ref == -INFINITY ? 0.f : ptx::ex2(m_ref - m);
