@@ -356,6 +356,21 @@ def test_drafting_steps(H, Hkv, d):
     assert fb.fa_get_device_status() == 0
 
 
+def test_outputs_where_torch_has_no_short_way(monkeypatch):
+    """The helpers' outputs, allocated either way: the same tensors."""
+    cu, sl, parents = T.i32([0, 3, 7]), T.i32([20, 30]), T.i32([-1, 0, 0, -1, 0, 1, 1])
+    q, k = (torch.randn((7, h, 64), device="cuda").bfloat16() for h in (4, 2))
+
+    def outputs():
+        return *fb.tree_layout(parents, sl, cu, 2), *fb.qk_norm_rope(q, k, None, None, None, None)
+
+    got = outputs()
+    monkeypatch.setattr(fb, "_new", fb._new_strided)
+    for a, b in zip(got, outputs()):
+        assert torch.equal(a, b) and a.stride() == b.stride() and a.dtype == b.dtype and a.device == b.device
+        assert a.is_contiguous()
+
+
 def test_caches_past_32_bits():
     """Pages whose elements are numbered past 2^31, in every operator."""
     Hkv, d, pool = 8, 128, 140000                  # 2.3e9 elements a cache

@@ -156,19 +156,28 @@ torch = _Torch()
 
 # Set by _bind_torch, before the e4m3 and tree helpers' first check: the current stream of a device
 # that is known to be the current one, the current device once there are tensors on one, the types of
-# the e4m3 cache's codes and scales, and torch's own under names that cost one look-up.
-_current_raw_stream = _current_device = _CODES = _SCALES = _I32 = _BF16 = _F32 = _empty = None
+# the e4m3 cache's codes and scales, torch's own types under names that cost one look-up, and new
+# memory on the current device, (size, strides, type) -> tensor: past torch's dispatcher where torch
+# offers that (behind a launch, whose code has pushed the dispatcher out of the caches, the two
+# outputs of an attention take 4.3 us instead of 7.8).
+_current_raw_stream = _current_device = _CODES = _SCALES = _I32 = _BF16 = _F32 = _U8 = _new = None
 
 
 def _bind_torch():
-    global _current_raw_stream, _current_device, _CODES, _SCALES, _I32, _BF16, _F32, _empty
-    _I32, _BF16, _F32, _empty = torch.int32, torch.bfloat16, torch.float32, torch.empty
+    global _current_raw_stream, _current_device, _CODES, _SCALES, _I32, _BF16, _F32, _U8, _new
+    _I32, _BF16, _F32, _U8 = torch.int32, torch.bfloat16, torch.float32, torch.uint8
+    guards = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
+    _new = getattr(guards, "_empty_strided_cuda", None) or _new_strided
     _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda device: torch.cuda.current_stream(device).cuda_stream)
     _SCALES = frozenset((torch.uint8, torch.int8) +
                         ((torch.float8_e8m0fnu,) if hasattr(torch, "float8_e8m0fnu") else ()))
     _CODES = frozenset((torch.float8_e4m3fn, torch.uint8, torch.int8))
+
+
+def _new_strided(size, strides, dtype):
+    return torch.empty_strided(size, strides, dtype=dtype, device="cuda")
 
 
 def _check(rc: int):
@@ -775,8 +784,10 @@ def tree_layout(parents, seq_lens, cu_seqlens, mask_words, stream=None):
             and device >= 0 and device == _current_device()):
         _refuse_ints("tree_layout", device, ("parents", parents, (T,)), ("seq_lens", seq_lens, (S,)),
                      ("cu_seqlens", cu_seqlens, (S + 1,)))
-    mask = _empty((T, mask_words), dtype=i32, device=parents.device)
-    positions = torch.empty_like(parents)
+    if mask_words < 0:
+        raise FaError(FA_ERR_INVALID_ARG, f"tree_layout: mask_words={mask_words}")
+    mask = _new((T, mask_words), (mask_words, 1), i32)
+    positions = _new((T,), (1,), i32)
     lib = _lib or load()
     rc = lib.fa_tree_layout(parents.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(), mask.data_ptr(),
                             positions.data_ptr(), S, T, mask_words, _current_raw_stream(device))
@@ -837,15 +848,15 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, section
         _bind_torch()
     fn = "qk_norm_rope"
     device = q.get_device()
-    T, H, d = shape = q.shape
-    k_shape = (T, k.shape[1], d)
+    T, H, d = q.shape
+    shape, k_shape = (T, H, d), (T, k.shape[1], d)
     if device < 0 or device != _current_device():
         _refuse(fn, device)
     qs, ks = _heads_stride(fn, "q", q, shape, device), _heads_stride(fn, "k", k, k_shape, device)
     qw, kw, cs, at, rot, axes, rows, host = _rotary(fn, device, T, d, q_weight, k_weight, cos_sin, positions,
                                                     sections)
-    q_out = _empty(shape, dtype=_BF16, device=q.device)
-    k_out = _empty(k_shape, dtype=_BF16, device=q.device)
+    q_out = _new(shape, (H * d, d, 1), _BF16)
+    k_out = _new(k_shape, (k_shape[1] * d, d, 1), _BF16)
     lib = _lib or load()
     rc = lib.fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), qw, kw, cs, at, q_out.data_ptr(), k_out.data_ptr(), T,
                              H, k_shape[1], d, qs, ks, rot, 1 if interleaved else 0, axes, host, rows, eps,
@@ -893,7 +904,7 @@ def paged_qkv_write(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_
                   _heads_stride(fn, "v", v, kv_shape, device))
     qw, kw, cs, at, rot, axes, rows, host = _rotary(fn, device, T, d, q_weight, k_weight, cos_sin, positions,
                                                     sections)
-    q_out = _empty(shape, dtype=_BF16, device=q.device)
+    q_out = _new(shape, (H * d, d, 1), _BF16)
     lib = _lib or load()
     rc = lib.fa_paged_qkv_write(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), qw, kw, cs, at, q_out.data_ptr(), k_cache.data_ptr(),
@@ -931,14 +942,14 @@ def paged_tree_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_
     if workspace is None:   # (a caller's own is sized for the caller's bound)
         max_seqlen_q = min(max_seqlen_q, T)
         size = _tree_workspace(S, max_seqlen_q, H, Hkv, d)
-        workspace = _empty(size, dtype=torch.uint8, device=q.device)
+        workspace = _new((size,), (1,), _U8)
     elif workspace.get_device() != device or not workspace.is_contiguous():
         raise FaError(FA_ERR_WORKSPACE, f"{fn}: the workspace is on {workspace.device} with strides "
                                         f"{workspace.stride()}")
     else:
         size = workspace.nbytes
-    o = torch.empty_like(q)
-    lse = _empty((H, T), dtype=_F32, device=q.device)
+    o = _new((T, H, d), (H * d, d, 1), _BF16)
+    lse = _new((H, T), (T, 1), _F32)
     lib = _lib or load()
     rc = lib.fa_paged_tree_attention(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
@@ -969,14 +980,14 @@ def paged_tree_attention_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table
     if workspace is None:   # (a caller's own is sized for the caller's bound)
         max_seqlen_q = min(max_seqlen_q, T)
         size = _tree_workspace(S, max_seqlen_q, H, Hkv, d)
-        workspace = _empty(size, dtype=torch.uint8, device=q.device)
+        workspace = _new((size,), (1,), _U8)
     elif workspace.get_device() != device or not workspace.is_contiguous():
         raise FaError(FA_ERR_WORKSPACE, f"{fn}: the workspace is on {workspace.device} with strides "
                                         f"{workspace.stride()}")
     else:
         size = workspace.nbytes
-    o = torch.empty_like(q)
-    lse = _empty((H, T), dtype=_F32, device=q.device)
+    o = _new((T, H, d), (H * d, d, 1), _BF16)
+    lse = _new((H, T), (T, 1), _F32)
     lib = _lib or load()
     rc = lib.fa_paged_tree_attention_e4m3(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
@@ -1034,7 +1045,7 @@ def paged_kv_accept(k_cache, v_cache, block_table, seq_lens, cu_seqlens, path, p
         _refuse_ints(fn, device, ("block_table", block_table, (S, max_blocks)), ("seq_lens", seq_lens, (S,)),
                      ("cu_seqlens", cu_seqlens, (S + 1,)), ("path", path, (S, max_path)),
                      ("path_lens", path_lens, (S,)))
-    new_lens = torch.empty_like(seq_lens)
+    new_lens = _new((S,), (1,), i32)
     lib = _lib or load()
     rc = lib.fa_paged_kv_accept(
         k_cache.data_ptr(), v_cache.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
