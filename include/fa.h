@@ -625,6 +625,8 @@ size_t fa_paged_tree_workspace_size(int num_seqs, int max_seqlen_q, int H, int H
  * nodes whose bit nobody has) are never used, NaN included; a NaN in a key that
  * one node sees, or an infinite value in its V, may reach others of its sequence.
  * A row whose visible scores hold a NaN gets O = LSE = NaN.
+ * O is summed in fp32 before it is divided, with weights of up to 2^8: finite values
+ * of V give a finite O while the largest times the keys of a row stays below 2^119.
  * A sequence of more than max_seqlen_q or 32*mask_words nodes is skipped and sets
  * FA_ERR_INVALID_ARG.  Page ids outside [0, num_pages) set
  * FA_ERR_BAD_BLOCK_TABLE; the sequence's output is then unspecified.

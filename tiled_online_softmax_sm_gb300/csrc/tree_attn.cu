@@ -72,9 +72,10 @@ constexpr int kCtas = 152;        // one per SM
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // The reference is raised when a row's maximum passes it by more than this (log2
-// units): p, and bf16's exponent, reach that far, and each raise multiplies O in
-// tensor memory.
-constexpr float kRaise = 24.f;
+// units).  Each raise multiplies O in tensor memory; without one p, and with it O's
+// fp32 sum of p V, grows by as much: values of V times the row's keys have to stay
+// below 2^119, and at 24 they would have to below 2^103.
+constexpr float kRaise = 8.f;
 
 // E4M3: K and V come from the e4m3 cache.  Warp 0 then stages their codes and scale
 // bytes, and two more warpgroups widen them to bf16 (exactly: a code has 4 significant
