@@ -566,8 +566,9 @@ fa_status fa_tree_layout(const int* parents, const int* seq_lens, const int* cu_
  * The arithmetic is fp32, rounded once to bf16.  A token with a position outside
  * [0, max_positions) is skipped (its rows are not written) and sets
  * FA_ERR_INVALID_ARG in the device status word.
- * (A head whose values reach 1e18 has squares beyond fp32: its norm is infinite and the
- * head becomes 0.)
+ * A head whose squares leave fp32's range at either end (values from 1e15, or with eps
+ * 0 up to 1e-23) is normed all the same: it is scaled by a power of two first.  With eps 0
+ * a head of zeros becomes NaN (0 / 0).
  * Supported: d in {64, 128}; rot_dim a multiple of 8 up to d; 1 <= num_axes <= 4;
  * pointers 16-byte aligned; H, Hkv <= 65536; total*(H + 2*Hkv) below 2^31.
  */

@@ -56,6 +56,39 @@ __device__ __forceinline__ uint32_t narrow(uint64_t v) {
   return ptx::pack_bf16x2(lo, hi);
 }
 
+// Squares leave fp32 where values reach 2^60 or (with an eps that does not hide it) fall
+// to 2^-75: a row's 1 / sqrt(mean square + eps) is taken as it is only within 2^-50 .. 2^50.
+__device__ __forceinline__ bool out_of_range(float r) {
+  return __float_as_uint(r) - 0x26800000u > 0x58800000u - 0x26800000u;   // (a NaN, too)
+}
+
+// The sum of a row's squares, in all of its lanes.
+template <int LANES>
+__device__ __forceinline__ float sum_squares(const uint64_t (&x)[4]) {
+  float lo, hi;
+  ptx::f2_split(ptx::ffma2(x[0], x[0], ptx::ffma2(x[1], x[1], ptx::ffma2(x[2], x[2], ptx::fmul2(x[3], x[3])))), lo, hi);
+  float sum = lo + hi;
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// The power of two that brings a row's largest magnitude to about 1 (to within 2^33, so that
+// the factor is a normal number).
+template <int LANES>
+__device__ __forceinline__ float unit_scale(const uint64_t (&x)[4]) {
+  float most = 0.f, lo, hi;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    ptx::f2_split(x[k], lo, hi);
+    most = fmaxf(most, fmaxf(fabsf(lo), fabsf(hi)));
+  }
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  const int e = min(max((int)(__float_as_uint(most) >> 23) - 127, -100), 100);
+  return __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e
+}
+
 // A group is up to kSteps * 32 / (D / 8) heads of q, of k or of v of one token; a
 // token's groups are shared out over `parts` warps.  A warp's next group is on its
 // way while it works on one.
@@ -81,11 +114,15 @@ qkv_rows_kernel(const QkvRowsParams p, int parts) {
   auto kind_of = [&](int g) { return g < q_groups ? 0 : g < q_groups + k_groups ? 1 : 2; };   // q, k, v
   auto head_of = [&](int g) { return (g - (g < q_groups ? 0 : g < q_groups + k_groups ? q_groups : q_groups + k_groups)) * kEach + sub; };
   uint2 a[kSteps], b[kSteps], na[kSteps], nb[kSteps];
+  auto source = [&](int g) __attribute__((always_inline)) {   // the lane's first row of the group
+    const int kind = kind_of(g);
+    return (kind == 0 ? static_cast<const __nv_bfloat16*>(p.q) + t * p.q_stride
+            : kind == 1 ? static_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride
+                        : static_cast<const __nv_bfloat16*>(p.v) + t * p.v_stride) + head_of(g) * D;
+  };
   auto fetch = [&](int g) __attribute__((always_inline)) {
-    const int kind = kind_of(g), heads = kind == 0 ? p.H : p.Hkv, h0 = head_of(g);
-    const __nv_bfloat16* src = (kind == 0 ? static_cast<const __nv_bfloat16*>(p.q) + t * p.q_stride
-                                : kind == 1 ? static_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride
-                                            : static_cast<const __nv_bfloat16*>(p.v) + t * p.v_stride) + h0 * D;
+    const int heads = kind_of(g) == 0 ? p.H : p.Hkv, h0 = head_of(g);
+    const __nv_bfloat16* src = source(g);
 #pragma unroll
     for (int e = 0; e < kSteps; ++e) {
       na[e] = nb[e] = make_uint2(0u, 0u);
@@ -186,22 +223,9 @@ qkv_rows_kernel(const QkvRowsParams p, int parts) {
         }
       }
     }
-#pragma unroll
-    for (int e = 0; e < kSteps; ++e) {
-      const int h = h0 + e * kRows;
-      uint32_t y[4] = {a[e].x, a[e].y, b[e].x, b[e].y};
+    // a row (its bits, its values and 1 / its norm) rotated and stored
+    auto finish = [&](int h, uint32_t (&y)[4], const uint64_t (&x)[4], float r) __attribute__((always_inline)) {
       if (!PAGED || kind < 2) {
-        const uint64_t x[4] = {widen(y[0]), widen(y[1]), widen(y[2]), widen(y[3])};
-        float r = 1.f;
-        if (norm) {
-          float lo, hi;
-          ptx::f2_split(
-              ptx::ffma2(x[0], x[0], ptx::ffma2(x[1], x[1], ptx::ffma2(x[2], x[2], ptx::fmul2(x[3], x[3])))), lo, hi);
-          float sum = lo + hi;
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          r = rsqrtf(sum * (1.f / D) + p.eps);
-        }
         const uint64_t r2 = ptx::f2_bits(r, r);
         uint64_t z[4];
 #pragma unroll
@@ -221,6 +245,48 @@ qkv_rows_kernel(const QkvRowsParams p, int parts) {
         *reinterpret_cast<uint2*>(dst + row * D + off_a) = make_uint2(y[0], y[1]);
         *reinterpret_cast<uint2*>(dst + row * D + off_b) = make_uint2(y[2], y[3]);
       }
+    };
+    // (all rows' norms before the first is used: one branch for the group, 90.2 us with one
+    // for each row, and the sums' shuffles go side by side)
+    float r[kSteps];
+#pragma unroll
+    for (int e = 0; e < kSteps; ++e) r[e] = 1.f;
+    if (norm && (!PAGED || kind < 2)) {
+      bool out = false;
+#pragma unroll
+      for (int e = 0; e < kSteps; ++e) {
+        const uint64_t x[4] = {widen(a[e].x), widen(a[e].y), widen(b[e].x), widen(b[e].y)};
+        r[e] = rsqrtf(sum_squares<kLanes>(x) * (1.f / D) + p.eps);
+        out = out || (h0 + e * kRows < heads && out_of_range(r[e]));
+      }
+      if (__any_sync(0xffffffffu, out)) {   // rows read again, one at a time: registers are short
+        const __nv_bfloat16* src = source(g);
+#pragma unroll 1
+        for (int e = 0; e < kSteps; ++e) {
+          uint32_t y[4] = {0u, 0u, 0u, 0u};
+          if (h0 + e * kRows < heads) {
+            const uint2 lo = ld_row(src + e * kRows * D + off_a), hi = ld_row(src + e * kRows * D + off_b);
+            y[0] = lo.x;
+            y[1] = lo.y;
+            y[2] = hi.x;
+            y[3] = hi.y;
+          }
+          uint64_t x[4] = {widen(y[0]), widen(y[1]), widen(y[2]), widen(y[3])};
+          const float scale = unit_scale<kLanes>(x);
+          const bool scaled = out_of_range(rsqrtf(sum_squares<kLanes>(x) * (1.f / D) + p.eps));
+          const float f = scaled ? scale : 1.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = ptx::fmul2(x[k], ptx::f2_bits(f, f));
+          finish(h0 + e * kRows, y, x, rsqrtf(sum_squares<kLanes>(x) * (1.f / D) + p.eps * f * f));
+        }
+        continue;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kSteps; ++e) {
+      uint32_t y[4] = {a[e].x, a[e].y, b[e].x, b[e].y};
+      const uint64_t x[4] = {widen(y[0]), widen(y[1]), widen(y[2]), widen(y[3])};
+      finish(h0 + e * kRows, y, x, r[e]);
     }
   }
 }
