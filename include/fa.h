@@ -566,9 +566,8 @@ fa_status fa_tree_layout(const int* parents, const int* seq_lens, const int* cu_
  * The arithmetic is fp32, rounded once to bf16.  A token with a position outside
  * [0, max_positions) is skipped (its rows are not written) and sets
  * FA_ERR_INVALID_ARG in the device status word.
- * A head whose squares leave fp32's range at either end (values from 1e15, or with eps
- * 0 up to 1e-23) is normed all the same: it is scaled by a power of two first.  With eps 0
- * a head of zeros becomes NaN (0 / 0).
+ * A head whose squares leave fp32's range is normed all the same (it is scaled by a power
+ * of two first).  With eps 0 a head of zeros becomes NaN (0 / 0).
  * Supported: d in {64, 128}; rot_dim a multiple of 8 up to d; 1 <= num_axes <= 4;
  * pointers 16-byte aligned; H, Hkv <= 65536; total*(H + 2*Hkv) below 2^31.
  */
@@ -618,7 +617,9 @@ size_t fa_paged_tree_workspace_size(int num_seqs, int max_seqlen_q, int H, int H
  *                 seq_lens[s] - n_s) and node t where bit t of its row is set.
  *                 Bits from n_s on are ignored.  A row that sees no key gets O = 0
  *                 and LSE = -inf.
- *   max_seqlen_q  upper bound of the per-sequence node counts
+ *   max_seqlen_q  upper bound of the per-sequence node counts.  With 0 the call does
+ *                 nothing: it looks at no sequence, and o and lse stay as they are
+ *                 (the binding's helpers, whose outputs are new, look at them all).
  *   workspace     device scratch of at least fa_paged_tree_workspace_size() bytes,
  *                 256-byte aligned; it needs no initialisation, and calls on one
  *                 workspace must not overlap on the GPU

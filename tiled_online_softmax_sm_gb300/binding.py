@@ -925,7 +925,8 @@ def _tree_workspace(*sizes):
 def paged_tree_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, max_seqlen_q, mask,
                          scale, workspace=None, stream=None):
     """Drafted nodes q [T,H,d] packed by cu_seqlens_q over the bf16 cache, mask [T,words] int32 of the
-    nodes that each node sees beside the context -> (o [T,H,d] bf16, lse [H,T] fp32)."""
+    nodes that each node sees beside the context -> (o [T,H,d] bf16, lse [H,T] fp32).  A max_seqlen_q of 0
+    counts as 1, with a workspace of the call's own."""
     if stream is not None:
         with _given(stream):
             return paged_tree_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q,
@@ -939,6 +940,8 @@ def paged_tree_attention(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_
     if not (q.dtype is _BF16 and mask.dtype is _I32 and width == d and mask.shape == (T, words)
             and mask.get_device() == device and q.is_contiguous() and mask.is_contiguous()):
         _refuse(fn, device, ("q", q, (_BF16,), (T, H, d)), ("mask", mask, (_I32,), (T, words)))
+    if max_seqlen_q == 0:   # (the entry would look at no sequence, and say nothing of one with nodes)
+        max_seqlen_q, workspace = 1, None
     if workspace is None:   # (a caller's own is sized for the caller's bound)
         max_seqlen_q = min(max_seqlen_q, T)
         size = _tree_workspace(S, max_seqlen_q, H, Hkv, d)
@@ -977,6 +980,8 @@ def paged_tree_attention_e4m3(q, k_cache, v_cache, k_scale, v_scale, block_table
     _check_rows(fn, device, "q", q, torch.bfloat16, (T, H, d))
     _check_rows(fn, device, "mask", mask, torch.int32, (T, words))
     _check_rows(fn, device, "cu_seqlens_q", cu_seqlens_q, torch.int32, (S + 1,))
+    if max_seqlen_q == 0:   # (the entry would look at no sequence, and say nothing of one with nodes)
+        max_seqlen_q, workspace = 1, None
     if workspace is None:   # (a caller's own is sized for the caller's bound)
         max_seqlen_q = min(max_seqlen_q, T)
         size = _tree_workspace(S, max_seqlen_q, H, Hkv, d)
