@@ -673,12 +673,13 @@ fa_status fa_paged_tree_attention_e4m3(const void* q, const void* k_cache, const
  *                 in increasing order, path_lens[s] of them (0 <= path_lens[s] <=
  *                 max_path); the entries behind them may be anything
  *   new_seq_lens  int32 [num_seqs] written: seq_lens[s] - n_s + path_lens[s] (an
- *                 array of its own, not seq_lens itself)
+ *                 array of its own, not seq_lens itself).  With num_layers 0 the call
+ *                 does nothing and leaves it as it is (the binding's helper refuses that)
  * The rows of node path[s][a] are copied to the slot of node a, for every a in
  * turn; the slots behind keep their contents.  A sequence whose path is longer
  * than max_path or n_s, leaves [0, n_s) or does not increase is skipped, its new
- * length is seq_lens[s], and FA_ERR_INVALID_ARG is set.  A node with a page id
- * out of range, its own or its destination's, is skipped and sets
+ * length is seq_lens[s], and FA_ERR_INVALID_ARG is set.  A node that moves and whose
+ * page id is out of range, its own or its destination's, is skipped and sets
  * FA_ERR_BAD_BLOCK_TABLE.  The pages that hold a sequence's nodes must be its
  * own: two sequences that move rows within one page leave an unspecified mix.
  * Supported: d in {64, 128}, page_size == 16, max_path <= 1024, Hkv <= 65536,

@@ -1037,6 +1037,8 @@ def paged_kv_accept(k_cache, v_cache, block_table, seq_lens, cu_seqlens, path, p
     fn = "paged_kv_accept"
     device = k_cache.get_device()
     layers, P, Hkv, page, d = _check_layers(fn, device, k_cache, v_cache, k_scale, v_scale)
+    if layers == 0:   # (the entry would do nothing, and the new lengths hold anything)
+        raise FaError(FA_ERR_INVALID_ARG, f"{fn}: caches without layers")
     S, max_blocks = block_table.shape
     max_path, i32 = path.shape[-1], _I32
     if not (block_table.dtype is i32 and seq_lens.dtype is i32 and cu_seqlens.dtype is i32
