@@ -763,9 +763,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const uint64_t sc2 = ptx::f2_bits(a.scale_log2, a.scale_log2);
     int ns = 0, nod[2] = {0, 0}, nstat = 0;
     bool ok = true;
-    if (threadIdx.x == 128) {   // for the merge: no unit cut behind this piece, until one is met
-      a.cuts[cta] = Cut{0, 0, 0, 0, 0, 0, 0, 0};
-    }
+    // for the merge: no unit cut behind this piece, until one is met
+    if (threadIdx.x == 128 && FA_IN_BOUNDS(cta, kCtas, status)) a.cuts[cta] = Cut{0, 0, 0, 0, 0, 0, 0, 0};
     while (ok && next_segment<PAIRS>(a, list, x, s, S)) {
       const int nt = S.j1 - S.j0;
       const int tile_rows = a.tile_nodes * a.G;
@@ -775,7 +774,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const int row = (S.pair && w == 1 ? tile_rows : 0) + r;                // of the unit
       // a warp without a valid row leaves P as it is: it reaches only its own rows
       const bool any = quarter * 32 < rows;
-      if (threadIdx.x == 128 && S.j0 == 0 && S.j1 < S.nt)
+      if (threadIdx.x == 128 && S.j0 == 0 && S.j1 < S.nt && FA_IN_BOUNDS(cta, kCtas, status))
         a.cuts[cta] = Cut{S.Q.q0 + S.node0, S.nodes * a.G, S.g * a.G, S.nt, S.first, S.cost, total, W};
       float m_ref = -INFINITY, l_run = 0.f, l_p = 0.f;
       const int step = S.pair ? 1 : 2, jw = S.pair ? 0 : w;

@@ -103,7 +103,7 @@ kv_accept_kernel(const KvAcceptParams p) {
   good = !__syncthreads_or(!good);
   if (first_block) {
     if (!good) atomicExch(p.c.status, kDevInvalidArg);
-    p.new_seq_lens[s] = good ? L - n + k : L;
+    if (FA_IN_BOUNDS(s, p.num_seqs, p.c.status)) p.new_seq_lens[s] = good ? L - n + k : L;
   }
   if (!good) return;
   // the entries that move, in order (those in place already are skipped)
