@@ -167,7 +167,8 @@ def _bind_torch():
     global _current_raw_stream, _current_device, _CODES, _SCALES, _I32, _BF16, _F32, _U8, _new
     _I32, _BF16, _F32, _U8 = torch.int32, torch.bfloat16, torch.float32, torch.uint8
     guards = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
-    _new = getattr(guards, "_empty_strided_cuda", None) or _new_strided
+    short = getattr(guards, "_empty_strided_cuda", None)
+    _new = short if short is not None and _fits(short, "cuda") else _new_strided
     _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -178,6 +179,15 @@ def _bind_torch():
 
 def _new_strided(size, strides, dtype):
     return torch.empty_strided(size, strides, dtype=dtype, device="cuda")
+
+
+def _fits(new, device):
+    """Whether new(size, strides, type) gives what the helpers expect: it is no public function of torch's."""
+    try:
+        t = new((2, 3), (1, 2), torch.int32)
+        return t.shape == (2, 3) and t.stride() == (1, 2) and t.dtype is torch.int32 and t.device.type == device
+    except Exception:
+        return False
 
 
 def _check(rc: int):
