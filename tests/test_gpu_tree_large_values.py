@@ -44,11 +44,11 @@ def _caches(rng, d, hotter, size, e4m3):
 
 
 # 20 log2 units more: weights against the first tiles' reference would reach 2^20, and with V around
-# 2^110 leave fp32's range, although no output does.  7: the reference stays where it is.
+# 2^110 leave fp32's range, although no output does.  7, 14: the reference stays where it is.
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("n", [5, 40])        # one and two query tiles of 4 heads a kv head
-@pytest.mark.parametrize("hotter,power", [(20, 110), (7, 100), (30, 110)])
+@pytest.mark.parametrize("hotter,power", [(20, 110), (7, 100), (14, 100), (30, 110)])
 def test_hot_tiles_behind_cold_ones(hotter, power, n, d, e4m3):
     rng = np.random.default_rng(60)
     H, scale = 4 * HKV, float(np.float32(d ** -0.5))
