@@ -29,8 +29,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kSteps = 4;     // rows that a lane works on
-// Blocks an SM: at 5 nothing is spilled.  us for 21 300 tokens (see above): 4 96, 5 88,
-// 6 99; 2 steps at 8 blocks 115, 3 steps at 6 97.
+// Blocks an SM: at 5 nothing is spilled.  us for 21 300 tokens (see above): 5 87, and when
+// that took 89 (the norms formed one row after the other) 4 96, 6 99; 2 steps at 8 blocks 115,
+// 3 steps at 6 97.
 constexpr int kBlocks = 5;
 
 __device__ __forceinline__ uint2 ld_row(const void* p) {
@@ -62,12 +63,15 @@ __device__ __forceinline__ bool out_of_range(float r) {
   return __float_as_uint(r) - 0x26800000u > 0x58800000u - 0x26800000u;   // (a NaN, too)
 }
 
-// The sum of a row's squares, in all of its lanes.
-template <int LANES>
-__device__ __forceinline__ float sum_squares(const uint64_t (&x)[4]) {
+// The sum of the squares of a lane's values, and of its row's (in all of the row's lanes).
+__device__ __forceinline__ float lane_squares(const uint64_t (&x)[4]) {
   float lo, hi;
   ptx::f2_split(ptx::ffma2(x[0], x[0], ptx::ffma2(x[1], x[1], ptx::ffma2(x[2], x[2], ptx::fmul2(x[3], x[3])))), lo, hi);
-  float sum = lo + hi;
+  return lo + hi;
+}
+template <int LANES>
+__device__ __forceinline__ float row_squares(const uint64_t (&x)[4]) {
+  float sum = lane_squares(x);
 #pragma unroll
   for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum;
@@ -125,7 +129,7 @@ qkv_rows_kernel(const QkvRowsParams p, int parts) {
     const __nv_bfloat16* src = source(g);
 #pragma unroll
     for (int e = 0; e < kSteps; ++e) {
-      na[e] = nb[e] = make_uint2(0u, 0u);
+      na[e] = nb[e] = make_uint2(0x3f803f80u, 0x3f803f80u);   // (ones: rows past the last head are in range)
       if (h0 + e * kRows < heads) {
         na[e] = ld_row(src + e * kRows * D + off_a);
         nb[e] = ld_row(src + e * kRows * D + off_b);
@@ -246,18 +250,26 @@ qkv_rows_kernel(const QkvRowsParams p, int parts) {
         *reinterpret_cast<uint2*>(dst + row * D + off_b) = make_uint2(y[2], y[3]);
       }
     };
-    // (all rows' norms before the first is used: one branch for the group, 90.2 us with one
-    // for each row, and the sums' shuffles go side by side)
+    // (all rows' norms before the first is used: the sums' shuffles go side by side, and the
+    // check of their range is one branch a group; 87.4 us, with a branch for each row 90.2)
     float r[kSteps];
 #pragma unroll
     for (int e = 0; e < kSteps; ++e) r[e] = 1.f;
     if (norm && (!PAGED || kind < 2)) {
-      bool out = false;
 #pragma unroll
       for (int e = 0; e < kSteps; ++e) {
         const uint64_t x[4] = {widen(a[e].x), widen(a[e].y), widen(b[e].x), widen(b[e].y)};
-        r[e] = rsqrtf(sum_squares<kLanes>(x) * (1.f / D) + p.eps);
-        out = out || (h0 + e * kRows < heads && out_of_range(r[e]));
+        r[e] = lane_squares(x);
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int e = 0; e < kSteps; ++e) r[e] += __shfl_xor_sync(0xffffffffu, r[e], o);
+      bool out = false;
+#pragma unroll
+      for (int e = 0; e < kSteps; ++e) {
+        r[e] = rsqrtf(r[e] * (1.f / D) + p.eps);
+        out = out || out_of_range(r[e]);
       }
       if (__any_sync(0xffffffffu, out)) {   // rows read again, one at a time: registers are short
         const __nv_bfloat16* src = source(g);
@@ -273,11 +285,11 @@ qkv_rows_kernel(const QkvRowsParams p, int parts) {
           }
           uint64_t x[4] = {widen(y[0]), widen(y[1]), widen(y[2]), widen(y[3])};
           const float scale = unit_scale<kLanes>(x);
-          const bool scaled = out_of_range(rsqrtf(sum_squares<kLanes>(x) * (1.f / D) + p.eps));
+          const bool scaled = out_of_range(rsqrtf(row_squares<kLanes>(x) * (1.f / D) + p.eps));
           const float f = scaled ? scale : 1.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) x[k] = ptx::fmul2(x[k], ptx::f2_bits(f, f));
-          finish(h0 + e * kRows, y, x, rsqrtf(sum_squares<kLanes>(x) * (1.f / D) + p.eps * f * f));
+          finish(h0 + e * kRows, y, x, rsqrtf(row_squares<kLanes>(x) * (1.f / D) + p.eps * f * f));
         }
         continue;
       }
