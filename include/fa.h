@@ -537,6 +537,8 @@ fa_status fa_paged_prefill_e4m3(const void* q, const void* k_cache, const void* 
  *              depth 0 for a child of the context
  * A sequence of more than 32*mask_words nodes is skipped and sets
  * FA_ERR_INVALID_ARG.
+ * Time grows with the depth of the deepest tree times mask_words (a chain of 256 nodes
+ * 20 us, of 1024 938; trees of 1024 nodes with random parents 30).
  * Supported: 1 <= mask_words <= 32; total*mask_words below 2^31.
  */
 fa_status fa_tree_layout(const int* parents, const int* seq_lens, const int* cu_seqlens, int* mask,
@@ -620,6 +622,9 @@ size_t fa_paged_tree_workspace_size(int num_seqs, int max_seqlen_q, int H, int H
  *   max_seqlen_q  upper bound of the per-sequence node counts.  With 0 the call does
  *                 nothing: it looks at no sequence, and o and lse stay as they are
  *                 (the binding's helpers, whose outputs are new, look at them all).
+ *                 A bound beyond floor(128 / (H/Hkv)) selects the form for units of
+ *                 two query tiles, which takes longer where every tree is smaller
+ *                 (16 nodes of 64 sequences, H/Hkv = 4: bounds to 32 200 us, above 208)
  *   workspace     device scratch of at least fa_paged_tree_workspace_size() bytes,
  *                 256-byte aligned; it needs no initialisation, and calls on one
  *                 workspace must not overlap on the GPU

@@ -30,8 +30,8 @@
 // exponentials run beside the other's MMAs, and the two states merge at the end
 // of the segment inside the CTA.
 //
-// Softmax as in the forward: p = 2^(s scale log2 e - ref), the reference raised
-// only when a tile's maximum passes it by far; two sums are kept, of p for the LSE
+// Softmax as in the forward: p = 2^(s scale log2 e - ref), the reference set somewhat
+// above the maximum and again only when a tile's maximum passes it by far; two sums are kept, of p for the LSE
 // and of the bf16-rounded p that the P V MMA multiplies for O (which forms that sum itself
 // at d = 64).
 //
@@ -159,7 +159,8 @@ __device__ __forceinline__ Seq load_seq(const Args& a, int s) {
 
 // Units of a sequence along its nodes, K/V tiles of each, and the cost of one: with
 // two query tiles it takes about a third longer (16 x [20, 64] nodes at d = 64, where both
-// occur: 2 : 3 59 us, 3 : 4 57, 4 : 5 58; 2 : 4 cost 12 us more than 2 : 3).
+// occur: 2 : 3 59 us, 3 : 4 57, 4 : 5 58; 2 : 4 cost 12 us more than 2 : 3).  Measured on the
+// bf16 cache; the e4m3 one, whose widening takes the same for both, has the same weights.
 // (a division by 2 * tile_nodes <= 256 as a product with its reciprocal in 2^-40, which is
 // exact below 2^32: the divisions of five roles' segments were a good part of the
 // code, and of a small call's time)

@@ -20,6 +20,7 @@ Workloads (sizes as in the bench and the parity tests):
   tree_c4      attention of 16 drafted nodes of each of the decode pool's 64 sequences
   tree_e4m3    the same over an e4m3 cache
   tree_long    64 drafted nodes of 4 sequences of [16384, 65536] tokens
+  tree_d64     64 drafted nodes of 16 sequences of [512, 8192] tokens, 24 heads of 8, d=64
   qkv_rows     q, k and v rows of 16 x 1024 new tokens: norms, rotation and cache write
   copy_pages   2048 pages of a bf16 cache (64 KB each with K and V) copied
 Inputs come from the same seeded generators; nothing is checked here.
@@ -165,11 +166,12 @@ def make(name: str, splits: int = 8):
     if name == "window_c3":
         q, k, v = (torch.randn((1, 8192, 32, 128), device="cuda").bfloat16() for _ in range(3))
         return lambda: fb.forward_window(q, k, v, I.fp32_scale(128), 1024, 4)
-    if name in ("tree_c4", "tree_long"):
-        S, n, at = (64, 16, (512, 8192)) if name == "tree_c4" else (4, 64, (16384, 65536))
-        cache = bf16_cache(I.uniform_lengths(I.BASE_SEED, S, *at))
-        q, cu, mask, _ = drafted(cache[3], n)
-        return lambda: fb.paged_tree_attention(q, *cache, cu, n, mask, I.fp32_scale(128))
+    if name in ("tree_c4", "tree_long", "tree_d64"):
+        S, n, at, H, d = {"tree_c4": (64, 16, (512, 8192), 32, 128), "tree_long": (4, 64, (16384, 65536), 32, 128),
+                          "tree_d64": (16, 64, (512, 8192), 24, 64)}[name]
+        cache = bf16_cache(I.uniform_lengths(I.BASE_SEED, S, *at), d=d)
+        q, cu, mask, _ = drafted(cache[3], n, H, d)
+        return lambda: fb.paged_tree_attention(q, *cache, cu, n, mask, I.fp32_scale(d))
     if name == "tree_e4m3":
         k, v, cache, cu, _ = e4m3_cache(I.BASE_SEED, 64)
         fb.paged_kv_write_e4m3(k, v, *cache, cu)
