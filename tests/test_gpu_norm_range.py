@@ -26,7 +26,7 @@ def _heads(total, heads, d, seed):
     return (x * size[order]).float().bfloat16()
 
 
-@pytest.mark.parametrize("eps", [0.0, 1e-38, 1e-6, 1.0])
+@pytest.mark.parametrize("eps", [0.0, 1e-38, 1e-6, 1.0, 1e31])
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("d,rot", [(64, 64), (128, 128), (128, 64)])
 def test_heads_of_every_size(d, rot, interleaved, eps):

@@ -284,9 +284,9 @@ qkv_rows_kernel(const QkvRowsParams p, int parts) {
             y[3] = hi.y;
           }
           uint64_t x[4] = {widen(y[0]), widen(y[1]), widen(y[2]), widen(y[3])};
-          const float scale = unit_scale<kLanes>(x);
-          const bool scaled = out_of_range(rsqrtf(row_squares<kLanes>(x) * (1.f / D) + p.eps));
-          const float f = scaled ? scale : 1.f;
+          const float scale = unit_scale<kLanes>(x), mean = row_squares<kLanes>(x) * (1.f / D);
+          // (not for the sake of a large eps, which times the factor's square could leave fp32)
+          const float f = mean > 0x1p100f || mean + p.eps < 0x1p-100f ? scale : 1.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) x[k] = ptx::fmul2(x[k], ptx::f2_bits(f, f));
           finish(h0 + e * kRows, y, x, rsqrtf(row_squares<kLanes>(x) * (1.f / D) + p.eps * f * f));
