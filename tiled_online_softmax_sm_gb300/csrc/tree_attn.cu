@@ -31,9 +31,9 @@
 // of the segment inside the CTA.
 //
 // Softmax as in the forward: p = 2^(s scale log2 e - ref), the reference set somewhat
-// above the maximum and again only when a tile's maximum passes it by far; two sums are kept, of p for the LSE
-// and of the bf16-rounded p that the P V MMA multiplies for O (which forms that sum itself
-// at d = 64).
+// above the maximum and again only when a tile's maximum passes it by far; two sums are
+// kept, of p for the LSE and of the bf16-rounded p that the P V MMA multiplies for O
+// (which forms that sum itself at d = 64).
 //
 // Measured (d = 128, 32 heads of 8, contexts uniform on the range): 64 x 16 nodes over
 // [512, 8192] tokens, one query tile a unit, 175 us for 1.04 GB (6.0 TB/s, 0.89 of a
